@@ -1,0 +1,113 @@
+// la_dit.cuh -- shared host/device declarations of the operators around the
+// linear attention in a Linear DiT block: layer norm, linear, cross attention.
+// Nothing here is part of the public ABI (include/la.h).
+#pragma once
+
+#include <cstddef>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "la_internal.cuh"
+
+namespace la {
+
+// ---------------------------------------------------------------- layer norm
+
+struct NormPlan {
+    long long rows;      // B * N
+    int B, N, C;
+    int per_batch;       // weight and bias are [B][C], one vector a batch element
+    float eps;
+};
+size_t norm_bwd_ws(const NormPlan &p);
+int launch_norm_fwd(int is_bf16, const void *x, const void *w, const void *b, void *y, float *mean, float *rstd,
+                    const NormPlan &p, cudaStream_t s);
+int launch_norm_bwd(int is_bf16, const void *dy, const void *x, const void *w, const float *mean, const float *rstd,
+                    void *dx, void *dw, void *db, void *ws, const NormPlan &p, cudaStream_t s);
+
+// ---------------------------------------------------------------- linear
+
+// One product C[m][n] = sum_k A(m, k) B(n, k), row-major C, with the epilogue
+// z = C + bias[n]; pre = z; y = act(z) + res (each part optional).
+struct GemmPlan {
+    long long M, N, K;
+    int a_mn, b_mn;              // 0: K contiguous, 1: M (or N) contiguous
+    long long lda, ldb;          // elements between rows of the stored matrix
+    const void *a, *b;
+    const void *bias, *res;      // [N], [M][N] or null
+    void *pre, *y;               // [M][N] or null (pre), [M][N]
+    int act;
+};
+int launch_gemm_ffma(int is_bf16, const GemmPlan &g, cudaStream_t s);
+// dz = dy * act'(pre), element by element
+int launch_act_bwd(int is_bf16, const void *dy, const void *pre, void *dz, long long n, int act, cudaStream_t s);
+// out[c] = sum_r x[r][c] in a fixed order; ws holds col_sum_ws bytes
+size_t col_sum_ws(long long R, long long C);
+int launch_col_sum(int is_bf16, const void *x, void *out, long long R, long long C, void *ws, cudaStream_t s);
+
+#ifdef __CUDACC__
+// The activations and their derivatives in fp32.  GELU is the tanh form:
+// z/2 (1 + tanh u) = z sigmoid(2u), u = sqrt(2/pi) (z + 0.044715 z^3).
+__device__ __forceinline__ float sigmoid_f(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+constexpr float kGeluA = 1.5957691216057308f;   // sqrt(8/pi)
+
+__device__ __forceinline__ float act_f(float z, int act) {
+    if (act == 1) return z > 0.f ? z : (z == z ? 0.f : z);
+    if (act == 2) return z * sigmoid_f(z);
+    if (act == 3) return z * sigmoid_f(kGeluA * (z + 0.044715f * z * z * z));
+    return z;
+}
+
+__device__ __forceinline__ float act_slope(float z, int act) {
+    if (act == 1) return z > 0.f ? 1.f : 0.f;
+    if (act == 2) {
+        const float s = sigmoid_f(z);
+        return s * (1.f + z * (1.f - s));
+    }
+    if (act == 3) {
+        const float s = sigmoid_f(kGeluA * (z + 0.044715f * z * z * z));
+        return s * (1.f + z * (1.f - s) * kGeluA * (1.f + 0.134145f * z * z));
+    }
+    return 1.f;
+}
+
+template <typename T> __device__ __forceinline__ float to_f(T x);
+template <> __device__ __forceinline__ float to_f<float>(float x) { return x; }
+template <> __device__ __forceinline__ float to_f<__nv_bfloat16>(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <typename T> __device__ __forceinline__ T from_f(float x);
+template <> __device__ __forceinline__ float from_f<float>(float x) { return x; }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+#endif
+
+// ---------------------------------------------------------------- cross attention
+
+struct CrossPlan {
+    int B, N, M, H, d;
+    long long ldk, ldv;      // elements between consecutive encoder states of k, v
+    long long lddk, lddv;    // the same of dk, dv
+    const int *kv_len;       // device, [B] or null
+    float scale;
+};
+size_t cross_fwd_ws(int is_bf16, const CrossPlan &p);
+size_t cross_bwd_ws(int is_bf16, const CrossPlan &p);
+int launch_cross_fwd(int is_bf16, const void *q, const void *k, const void *v, void *out, float *lse,
+                     const CrossPlan &p, void *ws, cudaStream_t s);
+int launch_cross_bwd(int is_bf16, const void *q, const void *k, const void *v, const void *out, const void *dout,
+                     const float *lse, void *dq, void *dk, void *dv, const CrossPlan &p, void *ws, cudaStream_t s);
+
+#ifdef __CUDACC__
+// The valid encoder states of batch element b: kv_len[b] held to [0, M].
+__device__ __forceinline__ int cross_len(const CrossPlan &p, int b) {
+    if (!p.kv_len) return p.M;
+    const int n = p.kv_len[b];
+    return n < 0 ? 0 : (n < p.M ? n : p.M);
+}
+#endif
+
+}  // namespace la

@@ -1,0 +1,217 @@
+// la_dit_api.cu -- the C entry points of layer norm, linear and cross
+// attention (declared in include/la.h): argument checks, workspace layout and
+// the sequence of kernel launches.
+#include <cmath>
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "../../include/la.h"
+#include "la_dit.cuh"
+
+namespace {
+
+bool al16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool al256(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 255u) == 0; }
+bool dtype_ok(la_dtype dt) { return dt == LA_F32 || dt == LA_BF16; }
+la_status done(int launched) { return launched < 0 ? LA_ECUDA : LA_OK; }
+
+// Sizes that keep every element offset of a tensor below 2^40.
+bool count_ok(long long a, long long b, long long c) {
+    return a > 0 && b > 0 && c > 0 && (double)a * (double)b * (double)c < (double)(1LL << 40);
+}
+
+la_status norm_plan(la::NormPlan &p, int B, int N, int C, int per_batch, float eps) {
+    if (!count_ok(B, N, C)) return LA_EINVAL;
+    if (!(eps >= 0.0f) || !std::isfinite(eps)) return LA_EINVAL;
+    if (per_batch && B > 65535) return LA_EUNSUPPORTED;
+    p.B = B; p.N = N; p.C = C;
+    p.rows = (long long)B * N;
+    p.per_batch = per_batch ? 1 : 0;
+    p.eps = eps;
+    return LA_OK;
+}
+
+la_status cross_plan(la::CrossPlan &p, la_dtype dt, int B, int N, int M, int H, int d, long long ldk, long long ldv,
+                     const int *kv_len, float scale) {
+    if (!dtype_ok(dt)) return LA_EINVAL;
+    if (H <= 0 || d <= 0 || !count_ok(B, N, (long long)H * d) || M <= 0) return LA_EINVAL;
+    if (d != 32 && d != 64) return LA_EUNSUPPORTED;
+    if ((long long)B * H > 65535) return LA_EUNSUPPORTED;
+    const long long e = dt == LA_BF16 ? 2 : 4;
+    if (ldk < (long long)H * d || ldv < (long long)H * d || (ldk * e) % 16 || (ldv * e) % 16) return LA_EINVAL;
+    if (!count_ok(B, M, ldk) || !count_ok(B, M, ldv)) return LA_EINVAL;
+    if (!(scale > 0.0f) || !std::isfinite(scale)) return LA_EINVAL;
+    if (reinterpret_cast<uintptr_t>(kv_len) & 3u) return LA_EINVAL;
+    p.B = B; p.N = N; p.M = M; p.H = H; p.d = d;
+    p.ldk = ldk; p.ldv = ldv;
+    p.lddk = ldk; p.lddv = ldv;
+    p.kv_len = kv_len;
+    p.scale = scale;
+    return LA_OK;
+}
+
+bool ws_ok(const void *ws, size_t have, size_t need) { return ws && have >= need && al256(ws); }
+
+// Backward of linear: the workspace holds dz (with an activation), then the
+// column sums' pieces.
+struct LinBwdWs {
+    size_t dz, cols, total;
+};
+LinBwdWs lin_bwd_ws(int R, int K, int N, la_dtype dt, la_act act) {
+    (void)K;
+    LinBwdWs w;
+    w.dz = 0;
+    w.cols = act == LA_ACT_NONE ? 0 : la::align256(size_t(R) * N * (dt == LA_BF16 ? 2 : 4));
+    w.total = w.cols + la::col_sum_ws(R, N);
+    return w;
+}
+
+bool act_ok(la_act a) { return a == LA_ACT_NONE || a == LA_ACT_RELU || a == LA_ACT_SILU || a == LA_ACT_GELU; }
+
+}  // namespace
+
+extern "C" {
+
+la_status la_layer_norm_forward(const void *x, const void *weight, const void *bias, void *y, float *mean,
+                                float *rstd, la_dtype dt, int B, int N, int C, int per_batch, float eps,
+                                void *stream) {
+    if (!x || !y || !al16(x) || !al16(y) || !al16(weight) || !al16(bias) || !al16(mean) || !al16(rstd)) return LA_EINVAL;
+    if (!dtype_ok(dt)) return LA_EINVAL;
+    la::NormPlan p{};
+    const la_status e = norm_plan(p, B, N, C, per_batch, eps);
+    if (e != LA_OK) return e;
+    return done(la::launch_norm_fwd(dt == LA_BF16, x, weight, bias, y, mean, rstd, p,
+                                    static_cast<cudaStream_t>(stream)));
+}
+
+size_t la_layer_norm_backward_workspace_size(int B, int N, int C, int per_batch) {
+    la::NormPlan p{};
+    return norm_plan(p, B, N, C, per_batch, 0.0f) == LA_OK ? la::norm_bwd_ws(p) : 0;
+}
+
+la_status la_layer_norm_backward(const void *dy, const void *x, const void *weight, const float *mean,
+                                 const float *rstd, void *dx, void *dweight, void *dbias, la_dtype dt, int B, int N,
+                                 int C, int per_batch, void *ws, size_t ws_bytes, void *stream) {
+    if (!dy || !x || !mean || !rstd || !dx) return LA_EINVAL;
+    if (!al16(dy) || !al16(x) || !al16(weight) || !al16(mean) || !al16(rstd) || !al16(dx) || !al16(dweight) ||
+        !al16(dbias))
+        return LA_EINVAL;
+    if (!dtype_ok(dt)) return LA_EINVAL;
+    la::NormPlan p{};
+    const la_status e = norm_plan(p, B, N, C, per_batch, 0.0f);
+    if (e != LA_OK) return e;
+    if ((dweight || dbias) && !ws_ok(ws, ws_bytes, la::norm_bwd_ws(p))) return LA_EWORKSPACE;
+    return done(la::launch_norm_bwd(dt == LA_BF16, dy, x, weight, mean, rstd, dx, dweight, dbias, ws, p,
+                                    static_cast<cudaStream_t>(stream)));
+}
+
+size_t la_linear_workspace_size(int R, int K, int N, la_dtype dt) {
+    if (!dtype_ok(dt) || !count_ok(R, K, 1) || !count_ok(N, K, 1) || !count_ok(R, N, 1)) return 0;
+    return 256;
+}
+
+la_status la_linear_forward(const void *x, const void *weight, const void *bias, const void *residual, void *y,
+                            void *pre, la_dtype dt, la_act act, int R, int K, int N, void *ws, size_t ws_bytes,
+                            void *stream) {
+    if (!x || !weight || !y) return LA_EINVAL;
+    if (!al16(x) || !al16(weight) || !al16(bias) || !al16(residual) || !al16(y) || !al16(pre)) return LA_EINVAL;
+    if (!dtype_ok(dt) || !act_ok(act)) return LA_EINVAL;
+    const size_t need = la_linear_workspace_size(R, K, N, dt);
+    if (!need) return LA_EINVAL;
+    if (!ws_ok(ws, ws_bytes, need)) return LA_EWORKSPACE;
+    la::GemmPlan g{};
+    g.M = R; g.N = N; g.K = K;
+    g.a = x; g.lda = K;
+    g.b = weight; g.ldb = K;
+    g.bias = bias; g.res = residual; g.pre = pre; g.y = y;
+    g.act = act;
+    return done(la::launch_gemm_ffma(dt == LA_BF16, g, static_cast<cudaStream_t>(stream)));
+}
+
+size_t la_linear_backward_workspace_size(int R, int K, int N, la_dtype dt, la_act act) {
+    if (!la_linear_workspace_size(R, K, N, dt) || !act_ok(act)) return 0;
+    return lin_bwd_ws(R, K, N, dt, act).total;
+}
+
+la_status la_linear_backward(const void *dy, const void *x, const void *weight, const void *pre, void *dx,
+                             void *dweight, void *dbias, la_dtype dt, la_act act, int R, int K, int N, void *ws,
+                             size_t ws_bytes, void *stream) {
+    if (!dy || (dx && !weight) || (dweight && !x)) return LA_EINVAL;
+    if (!al16(dy) || !al16(x) || !al16(weight) || !al16(pre) || !al16(dx) || !al16(dweight) || !al16(dbias))
+        return LA_EINVAL;
+    if (!dtype_ok(dt) || !act_ok(act) || (act != LA_ACT_NONE && !pre)) return LA_EINVAL;
+    const size_t need = la_linear_backward_workspace_size(R, K, N, dt, act);
+    if (!need) return LA_EINVAL;
+    if (!ws_ok(ws, ws_bytes, need)) return LA_EWORKSPACE;
+    const LinBwdWs w = lin_bwd_ws(R, K, N, dt, act);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const int bf = dt == LA_BF16;
+    const void *dz = dy;
+    if (act != LA_ACT_NONE) {
+        void *buf = static_cast<char *>(ws) + w.dz;
+        if (la::launch_act_bwd(bf, dy, pre, buf, (long long)R * N, act, s) < 0) return LA_ECUDA;
+        dz = buf;
+    }
+    if (dbias && la::launch_col_sum(bf, dz, dbias, R, N, static_cast<char *>(ws) + w.cols, s) < 0) return LA_ECUDA;
+    if (dx) {
+        la::GemmPlan g{};
+        g.M = R; g.N = K; g.K = N;
+        g.a = dz; g.lda = N;
+        g.b = weight; g.ldb = K; g.b_mn = 1;
+        g.y = dx;
+        if (la::launch_gemm_ffma(bf, g, s) < 0) return LA_ECUDA;
+    }
+    if (dweight) {
+        la::GemmPlan g{};
+        g.M = N; g.N = K; g.K = R;
+        g.a = dz; g.lda = N; g.a_mn = 1;
+        g.b = x; g.ldb = K; g.b_mn = 1;
+        g.y = dweight;
+        if (la::launch_gemm_ffma(bf, g, s) < 0) return LA_ECUDA;
+    }
+    return LA_OK;
+}
+
+size_t la_cross_attention_workspace_size(la_dtype dt, int B, int N, int M, int H, int d) {
+    la::CrossPlan p{};
+    const long long ld = (long long)H * d;
+    return cross_plan(p, dt, B, N, M, H, d, ld, ld, nullptr, 1.0f) == LA_OK ? la::cross_fwd_ws(dt == LA_BF16, p) : 0;
+}
+
+size_t la_cross_attention_backward_workspace_size(la_dtype dt, int B, int N, int M, int H, int d) {
+    la::CrossPlan p{};
+    const long long ld = (long long)H * d;
+    return cross_plan(p, dt, B, N, M, H, d, ld, ld, nullptr, 1.0f) == LA_OK ? la::cross_bwd_ws(dt == LA_BF16, p) : 0;
+}
+
+la_status la_cross_attention_forward(const void *q, const void *k, const void *v, const int *kv_len, void *out,
+                                     float *lse, la_dtype dt, int B, int N, int M, int H, int d, long long ldk,
+                                     long long ldv, float scale, void *ws, size_t ws_bytes, void *stream) {
+    if (!q || !k || !v || !out || !al16(q) || !al16(k) || !al16(v) || !al16(out) || !al16(lse)) return LA_EINVAL;
+    la::CrossPlan p{};
+    const la_status e = cross_plan(p, dt, B, N, M, H, d, ldk, ldv, kv_len, scale);
+    if (e != LA_OK) return e;
+    if (!ws_ok(ws, ws_bytes, la::cross_fwd_ws(dt == LA_BF16, p))) return LA_EWORKSPACE;
+    return done(la::launch_cross_fwd(dt == LA_BF16, q, k, v, out, lse, p, ws, static_cast<cudaStream_t>(stream)));
+}
+
+la_status la_cross_attention_backward(const void *q, const void *k, const void *v, const int *kv_len,
+                                      const void *out, const float *lse, const void *dout, void *dq, void *dk,
+                                      void *dv, la_dtype dt, int B, int N, int M, int H, int d, long long ldk,
+                                      long long ldv, long long lddk, long long lddv, float scale, void *ws,
+                                      size_t ws_bytes, void *stream) {
+    for (const void *t : {q, k, v, out, static_cast<const void *>(lse), dout, static_cast<const void *>(dq),
+                          static_cast<const void *>(dk), static_cast<const void *>(dv)})
+        if (!t || !al16(t)) return LA_EINVAL;
+    la::CrossPlan p{}, g{};
+    la_status e = cross_plan(p, dt, B, N, M, H, d, ldk, ldv, kv_len, scale);
+    if (e == LA_OK) e = cross_plan(g, dt, B, N, M, H, d, lddk, lddv, kv_len, scale);
+    if (e != LA_OK) return e;
+    p.lddk = lddk;
+    p.lddv = lddv;
+    if (!ws_ok(ws, ws_bytes, la::cross_bwd_ws(dt == LA_BF16, p))) return LA_EWORKSPACE;
+    return done(la::launch_cross_bwd(dt == LA_BF16, q, k, v, out, dout, lse, dq, dk, dv, p, ws,
+                                     static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

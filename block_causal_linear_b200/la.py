@@ -97,6 +97,28 @@ def lib() -> ctypes.CDLL:
         L.la_block_apply.argtypes = [vp, vp, ip, ip, ip, ip, ip, vp, ip, ctypes.POINTER(la_state), ip,
                                      ctypes.POINTER(la_rope), fp, vp, sz, vp]
         L.la_block_apply.restype = ip
+        ll = ctypes.c_longlong
+        L.la_layer_norm_forward.argtypes = [vp] * 6 + [ip] * 5 + [fp, vp]
+        L.la_layer_norm_forward.restype = ip
+        L.la_layer_norm_backward_workspace_size.argtypes = [ip] * 4
+        L.la_layer_norm_backward_workspace_size.restype = sz
+        L.la_layer_norm_backward.argtypes = [vp] * 8 + [ip] * 5 + [vp, sz, vp]
+        L.la_layer_norm_backward.restype = ip
+        L.la_linear_workspace_size.argtypes = [ip] * 4
+        L.la_linear_workspace_size.restype = sz
+        L.la_linear_forward.argtypes = [vp] * 6 + [ip] * 5 + [vp, sz, vp]
+        L.la_linear_forward.restype = ip
+        L.la_linear_backward_workspace_size.argtypes = [ip] * 5
+        L.la_linear_backward_workspace_size.restype = sz
+        L.la_linear_backward.argtypes = [vp] * 7 + [ip] * 5 + [vp, sz, vp]
+        L.la_linear_backward.restype = ip
+        for n in ("la_cross_attention_workspace_size", "la_cross_attention_backward_workspace_size"):
+            getattr(L, n).argtypes = [ip] * 6
+            getattr(L, n).restype = sz
+        L.la_cross_attention_forward.argtypes = [vp] * 6 + [ip] * 6 + [ll, ll, fp, vp, sz, vp]
+        L.la_cross_attention_forward.restype = ip
+        L.la_cross_attention_backward.argtypes = [vp] * 10 + [ip] * 6 + [ll] * 4 + [fp, vp, sz, vp]
+        L.la_cross_attention_backward.restype = ip
         L.la_backward_workspace_size.argtypes = [ip, ip, ip, ip, ip]
         L.la_backward_workspace_size.restype = sz
         L.la_full_backward.argtypes = [vp, vp, vp, vp, vp, vp, vp, ip, ip, ip, ip, ip, ip,
@@ -534,6 +556,293 @@ def full_backward(q, k, v, dout, tokens_per_block=0, rope: Optional[la_rope] = N
                           ws.data_ptr(), ws.numel() * ws.element_size(), _stream_ptr(stream))
     if rc != LA_OK:
         raise LAError(rc, "la_full_backward")
+    return dq, dk, dv
+
+
+# ---------------------------------------------------------------- layer norm, linear, cross attention
+
+LA_ACT = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
+
+
+def _launch(name, device, stream, call):
+    """call(lib, stream pointer) with `device` current; raises LAError on a non-zero status."""
+    if stream is None and device.index == torch.cuda.current_device():
+        rc = call(lib(), torch.cuda.current_stream().cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            rc = call(lib(), (stream if stream is not None else torch.cuda.current_stream()).cuda_stream)
+    if rc != LA_OK:
+        raise LAError(rc, name)
+
+
+def _empty(shape, dtype, device, stream):
+    """torch.empty whose memory belongs to the stream that will use it (a
+    buffer freed by the caller is then not handed out while that stream's
+    kernels still use it)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _check_like(name, t, shape, dtype, device):
+    """t is None, or a contiguous CUDA tensor of this shape, dtype and device."""
+    if t is None:
+        return
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor on {device}")
+
+
+def _check_main(name, t, dims):
+    if not t.is_cuda or not t.is_contiguous() or t.dim() not in dims:
+        raise ValueError(f"{name} must be a contiguous CUDA tensor of {' or '.join(map(str, dims))} dimensions")
+    if t.numel() == 0:
+        raise ValueError(f"{name} is empty")
+    return _dtype_code(t)
+
+
+def _check_stream(device, stream):
+    if stream is not None and stream.device != device:
+        raise ValueError(f"the stream belongs to {stream.device}, the tensors to {device}")
+
+
+def _workspace(n, name, ws, device, stream):
+    if n == 0:
+        raise LAError(LA_EINVAL, name)
+    if ws is None:
+        return _empty(n, torch.uint8, device, stream)
+    if ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous tensor on {device}")
+    return ws
+
+
+def _norm_sizes(x, weight, bias):
+    """(B, N, C, per_batch) of x [..., C]; a [B, C] weight or bias has one vector per x[b]."""
+    C = x.shape[-1]
+    vecs = [t for t in (weight, bias) if t is not None]
+    per_batch = bool(vecs) and vecs[0].dim() == 2
+    B = x.shape[0] if per_batch or x.dim() == 3 else 1
+    N = x.numel() // (B * C)
+    for name, t in (("weight", weight), ("bias", bias)):
+        _check_like(name, t, (B, C) if per_batch else (C,), x.dtype, x.device)
+    return B, N, C, int(per_batch)
+
+
+def layer_norm_forward(x, weight=None, bias=None, eps=1e-6, return_stats=False, out=None, stats=None, stream=None):
+    """Layer norm of x [B, N, C] (or [N, C]) over its channels; weight, bias [C],
+    or [B, C] for one scale and shift per batch element.  Returns y, or with
+    return_stats (y, mean, rstd), fp32 [B, N], for layer_norm_backward; stats
+    may give the two buffers."""
+    dt = _check_main("x", x, (2, 3))
+    B, N, C, pb = _norm_sizes(x, weight, bias)
+    _check_stream(x.device, stream)
+    _check_like("out", out, x.shape, x.dtype, x.device)
+    y = _empty(x.shape, x.dtype, x.device, stream) if out is None else out
+    mean = rstd = None
+    if stats is not None:
+        mean, rstd = stats
+    elif return_stats:
+        mean, rstd = (_empty(x.shape[:-1], torch.float32, x.device, stream) for _ in range(2))
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        _check_like(name, t, x.shape[:-1], torch.float32, x.device)
+    _launch("la_layer_norm_forward", x.device, stream, lambda L, s: L.la_layer_norm_forward(
+        x.data_ptr(), _ptr(weight), _ptr(bias), y.data_ptr(), _ptr(mean), _ptr(rstd), dt, B, N, C, pb, float(eps), s))
+    return (y, mean, rstd) if return_stats else y
+
+
+def layer_norm_backward(dy, x, weight, mean, rstd, per_batch=None, weight_grad=True, bias_grad=True, ws=None,
+                        grads=None, stream=None):
+    """(dx, dweight, dbias) of sum(layer_norm_forward(x, weight, bias) * dy), from
+    the forward pass's mean and rstd.  per_batch says whether the vectors' gradients
+    are [B, C] rather than [C] where there is no weight to tell (default: as weight).
+    grads may give the three buffers (None for one that is not wanted)."""
+    dt = _check_main("x", x, (2, 3))
+    B, N, C, pb = _norm_sizes(x, weight, None)
+    if per_batch is not None and bool(per_batch) != bool(pb):
+        if weight is not None:
+            raise ValueError("per_batch contradicts the weight's shape")
+        pb = 1
+        B, N = x.shape[0], x.numel() // (x.shape[0] * C)
+    _check_stream(x.device, stream)
+    _check_like("dy", dy, x.shape, x.dtype, x.device)
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        if t is None:
+            raise ValueError(f"{name} is missing (layer_norm_forward with return_stats gives it)")
+        _check_like(name, t, x.shape[:-1], torch.float32, x.device)
+    vec = (B, C) if pb else (C,)
+    if grads is None:
+        grads = (_empty(x.shape, x.dtype, x.device, stream),
+                 _empty(vec, x.dtype, x.device, stream) if weight_grad else None,
+                 _empty(vec, x.dtype, x.device, stream) if bias_grad else None)
+    dx, dw, db = grads
+    for name, t, shape in (("dx", dx, x.shape), ("dweight", dw, vec), ("dbias", db, vec)):
+        _check_like(name, t, shape, x.dtype, x.device)
+    if dx is None:
+        raise ValueError("dx is missing")
+    if dw is not None or db is not None:
+        n = lib().la_layer_norm_backward_workspace_size(B, N, C, pb)
+        ws = _workspace(n, "la_layer_norm_backward_workspace_size", ws, x.device, stream)
+    _launch("la_layer_norm_backward", x.device, stream, lambda L, s: L.la_layer_norm_backward(
+        dy.data_ptr(), x.data_ptr(), _ptr(weight), mean.data_ptr(), rstd.data_ptr(), dx.data_ptr(), _ptr(dw), _ptr(db),
+        dt, B, N, C, pb, _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), s))
+    return dx, dw, db
+
+
+def _act_code(act):
+    if act not in LA_ACT:
+        raise ValueError(f"act must be one of {', '.join(LA_ACT)}, not {act!r}")
+    return LA_ACT[act]
+
+
+def _linear_sizes(x, weight):
+    """(R, K, N, dtype) of x [..., K] and weight [N, K]."""
+    dt = _check_main("x", x, (1, 2, 3, 4, 5))
+    if weight.dim() != 2:
+        raise ValueError("weight must be [N, K]")
+    K, N = x.shape[-1], weight.shape[0]
+    if N == 0:
+        raise ValueError("weight is empty")
+    _check_like("weight", weight, (N, K), x.dtype, x.device)
+    return x.numel() // K, K, N, dt
+
+
+def linear_forward(x, weight, bias=None, act="none", residual=None, return_pre=False, ws=None, out=None, pre=None,
+                   stream=None):
+    """act(x weight^T + bias) + residual: x [..., K], weight [N, K], bias [N], residual
+    [..., N]; act "none", "relu", "silu" or "gelu" (tanh form).  Returns y, or with
+    return_pre (y, z), z being what the activation acts on, for linear_backward (None
+    without an activation, where the backward pass needs none).  out may be the
+    residual's tensor."""
+    R, K, N, dt = _linear_sizes(x, weight)
+    code = _act_code(act)
+    shape = (*x.shape[:-1], N)
+    _check_stream(x.device, stream)
+    _check_like("bias", bias, (N,), x.dtype, x.device)
+    for name, t in (("residual", residual), ("out", out), ("pre", pre)):
+        _check_like(name, t, shape, x.dtype, x.device)
+    y = _empty(shape, x.dtype, x.device, stream) if out is None else out
+    if return_pre and pre is None and code:
+        pre = _empty(shape, x.dtype, x.device, stream)
+    ws = _workspace(lib().la_linear_workspace_size(R, K, N, dt), "la_linear_workspace_size", ws, x.device, stream)
+    _launch("la_linear_forward", x.device, stream, lambda L, s: L.la_linear_forward(
+        x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(residual), y.data_ptr(), _ptr(pre), dt, code, R, K, N,
+        ws.data_ptr(), ws.numel() * ws.element_size(), s))
+    return (y, pre) if return_pre else y
+
+
+def linear_backward(dy, x, weight, pre=None, act="none", input_grad=True, weight_grad=True, bias_grad=True, ws=None,
+                    grads=None, stream=None):
+    """(dx, dweight, dbias) of sum(linear_forward(x, weight, bias, act, residual) * dy);
+    the residual's gradient is dy.  pre is linear_forward's second result.  grads may
+    give the three buffers (None for one that is not wanted)."""
+    R, K, N, dt = _linear_sizes(x, weight)
+    code = _act_code(act)
+    shape = (*x.shape[:-1], N)
+    _check_stream(x.device, stream)
+    _check_like("dy", dy, shape, x.dtype, x.device)
+    _check_like("pre", pre, shape, x.dtype, x.device)
+    if code and pre is None:
+        raise ValueError("pre is missing (linear_forward with return_pre gives it)")
+    if grads is None:
+        grads = (_empty(x.shape, x.dtype, x.device, stream) if input_grad else None,
+                 _empty((N, K), x.dtype, x.device, stream) if weight_grad else None,
+                 _empty((N,), x.dtype, x.device, stream) if bias_grad else None)
+    dx, dw, db = grads
+    for name, t, sh in (("dx", dx, x.shape), ("dweight", dw, (N, K)), ("dbias", db, (N,))):
+        _check_like(name, t, sh, x.dtype, x.device)
+    n = lib().la_linear_backward_workspace_size(R, K, N, dt, code)
+    ws = _workspace(n, "la_linear_backward_workspace_size", ws, x.device, stream)
+    _launch("la_linear_backward", x.device, stream, lambda L, s: L.la_linear_backward(
+        dy.data_ptr(), x.data_ptr(), weight.data_ptr(), _ptr(pre), _ptr(dx), _ptr(dw), _ptr(db), dt, code, R, K, N,
+        ws.data_ptr(), ws.numel() * ws.element_size(), s))
+    return dx, dw, db
+
+
+def _check_states(name, t, q, M=None):
+    """Elements between consecutive states of an encoder tensor [B, M, H, d], which
+    may be a view of a wider one (the heads of a state contiguous)."""
+    B, _, H, d = q.shape
+    if t.dim() != 4 or t.shape[0] != B or t.shape[2:] != (H, d) or (M is not None and t.shape[1] != M):
+        raise ValueError(f"{name} must be [B, M, H, d] with q's B, H and d")
+    if t.dtype != q.dtype:
+        raise TypeError(f"{name} must be {q.dtype}, not {t.dtype}")
+    if t.device != q.device:
+        raise ValueError(f"{name} must be on {q.device}")
+    B, M = t.shape[:2]
+    if M == 0:
+        raise ValueError(f"{name} is empty")
+    sb, sm, sh, sd = t.stride()
+    if M == 1:      # one state a batch element: the distance between batch elements
+        sm = sb if B > 1 else H * d
+    if sd != 1 or (H > 1 and sh != d) or (B > 1 and sb != M * sm) or sm < H * d:
+        raise ValueError(f"{name}: the heads of a state must be contiguous and the batch elements M states apart")
+    return sm
+
+
+def _cross_sizes(q, k, v, kv_len, scale):
+    dt = _check_main("q", q, (4,))
+    ldk = _check_states("k", k, q)
+    ldv = _check_states("v", v, q, k.shape[1])
+    _check_like("kv_len", kv_len, (q.shape[0],), torch.int32, q.device)
+    B, N, H, d = q.shape
+    return dt, B, N, k.shape[1], H, d, ldk, ldv, float(d ** -0.5 if scale is None else scale)
+
+
+def cross_attention_forward(q, k, v, kv_len=None, scale=None, return_lse=False, ws=None, out=None, lse=None,
+                            stream=None):
+    """Softmax attention of q [B, N, H, d] to an encoder's states k, v [B, M, H, d]
+    (which may be views kv[:, :, 0], kv[:, :, 1] of one projection's output); kv_len
+    int32 [B] gives each batch element's valid states; scale defaults to d^-0.5.
+    Returns out, or with return_lse (out, lse), lse fp32 [B, H, N], for
+    cross_attention_backward."""
+    dt, B, N, M, H, d, ldk, ldv, sc = _cross_sizes(q, k, v, kv_len, scale)
+    _check_stream(q.device, stream)
+    _check_like("out", out, q.shape, q.dtype, q.device)
+    _check_like("lse", lse, (B, H, N), torch.float32, q.device)
+    o = _empty(q.shape, q.dtype, q.device, stream) if out is None else out
+    if return_lse and lse is None:
+        lse = _empty((B, H, N), torch.float32, q.device, stream)
+    n = lib().la_cross_attention_workspace_size(dt, B, N, M, H, d)
+    if n == 0:
+        raise LAError(LA_EUNSUPPORTED if d not in (32, 64) else LA_EINVAL, "la_cross_attention_forward")
+    ws = _workspace(n, "la_cross_attention_workspace_size", ws, q.device, stream)
+    _launch("la_cross_attention_forward", q.device, stream, lambda L, s: L.la_cross_attention_forward(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(kv_len), o.data_ptr(), _ptr(lse), dt, B, N, M, H, d, ldk, ldv,
+        sc, ws.data_ptr(), ws.numel() * ws.element_size(), s))
+    return (o, lse) if return_lse else o
+
+
+def cross_attention_backward(q, k, v, out, lse, dout, kv_len=None, scale=None, ws=None, grads=None, stream=None):
+    """(dq, dk, dv) of sum(cross_attention_forward(q, k, v, kv_len, scale) * dout), from
+    the forward pass's out and lse.  grads may give the three buffers; dk and dv may
+    be views of a wider tensor, as k and v."""
+    dt, B, N, M, H, d, ldk, ldv, sc = _cross_sizes(q, k, v, kv_len, scale)
+    _check_stream(q.device, stream)
+    for name, t in (("out", out), ("dout", dout)):
+        _check_like(name, t, q.shape, q.dtype, q.device)
+    _check_like("lse", lse, (B, H, N), torch.float32, q.device)
+    if grads is None:
+        grads = (_empty(q.shape, q.dtype, q.device, stream),
+                 *(_empty((B, M, H, d), q.dtype, q.device, stream) for _ in range(2)))
+    dq, dk, dv = grads
+    _check_like("dq", dq, q.shape, q.dtype, q.device)
+    lddk, lddv = _check_states("dk", dk, q, M), _check_states("dv", dv, q, M)
+    n = lib().la_cross_attention_backward_workspace_size(dt, B, N, M, H, d)
+    if n == 0:
+        raise LAError(LA_EUNSUPPORTED if d not in (32, 64) else LA_EINVAL, "la_cross_attention_backward")
+    ws = _workspace(n, "la_cross_attention_backward_workspace_size", ws, q.device, stream)
+    _launch("la_cross_attention_backward", q.device, stream, lambda L, s: L.la_cross_attention_backward(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(kv_len), out.data_ptr(), lse.data_ptr(), dout.data_ptr(),
+        dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dt, B, N, M, H, d, ldk, ldv, lddk, lddv, sc, ws.data_ptr(),
+        ws.numel() * ws.element_size(), s))
     return dq, dk, dv
 
 

@@ -327,6 +327,110 @@ LA_API la_status la_dwconv3d(const void *x, void *y, la_dtype dt, int B, int T, 
                              void *stream);
 
 /*
+ * The operators around the linear attention in a Linear DiT block: the norms,
+ * the projections (and the Mix-FFN's pointwise convolutions, which over
+ * channels-last tokens are matrix products) and the attention of the video
+ * tokens to a text encoder's states.  "Nvidia, MIT ve diğerleri video yapay
+ * zeka devrimini başlattı" (aihaber.org), section "Verimli doğrusal DiT",
+ * names the block's linear attention and Mix-FFN; it gives no formulas for
+ * the rest, which are the usual ones, stated at each entry.
+ *
+ * Common to them: DEVICE pointers, 16-byte aligned, of element type dt unless
+ * stated; caller-owned, alive until the enqueued work has finished; outputs
+ * overlap neither inputs nor each other unless stated.  Sums, statistics and
+ * states are fp32, results are rounded once to dt (to nearest even).  Every
+ * workspace must be 256-byte aligned and hold the bytes of the matching
+ * *_workspace_size (a host function; 0 for invalid sizes), else
+ * LA_EWORKSPACE; its contents need not be set, and calls that may overlap in
+ * time need one each (two CUDA graphs that never run at once may share it).
+ * Argument errors return LA_EINVAL / LA_EUNSUPPORTED before anything is
+ * enqueued.  Repeated calls give the same bits.
+ */
+
+/*
+ * Layer norm over the channels of x [B][N][C], with a weight and a bias per
+ * channel: [C], or with per_batch != 0 [B][C], one scale and shift for each
+ * batch element (the modulated norm of a diffusion transformer, the caller
+ * adding the 1 of "1 + scale").
+ *   xh = (x - mean) rstd,  rstd = 1 / sqrt(var + eps)  (var over C, not C - 1),
+ *   y = weight xh + bias
+ * weight and bias may each be NULL (1 and 0).  mean, rstd: fp32 [B][N],
+ * written for the backward pass, or NULL.
+ * Backward, given dy = d loss / d y:
+ *   g = weight dy,  dx = rstd (g - mean_C(g) - xh mean_C(g xh)),
+ *   dweight = sum dy xh,  dbias = sum dy  over the rows that share the vector
+ * ([C] or [B][C], type dt).  dweight and dbias may each be NULL (ws may be
+ * NULL if both are).  B at most 65535 with per_batch, else LA_EUNSUPPORTED.
+ */
+LA_API la_status la_layer_norm_forward(const void *x, const void *weight, const void *bias, void *y, float *mean,
+                                       float *rstd, la_dtype dt, int B, int N, int C, int per_batch, float eps,
+                                       void *stream);
+LA_API size_t la_layer_norm_backward_workspace_size(int B, int N, int C, int per_batch);
+LA_API la_status la_layer_norm_backward(const void *dy, const void *x, const void *weight, const float *mean,
+                                        const float *rstd, void *dx, void *dweight, void *dbias, la_dtype dt,
+                                        int B, int N, int C, int per_batch, void *ws, size_t ws_bytes,
+                                        void *stream);
+
+/*
+ * Matrix product with bias, activation and residual: x [R][K] (R = all tokens
+ * of all batch elements), weight [N][K], bias [N] or NULL, residual [R][N] or
+ * NULL:
+ *   z = x weight^T + bias,  y = act(z) + residual        (y [R][N])
+ * with act none, ReLU, SiLU (z / (1 + e^-z)) or GELU in its tanh form
+ * (z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3)))).  y may be the residual's
+ * buffer (the residual stream updated in place).  pre, if not NULL, receives
+ * z (rounded to dt) for the backward pass.
+ * Backward, given dy:  dz = dy act'(z),
+ *   dx = dz weight [R][K],  dweight = dz^T x [N][K],  dbias = sum_rows dz [N];
+ * the residual's gradient is dy itself.  dx, dweight and dbias may each be
+ * NULL (then weight, x are not needed).  pre is read only with an
+ * activation, and dz is then rounded to dt once, as the products' operand.
+ */
+typedef enum { LA_ACT_NONE = 0, LA_ACT_RELU = 1, LA_ACT_SILU = 2, LA_ACT_GELU = 3 } la_act;
+LA_API size_t la_linear_workspace_size(int R, int K, int N, la_dtype dt);
+LA_API la_status la_linear_forward(const void *x, const void *weight, const void *bias, const void *residual,
+                                   void *y, void *pre, la_dtype dt, la_act act, int R, int K, int N, void *ws,
+                                   size_t ws_bytes, void *stream);
+LA_API size_t la_linear_backward_workspace_size(int R, int K, int N, la_dtype dt, la_act act);
+LA_API la_status la_linear_backward(const void *dy, const void *x, const void *weight, const void *pre, void *dx,
+                                    void *dweight, void *dbias, la_dtype dt, la_act act, int R, int K, int N,
+                                    void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Cross attention of N tokens to the M states of an encoder (softmax over the
+ * states): q, out [B][N][H][d]; k, v: state j of batch element b, head h at
+ * element (b M + j) ld + h d, with ld = ldk or ldv >= H d elements between
+ * consecutive states (a multiple of 16 bytes), so that k and v may be views
+ * of one projection's output [B][M][2][H][d].  d is 32 or 64 and B H at most
+ * 65535, else LA_EUNSUPPORTED.
+ * kv_len: int32 [B] on the device, or NULL: element b attends to its first
+ * kv_len[b] states only (a value outside [0, M] is held to it); whatever k
+ * and v hold behind them, NaN included, has no effect.
+ *   s_ij = scale q_i . k_j,  p_i = softmax(s_i),  out_i = sum_j p_ij v_j
+ * scale finite and > 0.  lse: fp32 [B][H][N], log sum_j exp(s_ij), written
+ * for the backward pass, or NULL.  An element with no states has out = 0,
+ * lse = -inf.
+ * Backward, given dout:  D_i = dout_i . out_i,
+ *   dv_j = sum_i p_ij dout_i,  ds_ij = p_ij (dout_i . v_j - D_i),
+ *   dq_i = scale sum_j ds_ij k_j,  dk_j = scale sum_i ds_ij q_i
+ * dq as q; dk, dv laid out as k, v with their own lddk, lddv; states behind
+ * kv_len get zero gradients, an element with no states zero dq.  p and ds are
+ * rounded to bf16 as the operands of bf16 products (the sum of the softmax is
+ * not).
+ */
+LA_API size_t la_cross_attention_workspace_size(la_dtype dt, int B, int N, int M, int H, int d);
+LA_API la_status la_cross_attention_forward(const void *q, const void *k, const void *v, const int *kv_len,
+                                            void *out, float *lse, la_dtype dt, int B, int N, int M, int H, int d,
+                                            long long ldk, long long ldv, float scale, void *ws, size_t ws_bytes,
+                                            void *stream);
+LA_API size_t la_cross_attention_backward_workspace_size(la_dtype dt, int B, int N, int M, int H, int d);
+LA_API la_status la_cross_attention_backward(const void *q, const void *k, const void *v, const int *kv_len,
+                                             const void *out, const float *lse, const void *dout, void *dq,
+                                             void *dk, void *dv, la_dtype dt, int B, int N, int M, int H, int d,
+                                             long long ldk, long long ldv, long long lddk, long long lddv,
+                                             float scale, void *ws, size_t ws_bytes, void *stream);
+
+/*
  * Token split of one block over R GPUs (one process per GPU), for blocks
  * whose (batch, head) pairs are too few to fill the GPUs: rank r holds a
  * contiguous slice of the block's tokens (q, k, v [B][N_slice][H][d]).  The
