@@ -1,143 +1,259 @@
-// k_linear.cu -- matrix products with bias, activation and residual on the
-// CUDA cores (fp32 accumulation), the activation's derivative, column sums.
+// k_linear.cu -- the parts of the linear layer that run on the CUDA cores:
+// fp32 matrix products, products with few rows, the activation's derivative
+// and column sums.
 //
-//   C[m][n] = sum_k A(m, k) B(n, k);  z = C + bias;  y = act(z) + residual
+//   C[m][n] = sum_k A(m, k) B(n, k);  z = C + bias;  pre = z;  y = act(z) + residual
 // The three products of a linear layer are this one with other layouts:
 // forward A = x, B = W; dx: A = dz, B = W read along its rows; dW: both read
 // along their rows.
 #include "la_dit.cuh"
+#include "la_sm100.cuh"
 
 namespace la {
 namespace {
 
-constexpr int kBM = 64, kBN = 64, kBK = 16, kThreads = 256;
+constexpr int kBK = 16, kThreads = 256;
 
-// 64x64 tile, 4x4 outputs a thread.  AMN / BMN: the operand's m (n) index is contiguous.
-template <typename T, bool AMN, bool BMN>
+template <typename T>
+__device__ __forceinline__ void epilogue(const GemmPlan &g, long long m, long long n, float z) {
+    const long long o = m * g.N + n;
+    if (g.bias) z += to_f(((const T *)g.bias)[n]);
+    if (g.pre) ((T *)g.pre)[o] = from_f<T>(z);
+    z = act_f(z, g.act);
+    if (g.res) z += to_f(((const T *)g.res)[o]);
+    ((T *)g.y)[o] = from_f<T>(z);
+}
+
+// fp32 products: BT x BT tiles, BT/16 x BT/16 outputs a thread, the next 16 k
+// loaded into registers while the current ones are multiplied.  Two fused
+// multiply-adds an instruction.  AMN / BMN: the operand's m (n) index is contiguous.
+template <int BT, bool AMN, bool BMN>
 __global__ void __launch_bounds__(kThreads)
-gemm_ffma(const GemmPlan g) {
-    __shared__ float sa[kBK][kBM + 4], sb[kBK][kBN + 4];
-    const T *A = (const T *)g.a, *B = (const T *)g.b;
-    const long long nt = (g.N + kBN - 1) / kBN;
-    const long long m0 = (long long)blockIdx.x / nt * kBM, n0 = (long long)blockIdx.x % nt * kBN;
+gemm_f32(const GemmPlan g) {
+    constexpr int TM = BT / 16, LD = BT * kBK / kThreads;
+    __shared__ float sa[2][kBK][BT + 4], sb[2][kBK][BT + 4];
+    const float *A = (const float *)g.a, *B = (const float *)g.b;
+    const long long nt = (g.N + BT - 1) / BT;
+    const long long m0 = (long long)blockIdx.x / nt * BT, n0 = (long long)blockIdx.x % nt * BT;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    float acc[4][4] = {};
-    for (long long k0 = 0; k0 < g.K; k0 += kBK) {
+    float2 acc[TM][TM / 2];
 #pragma unroll
-        for (int i = 0; i < kBM * kBK / kThreads; ++i) {
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TM / 2; ++j) acc[i][j] = make_float2(0.f, 0.f);
+    float ra[LD], rb[LD];
+    auto fetch = [&](long long k0) {
+#pragma unroll
+        for (int i = 0; i < LD; ++i) {
             const int e = threadIdx.x + i * kThreads;
-            {
-                const int m = AMN ? e % kBM : e / kBK, k = AMN ? e / kBM : e % kBK;
-                const bool ok = m0 + m < g.M && k0 + k < g.K;
-                sa[k][m] = ok ? to_f(AMN ? A[(k0 + k) * g.lda + m0 + m] : A[(m0 + m) * g.lda + k0 + k]) : 0.f;
-            }
-            {
-                const int n = BMN ? e % kBN : e / kBK, k = BMN ? e / kBN : e % kBK;
-                const bool ok = n0 + n < g.N && k0 + k < g.K;
-                sb[k][n] = ok ? to_f(BMN ? B[(k0 + k) * g.ldb + n0 + n] : B[(n0 + n) * g.ldb + k0 + k]) : 0.f;
-            }
+            const int m = AMN ? e % BT : e / kBK, ka = AMN ? e / BT : e % kBK;
+            const int n = BMN ? e % BT : e / kBK, kb = BMN ? e / BT : e % kBK;
+            ra[i] = m0 + m < g.M && k0 + ka < g.K ? (AMN ? A[(k0 + ka) * g.lda + m0 + m] : A[(m0 + m) * g.lda + k0 + ka]) : 0.f;
+            rb[i] = n0 + n < g.N && k0 + kb < g.K ? (BMN ? B[(k0 + kb) * g.ldb + n0 + n] : B[(n0 + n) * g.ldb + k0 + kb]) : 0.f;
         }
-        __syncthreads();
+    };
+    auto put = [&](int buf) {
+#pragma unroll
+        for (int i = 0; i < LD; ++i) {
+            const int e = threadIdx.x + i * kThreads;
+            sa[buf][AMN ? e / BT : e % kBK][AMN ? e % BT : e / kBK] = ra[i];
+            sb[buf][BMN ? e / BT : e % kBK][BMN ? e % BT : e / kBK] = rb[i];
+        }
+    };
+    fetch(0);
+    put(0);
+    __syncthreads();
+    int buf = 0;
+    for (long long k0 = 0; k0 < g.K; k0 += kBK, buf ^= 1) {
+        if (k0 + kBK < g.K) fetch(k0 + kBK);
 #pragma unroll
         for (int k = 0; k < kBK; ++k) {
-            float a[4], b[4];
+            float a[TM];
+            float2 b[TM / 2];
+            // columns and rows in groups of 4, 64 apart: whole 16-byte reads without bank conflicts
 #pragma unroll
-            for (int i = 0; i < 4; ++i) a[i] = sa[k][ty * 4 + i], b[i] = sb[k][tx * 4 + i];
+            for (int i = 0; i < TM / 4; ++i) {
+                const float4 t = *reinterpret_cast<const float4 *>(&sa[buf][k][i * 64 + ty * 4]);
+                a[4 * i] = t.x, a[4 * i + 1] = t.y, a[4 * i + 2] = t.z, a[4 * i + 3] = t.w;
+                const float4 u = *reinterpret_cast<const float4 *>(&sb[buf][k][i * 64 + tx * 4]);
+                b[2 * i] = make_float2(u.x, u.y), b[2 * i + 1] = make_float2(u.z, u.w);
+            }
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < TM; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] += a[i] * b[j];
+                for (int j = 0; j < TM / 2; ++j) acc[i][j] = sm100::ffma2(make_float2(a[i], a[i]), b[j], acc[i][j]);
         }
+        if (k0 + kBK < g.K) put(buf ^ 1);
         __syncthreads();
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < TM; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const long long m = m0 + ty * 4 + i, n = n0 + tx * 4 + j;
-            if (m >= g.M || n >= g.N) continue;
-            const long long o = m * g.N + n;
-            float z = acc[i][j];
-            if (g.bias) z += to_f(((const T *)g.bias)[n]);
-            if (g.pre) ((T *)g.pre)[o] = from_f<T>(z);
-            z = act_f(z, g.act);
-            if (g.res) z += to_f(((const T *)g.res)[o]);
-            ((T *)g.y)[o] = from_f<T>(z);
+        for (int j = 0; j < TM; ++j) {
+            const long long m = m0 + i / 4 * 64 + ty * 4 + i % 4, n = n0 + j / 4 * 64 + tx * 4 + j % 4;
+            if (m < g.M && n < g.N) epilogue<float>(g, m, n, j & 1 ? acc[i][j / 2].y : acc[i][j / 2].x);
         }
 }
 
-template <typename T>
-int gemm_t(const GemmPlan &g, cudaStream_t s) {
-    const long long grid = ((g.M + kBM - 1) / kBM) * ((g.N + kBN - 1) / kBN);
+template <int BT>
+int gemm_f32_t(const GemmPlan &g, cudaStream_t s) {
+    const long long grid = ((g.M + BT - 1) / BT) * ((g.N + BT - 1) / BT);
     if (grid > 0x7fffffffLL) return -1;
-    auto f = g.a_mn ? (g.b_mn ? gemm_ffma<T, true, true> : gemm_ffma<T, true, false>)
-                    : (g.b_mn ? gemm_ffma<T, false, true> : gemm_ffma<T, false, false>);
+    auto f = g.a_mn ? (g.b_mn ? gemm_f32<BT, true, true> : gemm_f32<BT, true, false>)
+                    : (g.b_mn ? gemm_f32<BT, false, true> : gemm_f32<BT, false, false>);
     f<<<(unsigned)grid, kThreads, 0, s>>>(g);
     return cudaGetLastError() == cudaSuccess ? 1 : -1;
 }
 
-template <typename T>
+// Products with at most 8 rows, both operands k-contiguous: the weight's bytes
+// are the time, so each is read once, by whole warps, 16 bytes a lane (VEC),
+// NC columns at a time for all R rows.
+template <typename T, int VEC>
+struct alignas(sizeof(T) * VEC) Pack {
+    T v[VEC];
+};
+
+template <typename T, int VEC, int R, int NC>
 __global__ void __launch_bounds__(kThreads)
-act_bwd_kernel(const T *__restrict__ dy, const T *__restrict__ pre, T *__restrict__ dz, long long n, int act) {
-    for (long long i = (long long)blockIdx.x * kThreads + threadIdx.x; i < n; i += (long long)gridDim.x * kThreads)
-        dz[i] = from_f<T>(to_f(dy[i]) * act_slope(to_f(pre[i]), act));
+gemm_rows(const GemmPlan g) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const long long n0 = ((long long)blockIdx.x * (kThreads / 32) + warp) * NC;
+    const T *A = (const T *)g.a, *B = (const T *)g.b;
+    if (n0 >= g.N) return;
+    float acc[R][NC] = {};
+#pragma unroll 2
+    for (long long k = lane * VEC; k < g.K; k += 32 * VEC) {
+        Pack<T, VEC> b[NC], a[R];
+#pragma unroll
+        for (int j = 0; j < NC; ++j)
+            b[j] = *reinterpret_cast<const Pack<T, VEC> *>(B + (n0 + j < g.N ? n0 + j : g.N - 1) * g.ldb + k);
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            a[i] = *reinterpret_cast<const Pack<T, VEC> *>(A + (i < g.M ? i : g.M - 1) * g.lda + k);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+#pragma unroll
+            for (int j = 0; j < NC; ++j) {
+                const float f = to_f(b[j].v[e]);
+#pragma unroll
+                for (int i = 0; i < R; ++i) acc[i][j] += to_f(a[i].v[e]) * f;
+            }
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int j = 0; j < NC; ++j) {
+            const float z = warp_sum(acc[i][j]);
+            if (lane == i * NC + j && i < g.M && n0 + j < g.N) epilogue<T>(g, i, n0 + j, z);
+        }
 }
 
-template <typename T>
+template <typename T, int VEC, int R>
+int rows_nc(const GemmPlan &g, cudaStream_t s) {
+    // 4 columns a warp where that still leaves 4 warps a scheduler of the GPU, else 1
+    if (g.N >= 4 * 16 * kSmCount)
+        gemm_rows<T, VEC, R, 4><<<(unsigned)((g.N + 31) / 32), kThreads, 0, s>>>(g);
+    else
+        gemm_rows<T, VEC, R, 1><<<(unsigned)((g.N + 7) / 8), kThreads, 0, s>>>(g);
+    return cudaGetLastError() == cudaSuccess ? 1 : -1;
+}
+
+template <typename T, int VEC>
+int rows_r(const GemmPlan &g, cudaStream_t s) {
+    if (g.M <= 1) return rows_nc<T, VEC, 1>(g, s);
+    if (g.M <= 2) return rows_nc<T, VEC, 2>(g, s);
+    if (g.M <= 4) return rows_nc<T, VEC, 4>(g, s);
+    return rows_nc<T, VEC, 8>(g, s);
+}
+
+// dz = dy act'(pre) and the column sums of dz (of dy without an activation),
+// in one pass: a warp walks rows of 32 x VEC columns, a CTA's 8 warps every
+// 8th row of its range; the warps' sums are added in warp order and leave as
+// part[split][C].  dz or part may be null.
+template <typename T, int VEC>
 __global__ void __launch_bounds__(kThreads)
-col_part(const T *__restrict__ x, float *__restrict__ part, long long R, long long C) {
-    const long long c = (long long)blockIdx.x * kThreads + threadIdx.x;
+act_col(const T *__restrict__ dy, const T *__restrict__ pre, T *__restrict__ dz, float *__restrict__ part, long long R,
+        long long C, int act) {
+    __shared__ float red[8][32 * VEC];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const long long c = ((long long)blockIdx.x * 32 + lane) * VEC;
     const long long sp = blockIdx.y, splits = gridDim.y;
-    if (c >= C) return;
-    float a = 0.f;
-    for (long long r = R * sp / splits; r < R * (sp + 1) / splits; ++r) a += to_f(x[r * C + c]);
-    part[sp * C + c] = a;
-}
-
-template <typename T>
-__global__ void __launch_bounds__(kThreads)
-col_sum(const float *__restrict__ part, T *__restrict__ out, long long C, int splits) {
-    const long long c = (long long)blockIdx.x * kThreads + threadIdx.x;
-    if (c >= C) return;
-    float a = 0.f;
-    for (int s = 0; s < splits; ++s) a += part[(long long)s * C + c];
-    out[c] = from_f<T>(a);
+    const long long r1 = R * (sp + 1) / splits;
+    float a[VEC] = {};
+    if (c < C) {
+#pragma unroll 4
+        for (long long r = R * sp / splits + warp; r < r1; r += 8) {
+            Pack<T, VEC> d = *reinterpret_cast<const Pack<T, VEC> *>(dy + r * C + c);
+            if (act) {
+                const Pack<T, VEC> z = *reinterpret_cast<const Pack<T, VEC> *>(pre + r * C + c);
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    const float f = to_f(d.v[j]) * act_slope(to_f(z.v[j]), act);
+                    a[j] += f;
+                    d.v[j] = from_f<T>(f);
+                }
+                if (dz) *reinterpret_cast<Pack<T, VEC> *>(dz + r * C + c) = d;
+            } else {
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) a[j] += to_f(d.v[j]);
+            }
+        }
+    }
+    if (!part) return;
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) red[warp][j * 32 + lane] = a[j];
+    __syncthreads();
+    for (int e = threadIdx.x; e < 32 * VEC; e += kThreads) {
+        const long long col = ((long long)blockIdx.x * 32 + e % 32) * VEC + e / 32;
+        float s = 0.f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) s += red[w][e];
+        if (col < C) part[sp * C + col] = s;
+    }
 }
 
 int col_splits(long long R, long long C) {
-    const long long cb = (C + kThreads - 1) / kThreads;
-    long long s = (4 * kTargetCtas + cb - 1) / cb;
-    if (s > (R + 15) / 16) s = (R + 15) / 16;
+    const long long cb = (C + 255) / 256;
+    long long s = (8 * kSmCount + cb - 1) / cb;
+    if (s > (R + 31) / 32) s = (R + 31) / 32;
+    if (s > 65535) s = 65535;
     return (int)(s < 1 ? 1 : s);
+}
+
+template <typename T, int VEC>
+int act_col_t(const void *dy, const void *pre, void *dz, float *part, long long R, long long C, int act, cudaStream_t s) {
+    const dim3 grid((unsigned)((C + 32 * VEC - 1) / (32 * VEC)), (unsigned)col_splits(R, C));
+    act_col<T, VEC><<<grid, kThreads, 0, s>>>((const T *)dy, (const T *)pre, (T *)dz, part, R, C, act);
+    return cudaGetLastError() == cudaSuccess ? 1 : -1;
 }
 
 }  // namespace
 
-int launch_gemm_ffma(int is_bf16, const GemmPlan &g, cudaStream_t s) {
-    return is_bf16 ? gemm_t<__nv_bfloat16>(g, s) : gemm_t<float>(g, s);
+int launch_gemm_f32(const GemmPlan &g, cudaStream_t s) {
+    // 128-wide tiles (8 x 8 outputs a thread) where they fill the GPU
+    const long long big = ((g.M + 127) / 128) * ((g.N + 127) / 128);
+    return big >= kSmCount ? gemm_f32_t<128>(g, s) : gemm_f32_t<64>(g, s);
 }
 
-int launch_act_bwd(int is_bf16, const void *dy, const void *pre, void *dz, long long n, int act, cudaStream_t s) {
-    using bf = __nv_bfloat16;
-    const long long want = (n + kThreads - 1) / kThreads;
-    const unsigned grid = (unsigned)(want < 16 * kTargetCtas ? want : 16 * kTargetCtas);
-    if (is_bf16) act_bwd_kernel<bf><<<grid, kThreads, 0, s>>>((const bf *)dy, (const bf *)pre, (bf *)dz, n, act);
-    else act_bwd_kernel<float><<<grid, kThreads, 0, s>>>((const float *)dy, (const float *)pre, (float *)dz, n, act);
-    return cudaGetLastError() == cudaSuccess ? 1 : -1;
+int launch_gemm_rows(int is_bf16, const GemmPlan &g, cudaStream_t s) {
+    if (is_bf16) return g.K % 8 == 0 ? rows_r<__nv_bfloat16, 8>(g, s) : rows_r<__nv_bfloat16, 1>(g, s);
+    return g.K % 4 == 0 ? rows_r<float, 4>(g, s) : rows_r<float, 1>(g, s);
 }
 
-size_t col_sum_ws(long long R, long long C) { return align256(size_t(col_splits(R, C)) * C * sizeof(float)); }
+size_t act_col_ws(long long R, long long C) { return align256(size_t(col_splits(R, C)) * C * sizeof(float)); }
 
-int launch_col_sum(int is_bf16, const void *x, void *out, long long R, long long C, void *ws, cudaStream_t s) {
-    using bf = __nv_bfloat16;
-    const int sp = col_splits(R, C);
-    const unsigned cb = (unsigned)((C + kThreads - 1) / kThreads);
-    if (is_bf16) col_part<bf><<<dim3(cb, sp), kThreads, 0, s>>>((const bf *)x, (float *)ws, R, C);
-    else col_part<float><<<dim3(cb, sp), kThreads, 0, s>>>((const float *)x, (float *)ws, R, C);
-    if (cudaGetLastError() != cudaSuccess) return -1;
-    if (is_bf16) col_sum<bf><<<cb, kThreads, 0, s>>>((const float *)ws, (bf *)out, C, sp);
-    else col_sum<float><<<cb, kThreads, 0, s>>>((const float *)ws, (float *)out, C, sp);
-    return cudaGetLastError() == cudaSuccess ? 2 : -1;
+int launch_act_col(int is_bf16, const void *dy, const void *pre, void *dz, void *colsum, long long R, long long C,
+                   int act, void *ws, cudaStream_t s) {
+    float *part = colsum ? (float *)ws : nullptr;
+    int r;
+    if (is_bf16)
+        r = C % 8 == 0 ? act_col_t<__nv_bfloat16, 8>(dy, pre, dz, part, R, C, act, s)
+                       : act_col_t<__nv_bfloat16, 1>(dy, pre, dz, part, R, C, act, s);
+    else
+        r = C % 4 == 0 ? act_col_t<float, 4>(dy, pre, dz, part, R, C, act, s)
+                       : act_col_t<float, 1>(dy, pre, dz, part, R, C, act, s);
+    if (r < 0 || !colsum) return r;
+    return launch_split_sum(is_bf16, part, colsum, C, col_splits(R, C), s) < 0 ? -1 : 2;
 }
 
 }  // namespace la

@@ -2,12 +2,98 @@
 //
 //   xh = (x - mean) rstd, mean and variance over C, rstd = 1 / sqrt(var + eps);  y = w xh + b
 //   g = w dy;  dx = rstd (g - mean(g) - xh mean(g xh));  dw = sum dy xh, db = sum dy over the rows
+//
+// Bound by HBM: each element is read once (x; x and dy) and written once.  The
+// row stays in registers between the statistics and the result; the vectors
+// come from L1.
 #include "la_dit.cuh"
 
 namespace la {
 namespace {
 
 constexpr int kThreads = 256;
+
+// VEC elements moved by one load or store.
+template <typename T, int VEC>
+struct alignas(sizeof(T) * VEC) Pack {
+    T v[VEC];
+};
+
+template <typename T, int VEC>
+__device__ __forceinline__ Pack<T, VEC> load_pack(const T *p) { return *reinterpret_cast<const Pack<T, VEC> *>(p); }
+
+// Forward, one row on WPR warps, EPT elements a thread.  The variance is the
+// mean square of the deviations (a second pass over the registers).
+template <typename T, int VEC, int EPT, int WPR>
+__global__ void __launch_bounds__(kThreads)
+norm_fwd(const T *__restrict__ x, const T *__restrict__ w, const T *__restrict__ b, T *__restrict__ y,
+         float *__restrict__ mean_out, float *__restrict__ rstd_out, const NormPlan p) {
+    constexpr int TPR = 32 * WPR, RPC = kThreads / TPR, NV = EPT / VEC;
+    __shared__ float red[2][kThreads / 32];
+    const int t = threadIdx.x % TPR, warp = threadIdx.x >> 5;
+    const long long r = (long long)blockIdx.x * RPC + threadIdx.x / TPR;
+    const bool ok = r < p.rows;
+    const T *xr = x + (ok ? r : 0) * p.C;
+    float v[EPT];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * TPR + t) * VEC;
+        if (ok && c < p.C) {
+            const Pack<T, VEC> k = load_pack<T, VEC>(xr + c);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) v[i * VEC + j] = to_f(k.v[j]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) v[i * VEC + j] = 0.f;
+        }
+    }
+    auto row_sum = [&](float s, int which) {
+        s = warp_sum(s);
+        if constexpr (WPR > 1) {
+            if ((threadIdx.x & 31) == 0) red[which][warp] = s;
+            __syncthreads();
+            s = 0.f;
+#pragma unroll
+            for (int i = 0; i < WPR; ++i) s += red[which][warp / WPR * WPR + i];
+        }
+        return s;
+    };
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < EPT; ++i) s += v[i];
+    const float mean = row_sum(s, 0) / (float)p.C;
+    s = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+            const float d = v[i * VEC + j] - mean;
+            s += (i * TPR + t) * VEC < p.C ? d * d : 0.f;
+        }
+    const float rstd = rsqrtf(row_sum(s, 1) / (float)p.C + p.eps);
+    if (!ok) return;
+    const long long vo = p.per_batch ? r / p.N * p.C : 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * TPR + t) * VEC;
+        if (c >= p.C) break;
+        Pack<T, VEC> wk, bk, o;
+        if (w) wk = load_pack<T, VEC>(w + vo + c);
+        if (b) bk = load_pack<T, VEC>(b + vo + c);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+            float f = (v[i * VEC + j] - mean) * rstd;
+            if (w) f *= to_f(wk.v[j]);
+            if (b) f += to_f(bk.v[j]);
+            o.v[j] = from_f<T>(f);
+        }
+        *reinterpret_cast<Pack<T, VEC> *>(y + r * p.C + c) = o;
+    }
+    if (t == 0) {
+        if (mean_out) mean_out[r] = mean;
+        if (rstd_out) rstd_out[r] = rstd;
+    }
+}
 
 __device__ __forceinline__ float block_sum(float x, float *red) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -21,11 +107,12 @@ __device__ __forceinline__ float block_sum(float x, float *red) {
     return t;
 }
 
-// One CTA a row, any C: the row is read three times (the second and third time from L1 or L2).
+// Forward of rows too wide for the registers: one CTA a row, read three times
+// (the second and third time from L1 or L2).
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
-norm_fwd_any(const T *__restrict__ x, const T *__restrict__ w, const T *__restrict__ b, T *__restrict__ y,
-             float *__restrict__ mean_out, float *__restrict__ rstd_out, const NormPlan p) {
+norm_fwd_wide(const T *__restrict__ x, const T *__restrict__ w, const T *__restrict__ b, T *__restrict__ y,
+              float *__restrict__ mean_out, float *__restrict__ rstd_out, const NormPlan p) {
     __shared__ float red[kThreads / 32];
     for (long long r = blockIdx.x; r < p.rows; r += gridDim.x) {
         const T *xr = x + r * p.C;
@@ -52,10 +139,124 @@ norm_fwd_any(const T *__restrict__ x, const T *__restrict__ w, const T *__restri
     }
 }
 
+// Backward in one pass over x and dy.  A CTA of TPR x TY threads walks the
+// rows of its range, TY at a time, kEpt channels a thread; the channels' sums
+// of dy xh and dy stay in registers until the range ends and leave as one
+// piece, part[group][split][2][C].  The next rows are loaded before the
+// current ones are reduced.
+template <typename T, int VEC, int kEpt, int MAXT>
+__global__ void __launch_bounds__(MAXT)
+norm_bwd(const T *__restrict__ dy, const T *__restrict__ x, const T *__restrict__ w, const float *__restrict__ mean,
+         const float *__restrict__ rstd, T *__restrict__ dx, float *__restrict__ part, const NormPlan p, int tpr,
+         int splits) {
+    constexpr int NV = kEpt / VEC;
+    extern __shared__ float sh[];          // [2][2][warps], then (at the end) [threads][2 kEpt]
+    const int warps = blockDim.x >> 5, wpr = tpr >> 5, ty = blockDim.x / tpr;
+    const int t = threadIdx.x % tpr, yy = threadIdx.x / tpr, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = blockIdx.x / splits, sp = blockIdx.x % splits;
+    const long long rows = p.per_batch ? p.N : p.rows;
+    const long long r0 = g * rows + rows * sp / splits, r1 = g * rows + rows * (sp + 1) / splits;
+    const float inv = 1.f / (float)p.C;
+    float wv[kEpt], aw[kEpt] = {}, ab[kEpt] = {};
+    Pack<T, VEC> xp[NV], dp[NV];
+    float m = 0.f, rs = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * tpr + t) * VEC;
+        Pack<T, VEC> k;
+        if (w && c < p.C) k = load_pack<T, VEC>(w + (p.per_batch ? (long long)g * p.C : 0) + c);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) wv[i * VEC + j] = c < p.C ? (w ? to_f(k.v[j]) : 1.f) : 0.f;
+    }
+    auto fetch = [&](long long r) {
+        const bool ok = r < r1;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * tpr + t) * VEC;
+            if (ok && c < p.C) {
+                xp[i] = load_pack<T, VEC>(x + r * p.C + c);
+                dp[i] = load_pack<T, VEC>(dy + r * p.C + c);
+            } else {
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) xp[i].v[j] = dp[i].v[j] = from_f<T>(0.f);
+            }
+        }
+        m = ok ? mean[r] : 0.f;
+        rs = ok ? rstd[r] : 0.f;
+    };
+    fetch(r0 + yy);
+    int par = 0;
+    for (long long r = r0 + yy; r - yy < r1; r += ty, par ^= 1) {
+        float xh[kEpt], d[kEpt];
+        const float rsc = rs;
+        float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+        for (int i = 0; i < kEpt; ++i) {
+            xh[i] = (to_f(xp[i / VEC].v[i % VEC]) - m) * rs;
+            d[i] = to_f(dp[i / VEC].v[i % VEC]);
+            const float gi = d[i] * wv[i];
+            s1 += gi;
+            s2 += gi * xh[i];
+            aw[i] += d[i] * xh[i];
+            ab[i] += d[i];
+        }
+        fetch(r + ty);
+        s1 = warp_sum(s1);
+        s2 = warp_sum(s2);
+        if (wpr > 1) {
+            float *red = sh + par * 2 * warps;
+            if (lane == 0) red[warp] = s1, red[warps + warp] = s2;
+            __syncthreads();
+            s1 = s2 = 0.f;
+            for (int i = 0; i < wpr; ++i) s1 += red[yy * wpr + i], s2 += red[warps + yy * wpr + i];
+        }
+        s1 *= inv;
+        s2 *= inv;
+        if (r < r1) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = (i * tpr + t) * VEC;
+                Pack<T, VEC> o;
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    const int e = i * VEC + j;
+                    o.v[j] = from_f<T>(rsc * (d[e] * wv[e] - s1 - xh[e] * s2));
+                }
+                if (c < p.C) *reinterpret_cast<Pack<T, VEC> *>(dx + r * p.C + c) = o;
+            }
+        }
+    }
+    if (!part) return;
+    float *o = part + ((long long)g * splits + sp) * 2 * p.C;
+    if (ty == 1) {
+#pragma unroll
+        for (int i = 0; i < kEpt; ++i) {
+            const int c = (i / VEC * tpr + t) * VEC + i % VEC;
+            if (c < p.C) o[c] = aw[i], o[p.C + c] = ab[i];
+        }
+        return;
+    }
+    // the TY rows' sums, added in row order
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kEpt; ++i) sh[i * blockDim.x + threadIdx.x] = aw[i], sh[(kEpt + i) * blockDim.x + threadIdx.x] = ab[i];
+    __syncthreads();
+    if (yy) return;
+#pragma unroll
+    for (int i = 0; i < kEpt; ++i) {
+        const int c = (i / VEC * tpr + t) * VEC + i % VEC;
+        float a = 0.f, bsum = 0.f;
+        for (int k = 0; k < ty; ++k) a += sh[i * blockDim.x + k * tpr + t], bsum += sh[(kEpt + i) * blockDim.x + k * tpr + t];
+        if (c < p.C) o[c] = a, o[p.C + c] = bsum;
+    }
+}
+
+// Backward of rows wider than norm_bwd takes: dx a CTA a row, the channels'
+// sums in a second pass, one thread a channel.
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
-norm_dx_any(const T *__restrict__ dy, const T *__restrict__ x, const T *__restrict__ w,
-            const float *__restrict__ mean, const float *__restrict__ rstd, T *__restrict__ dx, const NormPlan p) {
+norm_dx_wide(const T *__restrict__ dy, const T *__restrict__ x, const T *__restrict__ w,
+             const float *__restrict__ mean, const float *__restrict__ rstd, T *__restrict__ dx, const NormPlan p) {
     __shared__ float red[kThreads / 32];
     for (long long r = blockIdx.x; r < p.rows; r += gridDim.x) {
         const long long o = r * p.C, vo = p.per_batch ? r / p.N * p.C : 0;
@@ -76,14 +277,12 @@ norm_dx_any(const T *__restrict__ dy, const T *__restrict__ x, const T *__restri
     }
 }
 
-// Column sums of dy xh and dy: one thread a column, `splits` row ranges a
-// group of rows (a batch element, or all rows); part[group][split][2][C].
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
-norm_dw_part(const T *__restrict__ dy, const T *__restrict__ x, const float *__restrict__ mean,
+norm_dw_wide(const T *__restrict__ dy, const T *__restrict__ x, const float *__restrict__ mean,
              const float *__restrict__ rstd, float *__restrict__ part, const NormPlan p, int splits) {
     const int c = blockIdx.x * kThreads + threadIdx.x;
-    const int g = blockIdx.z, sp = blockIdx.y;
+    const int g = blockIdx.y / splits, sp = blockIdx.y % splits;
     const long long rows = p.per_batch ? p.N : p.rows;
     const long long r0 = g * rows + rows * sp / splits, r1 = g * rows + rows * (sp + 1) / splits;
     if (c >= p.C) return;
@@ -98,55 +297,121 @@ norm_dw_part(const T *__restrict__ dy, const T *__restrict__ x, const float *__r
     o[p.C + c] = bsum;
 }
 
+// out[group][e] = sum over splits of part[group][split][e], e < width: 32
+// columns a CTA, its 8 warps taking every 8th split, then the warps' sums in
+// warp order.  Columns below `cut` go to out0, the rest to out1.
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
-norm_dw_sum(const float *__restrict__ part, T *__restrict__ dw, T *__restrict__ db, int C, int splits) {
-    const int c = blockIdx.x * kThreads + threadIdx.x, g = blockIdx.y;
-    if (c >= C) return;
-    float a = 0.f, b = 0.f;
-    for (int s = 0; s < splits; ++s) {
-        const float *o = part + ((long long)g * splits + s) * 2 * C;
-        a += o[c];
-        b += o[C + c];
+split_sum(const float *__restrict__ part, T *__restrict__ out0, T *__restrict__ out1, long long width, long long cut,
+          int splits) {
+    __shared__ float red[8][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const long long e = (long long)blockIdx.x * 32 + lane, g = blockIdx.y;
+    float a = 0.f;
+    if (e < width) {
+        const float *src = part + g * splits * width + e;
+#pragma unroll 4
+        for (int s = warp; s < splits; s += 8) a += src[s * width];
     }
-    if (dw) dw[(long long)g * C + c] = from_f<T>(a);
-    if (db) db[(long long)g * C + c] = from_f<T>(b);
+    red[warp][lane] = a;
+    __syncthreads();
+    if (warp || e >= width) return;
+    a = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a += red[i][lane];
+    T *o = e < cut ? out0 : out1;
+    if (o) o[e < cut ? g * cut + e : g * (width - cut) + e - cut] = from_f<T>(a);
 }
 
-// Row ranges per group of the partial sums.
-int norm_splits(const NormPlan &p) {
+// ---------------------------------------------------------------- host
+
+constexpr int kWideBwd = 512 * 16;       // widest row of norm_bwd
+constexpr int kWideFwd = 256 * 64;       // widest row of norm_fwd
+
+// Threads a row and a CTA of norm_bwd, and the row ranges of a group (a batch
+// element with per_batch, else all rows): as many CTAs as stay resident.
+struct BwdShape {
+    int ept, tpr, threads, splits;
+};
+BwdShape bwd_shape(const NormPlan &p) {
+    BwdShape b;
+    b.ept = p.C <= 4096 ? 8 : 16;
+    b.tpr = ((p.C + b.ept - 1) / b.ept + 31) / 32 * 32;
+    if (b.tpr > 512) b.tpr = 256;
+    b.threads = b.tpr >= 256 ? b.tpr : 256 / b.tpr * b.tpr;
     const long long rows = p.per_batch ? p.N : p.rows, groups = p.per_batch ? p.B : 1;
-    long long s = (2 * kTargetCtas + groups - 1) / groups;
-    if (s > (rows + 15) / 16) s = (rows + 15) / 16;
-    return (int)(s < 1 ? 1 : s);
+    const int resident = b.threads <= 256 ? 4 : 2;
+    long long s = (long long)resident * kSmCount / groups;
+    if (s > (rows + 7) / 8) s = (rows + 7) / 8;
+    b.splits = (int)(s < 1 ? 1 : s);
+    return b;
+}
+
+template <typename T, int VEC, int EPT, int WPR>
+int fwd_launch(const T *x, const T *w, const T *b, T *y, float *mean, float *rstd, const NormPlan &p, cudaStream_t s) {
+    constexpr int RPC = kThreads / (32 * WPR);
+    const long long grid = (p.rows + RPC - 1) / RPC;
+    if (grid > 0x7fffffffLL) return -1;
+    norm_fwd<T, VEC, EPT, WPR><<<(unsigned)grid, kThreads, 0, s>>>(x, w, b, y, mean, rstd, p);
+    return cudaGetLastError() == cudaSuccess ? 1 : -1;
+}
+
+template <typename T, int VEC>
+int fwd_pick(const T *x, const T *w, const T *b, T *y, float *mean, float *rstd, const NormPlan &p, cudaStream_t s) {
+    if (p.C <= 256) return fwd_launch<T, VEC, 8, 1>(x, w, b, y, mean, rstd, p, s);
+    if (p.C <= 512) return fwd_launch<T, VEC, 16, 1>(x, w, b, y, mean, rstd, p, s);
+    if (p.C <= 1024) return fwd_launch<T, VEC, 32, 1>(x, w, b, y, mean, rstd, p, s);
+    if (p.C <= 2048) return fwd_launch<T, VEC, 64, 1>(x, w, b, y, mean, rstd, p, s);
+    if (p.C <= 4096) return fwd_launch<T, VEC, 64, 2>(x, w, b, y, mean, rstd, p, s);
+    if (p.C <= 8192) return fwd_launch<T, VEC, 64, 4>(x, w, b, y, mean, rstd, p, s);
+    return fwd_launch<T, VEC, 64, 8>(x, w, b, y, mean, rstd, p, s);
 }
 
 template <typename T>
 int norm_fwd_t(const T *x, const T *w, const T *b, T *y, float *mean, float *rstd, const NormPlan &p, cudaStream_t s) {
+    constexpr int V = 16 / sizeof(T);
+    if (p.C <= kWideFwd)
+        return p.C % V == 0 ? fwd_pick<T, V>(x, w, b, y, mean, rstd, p, s) : fwd_pick<T, 1>(x, w, b, y, mean, rstd, p, s);
     const long long grid = p.rows < (1 << 30) ? p.rows : (1 << 30);
-    norm_fwd_any<T><<<(unsigned)grid, kThreads, 0, s>>>(x, w, b, y, mean, rstd, p);
+    norm_fwd_wide<T><<<(unsigned)grid, kThreads, 0, s>>>(x, w, b, y, mean, rstd, p);
     return cudaGetLastError() == cudaSuccess ? 1 : -1;
 }
 
 template <typename T>
 int norm_bwd_t(const T *dy, const T *x, const T *w, const float *mean, const float *rstd, T *dx, T *dw, T *db,
                float *part, const NormPlan &p, cudaStream_t s) {
-    const long long grid = p.rows < (1 << 30) ? p.rows : (1 << 30);
-    norm_dx_any<T><<<(unsigned)grid, kThreads, 0, s>>>(dy, x, w, mean, rstd, dx, p);
+    constexpr int V = 16 / sizeof(T);
+    const BwdShape b = bwd_shape(p);
+    const int groups = p.per_batch ? p.B : 1;
+    if (!dw && !db) part = nullptr;
+    if (p.C <= kWideBwd) {
+        // the CTA's pieces at the end, or two rounds of two sums a warp
+        const int smem = b.threads > b.tpr ? b.threads * 2 * b.ept * 4 : b.threads / 32 * 16;
+        const unsigned grid = (unsigned)(groups * b.splits);
+        const bool vec = p.C % V == 0;
+        auto f = b.ept == 16      ? (vec ? norm_bwd<T, V, 16, 512> : norm_bwd<T, 1, 16, 512>)
+                 : b.threads > 256 ? (vec ? norm_bwd<T, V, 8, 512> : norm_bwd<T, 1, 8, 512>)
+                                   : (vec ? norm_bwd<T, V, 8, 256> : norm_bwd<T, 1, 8, 256>);
+        f<<<grid, b.threads, smem, s>>>(dy, x, w, mean, rstd, dx, part, p, b.tpr, b.splits);
+    } else {
+        const long long grid = p.rows < (1 << 30) ? p.rows : (1 << 30);
+        norm_dx_wide<T><<<(unsigned)grid, kThreads, 0, s>>>(dy, x, w, mean, rstd, dx, p);
+        if (cudaGetLastError() != cudaSuccess) return -1;
+        if (part)
+            norm_dw_wide<T><<<dim3((unsigned)((p.C + kThreads - 1) / kThreads), (unsigned)(groups * b.splits)), kThreads,
+                              0, s>>>(dy, x, mean, rstd, part, p, b.splits);
+    }
     if (cudaGetLastError() != cudaSuccess) return -1;
-    if (!dw && !db) return 1;
-    const int sp = norm_splits(p), groups = p.per_batch ? p.B : 1;
-    const unsigned cb = (unsigned)((p.C + kThreads - 1) / kThreads);
-    norm_dw_part<T><<<dim3(cb, sp, groups), kThreads, 0, s>>>(dy, x, mean, rstd, part, p, sp);
-    if (cudaGetLastError() != cudaSuccess) return -1;
-    norm_dw_sum<T><<<dim3(cb, groups), kThreads, 0, s>>>(part, dw, db, p.C, sp);
-    return cudaGetLastError() == cudaSuccess ? 3 : -1;
+    if (!part) return 1;
+    split_sum<T><<<dim3((unsigned)((2 * (long long)p.C + 31) / 32), groups), kThreads, 0, s>>>(part, dw, db, 2 * (long long)p.C,
+                                                                                              p.C, b.splits);
+    return cudaGetLastError() == cudaSuccess ? 2 : -1;
 }
 
 }  // namespace
 
 size_t norm_bwd_ws(const NormPlan &p) {
-    return align256(size_t(p.per_batch ? p.B : 1) * norm_splits(p) * 2 * p.C * sizeof(float));
+    return align256(size_t(p.per_batch ? p.B : 1) * bwd_shape(p).splits * 2 * p.C * sizeof(float));
 }
 
 int launch_norm_fwd(int is_bf16, const void *x, const void *w, const void *b, void *y, float *mean, float *rstd,
@@ -163,6 +428,14 @@ int launch_norm_bwd(int is_bf16, const void *dy, const void *x, const void *w, c
                                     (bf *)db, (float *)ws, p, s)
                    : norm_bwd_t<float>((const float *)dy, (const float *)x, (const float *)w, mean, rstd, (float *)dx,
                                        (float *)dw, (float *)db, (float *)ws, p, s);
+}
+
+int launch_split_sum(int is_bf16, const float *part, void *out, long long width, int splits, cudaStream_t s) {
+    using bf = __nv_bfloat16;
+    const unsigned grid = (unsigned)((width + 31) / 32);
+    if (is_bf16) split_sum<bf><<<grid, kThreads, 0, s>>>(part, (bf *)out, nullptr, width, width, splits);
+    else split_sum<float><<<grid, kThreads, 0, s>>>(part, (float *)out, nullptr, width, width, splits);
+    return cudaGetLastError() == cudaSuccess ? 1 : -1;
 }
 
 }  // namespace la

@@ -38,12 +38,25 @@ struct GemmPlan {
     void *pre, *y;               // [M][N] or null (pre), [M][N]
     int act;
 };
-int launch_gemm_ffma(int is_bf16, const GemmPlan &g, cudaStream_t s);
-// dz = dy * act'(pre), element by element
-int launch_act_bwd(int is_bf16, const void *dy, const void *pre, void *dz, long long n, int act, cudaStream_t s);
-// out[c] = sum_r x[r][c] in a fixed order; ws holds col_sum_ws bytes
-size_t col_sum_ws(long long R, long long C);
-int launch_col_sum(int is_bf16, const void *x, void *out, long long R, long long C, void *ws, cudaStream_t s);
+// fp32 products on the CUDA cores
+int launch_gemm_f32(const GemmPlan &g, cudaStream_t s);
+// at most kFewRows rows, both operands k-contiguous
+constexpr int kFewRows = 8;
+int launch_gemm_rows(int is_bf16, const GemmPlan &g, cudaStream_t s);
+// bf16 products on the tensor cores (k_linear_tc.cu); lda, ldb are the
+// operands' row lengths, of any size (rows that are not whole 16 bytes are
+// copied to the workspace first)
+bool gemm_tc_fits(long long M, long long N, long long K);
+size_t gemm_tc_ws(const GemmPlan &g);
+int launch_gemm_tc(const GemmPlan &g, void *ws, cudaStream_t s);
+int read_and_clear_linear_flag(unsigned *flag_out);
+// dz = dy * act'(pre) (with an activation and dz not null) and the column sums
+// of dz (colsum not null), in a fixed order; ws holds act_col_ws bytes
+size_t act_col_ws(long long R, long long C);
+int launch_act_col(int is_bf16, const void *dy, const void *pre, void *dz, void *colsum, long long R, long long C,
+                   int act, void *ws, cudaStream_t s);
+// out[e] = sum_s part[s][e], e < width, in a fixed order
+int launch_split_sum(int is_bf16, const float *part, void *out, long long width, int splits, cudaStream_t s);
 
 #ifdef __CUDACC__
 // The activations and their derivatives in fp32.  GELU is the tanh form:

@@ -52,17 +52,55 @@ la_status cross_plan(la::CrossPlan &p, la_dtype dt, int B, int N, int M, int H, 
 
 bool ws_ok(const void *ws, size_t have, size_t need) { return ws && have >= need && al256(ws); }
 
-// Backward of linear: the workspace holds dz (with an activation), then the
-// column sums' pieces.
+// The three products of a linear layer.
+la::GemmPlan fwd_product(long long R, long long K, long long N) {
+    la::GemmPlan g{};
+    g.M = R; g.N = N; g.K = K;
+    g.lda = K; g.ldb = K;
+    return g;
+}
+la::GemmPlan dx_product(long long R, long long K, long long N) {
+    la::GemmPlan g{};
+    g.M = R; g.N = K; g.K = N;
+    g.lda = N; g.ldb = K; g.b_mn = 1;
+    return g;
+}
+la::GemmPlan dw_product(long long R, long long K, long long N) {
+    la::GemmPlan g{};
+    g.M = N; g.N = K; g.K = R;
+    g.lda = N; g.a_mn = 1;
+    g.ldb = K; g.b_mn = 1;
+    return g;
+}
+size_t product_ws(la_dtype dt, const la::GemmPlan &g) {
+    const bool few = g.M <= la::kFewRows && !g.a_mn && !g.b_mn;
+    return dt == LA_BF16 && !few ? la::gemm_tc_ws(g) : 0;
+}
+// A product on the kernel for its type and shape.
+int product(la_dtype dt, const la::GemmPlan &g, void *ws, cudaStream_t s) {
+    if (g.M <= la::kFewRows && !g.a_mn && !g.b_mn) return la::launch_gemm_rows(dt == LA_BF16, g, s);
+    return dt == LA_BF16 ? la::launch_gemm_tc(g, ws, s) : la::launch_gemm_f32(g, s);
+}
+
+bool linear_sizes_ok(int R, int K, int N, la_dtype dt) {
+    return dtype_ok(dt) && count_ok(R, K, 1) && count_ok(N, K, 1) && count_ok(R, N, 1) &&
+           la::gemm_tc_fits(R, N, K) && la::gemm_tc_fits(R, K, N) && la::gemm_tc_fits(N, K, R);
+}
+
+// Backward of linear: the workspace holds dz (with an activation), then what
+// one step at a time needs: the column sums' pieces or a product's workspace.
 struct LinBwdWs {
-    size_t dz, cols, total;
+    size_t step, total;
 };
 LinBwdWs lin_bwd_ws(int R, int K, int N, la_dtype dt, la_act act) {
-    (void)K;
     LinBwdWs w;
-    w.dz = 0;
-    w.cols = act == LA_ACT_NONE ? 0 : la::align256(size_t(R) * N * (dt == LA_BF16 ? 2 : 4));
-    w.total = w.cols + la::col_sum_ws(R, N);
+    w.step = act == LA_ACT_NONE ? 0 : la::align256(size_t(R) * N * (dt == LA_BF16 ? 2 : 4));
+    size_t most = la::act_col_ws(R, N);
+    for (const la::GemmPlan &g : {dx_product(R, K, N), dw_product(R, K, N)}) {
+        const size_t n = product_ws(dt, g);
+        if (n > most) most = n;
+    }
+    w.total = w.step + most;
     return w;
 }
 
@@ -106,8 +144,9 @@ la_status la_layer_norm_backward(const void *dy, const void *x, const void *weig
 }
 
 size_t la_linear_workspace_size(int R, int K, int N, la_dtype dt) {
-    if (!dtype_ok(dt) || !count_ok(R, K, 1) || !count_ok(N, K, 1) || !count_ok(R, N, 1)) return 0;
-    return 256;
+    if (!linear_sizes_ok(R, K, N, dt)) return 0;
+    const size_t n = product_ws(dt, fwd_product(R, K, N));
+    return n ? n : 256;
 }
 
 la_status la_linear_forward(const void *x, const void *weight, const void *bias, const void *residual, void *y,
@@ -119,13 +158,11 @@ la_status la_linear_forward(const void *x, const void *weight, const void *bias,
     const size_t need = la_linear_workspace_size(R, K, N, dt);
     if (!need) return LA_EINVAL;
     if (!ws_ok(ws, ws_bytes, need)) return LA_EWORKSPACE;
-    la::GemmPlan g{};
-    g.M = R; g.N = N; g.K = K;
-    g.a = x; g.lda = K;
-    g.b = weight; g.ldb = K;
+    la::GemmPlan g = fwd_product(R, K, N);
+    g.a = x; g.b = weight;
     g.bias = bias; g.res = residual; g.pre = pre; g.y = y;
     g.act = act;
-    return done(la::launch_gemm_ffma(dt == LA_BF16, g, static_cast<cudaStream_t>(stream)));
+    return done(product(dt, g, ws, static_cast<cudaStream_t>(stream)));
 }
 
 size_t la_linear_backward_workspace_size(int R, int K, int N, la_dtype dt, la_act act) {
@@ -145,29 +182,20 @@ la_status la_linear_backward(const void *dy, const void *x, const void *weight, 
     if (!ws_ok(ws, ws_bytes, need)) return LA_EWORKSPACE;
     const LinBwdWs w = lin_bwd_ws(R, K, N, dt, act);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const int bf = dt == LA_BF16;
-    const void *dz = dy;
-    if (act != LA_ACT_NONE) {
-        void *buf = static_cast<char *>(ws) + w.dz;
-        if (la::launch_act_bwd(bf, dy, pre, buf, (long long)R * N, act, s) < 0) return LA_ECUDA;
-        dz = buf;
-    }
-    if (dbias && la::launch_col_sum(bf, dz, dbias, R, N, static_cast<char *>(ws) + w.cols, s) < 0) return LA_ECUDA;
+    void *step = static_cast<char *>(ws) + w.step;
+    const void *dz = act == LA_ACT_NONE ? dy : ws;
+    if ((act != LA_ACT_NONE || dbias) &&
+        la::launch_act_col(dt == LA_BF16, dy, pre, act == LA_ACT_NONE ? nullptr : ws, dbias, R, N, act, step, s) < 0)
+        return LA_ECUDA;
     if (dx) {
-        la::GemmPlan g{};
-        g.M = R; g.N = K; g.K = N;
-        g.a = dz; g.lda = N;
-        g.b = weight; g.ldb = K; g.b_mn = 1;
-        g.y = dx;
-        if (la::launch_gemm_ffma(bf, g, s) < 0) return LA_ECUDA;
+        la::GemmPlan g = dx_product(R, K, N);
+        g.a = dz; g.b = weight; g.y = dx;
+        if (product(dt, g, step, s) < 0) return LA_ECUDA;
     }
     if (dweight) {
-        la::GemmPlan g{};
-        g.M = N; g.N = K; g.K = R;
-        g.a = dz; g.lda = N; g.a_mn = 1;
-        g.b = x; g.ldb = K; g.b_mn = 1;
-        g.y = dweight;
-        if (la::launch_gemm_ffma(bf, g, s) < 0) return LA_ECUDA;
+        la::GemmPlan g = dw_product(R, K, N);
+        g.a = dz; g.b = x; g.y = dweight;
+        if (product(dt, g, step, s) < 0) return LA_ECUDA;
     }
     return LA_OK;
 }
