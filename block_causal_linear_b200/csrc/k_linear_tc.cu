@@ -3,8 +3,11 @@
 //
 //   C[m][n] = sum_k A(m, k) B(n, k);  z = C + bias;  pre = z;  y = act(z) + residual
 //
-// One CTA a SM, persistent over output tiles of 128 x BN (BN 256, 128 or 64).
-// Warp 0 fills a ring of K = 64 stages by TMA, warp 1 issues the MMAs, warps
+// One CTA a SM, persistent over output tiles: 256 x 256 or 256 x 128 on a pair
+// of CTAs (cta_group::2, each holding 128 rows of A and half of B's, so that a
+// stage's copies and the MMA's reads stay within a SM's 128 bytes of shared
+// memory a clock: a 128 x 256 tile on one CTA needs 192, and ran at 66%), or
+// 128 x 128 and 128 x 64 on one CTA for small outputs.  Warp 0 fills a ring of K = 64 stages by TMA, warp 1 issues the MMAs, warps
 // 2-5 run the epilogue of one tile while the MMAs of the next fill the other
 // half of TMEM.  Either operand may be stored with its k index contiguous
 // (K-major boxes of 64 x rows) or with its row index contiguous (MN-major
@@ -30,10 +33,12 @@ constexpr int kThreads = 192;
 constexpr int kChunk = 32;                        // output columns an epilogue step
 constexpr int kBuf = 32 * kChunk * 2;             // one warp's 32 x 32 bf16 buffer
 
-template <int BN>
+// CG CTAs share a tile of CG * 128 x BN: each holds its 128 rows of A and BN / CG of B's.
+template <int BN, int CG>
 struct Cfg {
-    static constexpr int kA = kBM * kBK * 2, kB = BN * kBK * 2, kStage = kA + kB;
-    static constexpr int kStages = BN == 256 ? 4 : (BN == 128 ? 6 : 8);
+    static constexpr int kBRows = BN / CG;
+    static constexpr int kA = kBM * kBK * 2, kB = kBRows * kBK * 2, kStage = kA + kB;
+    static constexpr int kStages = kBRows == 256 ? 4 : (kBRows == 128 ? 6 : 8);
     static constexpr int kStg = kStages * kStage;            // 4 warps x (2 y + 2 pre) buffers
     static constexpr int kBar = kStg + 4 * 4 * kBuf;
     static constexpr int kBars = 2 * kStages + 4 + 8;
@@ -74,12 +79,12 @@ __device__ __forceinline__ void block_out(const uint8_t *buf, __nv_bfloat16 *dst
                 *reinterpret_cast<const __nv_bfloat16 *>(buf + sw64(r, lane >> 3) + (lane & 7) * 2);
 }
 
-template <int BN>
+template <int BN, int CG>
 __global__ void __launch_bounds__(kThreads, 1)
 gemm_tc(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
         const __grid_constant__ CUtensorMap tm_y, const __grid_constant__ CUtensorMap tm_pre,
         const __grid_constant__ CUtensorMap tm_res, const TcArgs a) {
-    using C = Cfg<BN>;
+    using C = Cfg<BN, CG>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = align1024(smem_raw);
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::kBar), *empty = full + C::kStages;
@@ -88,20 +93,27 @@ gemm_tc(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtens
     volatile int *abort_word = reinterpret_cast<volatile int *>(tmem_slot + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const long long works = (long long)a.mt * a.nt * a.splits;
+    const int rank = CG == 2 ? (int)cluster_ctarank() : 0;         // the even CTA of a pair leads
+    const int first = blockIdx.x / CG, step = gridDim.x / CG;      // this CTA's (pair's) tiles
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::kStages; ++s) mbar_init(&full[s], 1), mbar_init(&empty[s], 1);
-        for (int s = 0; s < 2; ++s) mbar_init(&acc_full[s], 1), mbar_init(&acc_empty[s], 128);
+        for (int s = 0; s < 2; ++s) mbar_init(&acc_full[s], 1), mbar_init(&acc_empty[s], 128 * CG);
         for (int s = 0; s < 8; ++s) mbar_init(&rbar[s], 1);
         *abort_word = 0;
         fence_barrier_init();
     }
     if (warp == 1) {
-        tmem_alloc(tmem_slot, C::kTmem);
-        tmem_relinquish();
+        if constexpr (CG == 2) {
+            tmem_alloc_pair(tmem_slot, C::kTmem);
+        } else {
+            tmem_alloc(tmem_slot, C::kTmem);
+            tmem_relinquish();
+        }
     }
     tc_fence_before();
     __syncthreads();
+    if constexpr (CG == 2) cluster_sync();   // the pair's barriers are set up
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     int issued = 0;   // stages filled (warp 0 lane 0) or read (warp 1 lane 0)
@@ -110,9 +122,9 @@ gemm_tc(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtens
     if (warp == 0 && lane == 0) {
         prefetch_tmap(&tm_a);
         prefetch_tmap(&tm_b);
-        for (long long w = blockIdx.x; w < works; w += gridDim.x) {
+        for (long long w = first; w < works; w += step) {
             const int tile = (int)(w % ((long long)a.mt * a.nt)), sp = (int)(w / ((long long)a.mt * a.nt));
-            const int m0 = tile / a.nt * kBM, n0 = tile % a.nt * BN;
+            const int m0 = (tile / a.nt * CG + rank) * kBM, n0 = tile % a.nt * BN + rank * C::kBRows;
             const int k1 = (sp + 1) * a.kper < a.kiters ? (sp + 1) * a.kper : a.kiters;
             bool ok = true;
             for (int k = sp * a.kper; k < k1; ++k, ++issued) {
@@ -120,29 +132,33 @@ gemm_tc(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtens
                 const uint32_t ph = (uint32_t)(issued / C::kStages) & 1u;
                 if (!(ok = mbar_wait(&empty[s], ph ^ 1u, abort_word, &g_linear_flag, 1))) break;
                 uint8_t *sa = smem + s * C::kStage, *sb = sa + C::kA;
-                mbar_arrive_expect_tx(&full[s], C::kStage);
+                // the leader's barrier counts both CTAs' copies
+                if (rank == 0) mbar_arrive_expect_tx(&full[s], CG * C::kStage);
+                auto load = [&](void *dst, const CUtensorMap *m, int c0, int c1) {
+                    if constexpr (CG == 2) tma_load_2d_pair(dst, m, &full[s], c0, c1);
+                    else tma_load_2d(dst, m, &full[s], c0, c1);
+                };
                 if (a.a_mn) {
-                    tma_load_2d(sa, &tm_a, &full[s], m0, k * kBK);
-                    tma_load_2d(sa + 8192, &tm_a, &full[s], m0 + 64, k * kBK);
+                    load(sa, &tm_a, m0, k * kBK);
+                    load(sa + 8192, &tm_a, m0 + 64, k * kBK);
                 } else {
-                    tma_load_2d(sa, &tm_a, &full[s], k * kBK, m0);
+                    load(sa, &tm_a, k * kBK, m0);
                 }
                 if (a.b_mn) {
 #pragma unroll
-                    for (int j = 0; j < BN / 64; ++j)
-                        tma_load_2d(sb + j * 8192, &tm_b, &full[s], n0 + j * 64, k * kBK);
+                    for (int j = 0; j < C::kBRows / 64; ++j) load(sb + j * 8192, &tm_b, n0 + j * 64, k * kBK);
                 } else {
-                    tma_load_2d(sb, &tm_b, &full[s], k * kBK, n0);
+                    load(sb, &tm_b, k * kBK, n0);
                 }
             }
             if (!ok) break;
         }
-    } else if (warp == 1 && lane == 0) {
-        const uint32_t id = idesc_bf16(kBM, BN, a.a_mn, a.b_mn);
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+        const uint32_t id = idesc_bf16(CG * kBM, BN, a.a_mn, a.b_mn);
         // one MMA's 16 k: 32 bytes along a K-major row, two 8-k groups of 1024 bytes MN-major
         const uint32_t astep = a.a_mn ? 2048 : 32, bstep = a.b_mn ? 2048 : 32;
         bool ok = true;
-        for (long long w = blockIdx.x; ok && w < works; w += gridDim.x, ++tiles) {
+        for (long long w = first; ok && w < works; w += step, ++tiles) {
             const int sp = (int)(w / ((long long)a.mt * a.nt));
             const int k0 = sp * a.kper, k1 = k0 + a.kper < a.kiters ? k0 + a.kper : a.kiters;
             const int buf = tiles & 1;
@@ -157,12 +173,20 @@ gemm_tc(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtens
                 const uint32_t sa = smem_u32(smem + s * C::kStage), sb = sa + C::kA;
 #pragma unroll
                 for (int kk = 0; kk < kBK / 16; ++kk)
-                    mma_bf16(tmem + buf * BN, smem_desc(sa + kk * astep, a.a_mn ? 8192 : 16, 1024, kLayoutSw128),
-                             smem_desc(sb + kk * bstep, a.b_mn ? 8192 : 16, 1024, kLayoutSw128), id,
-                             k > k0 || kk > 0 ? 1u : 0u);
-                mma_commit(&empty[s]);
+                {
+                    const uint64_t da = smem_desc(sa + kk * astep, a.a_mn ? 8192 : 16, 1024, kLayoutSw128);
+                    const uint64_t db = smem_desc(sb + kk * bstep, a.b_mn ? 8192 : 16, 1024, kLayoutSw128);
+                    const uint32_t acc = k > k0 || kk > 0 ? 1u : 0u;
+                    if constexpr (CG == 2) mma_bf16_pair(tmem + buf * BN, da, db, id, acc);
+                    else mma_bf16(tmem + buf * BN, da, db, id, acc);
+                }
+                if constexpr (CG == 2) mma_commit_pair(&empty[s]);
+                else mma_commit(&empty[s]);
             }
-            if (ok) mma_commit(&acc_full[buf]);
+            if (ok) {
+                if constexpr (CG == 2) mma_commit_pair(&acc_full[buf]);
+                else mma_commit(&acc_full[buf]);
+            }
         }
     } else if (warp >= 2) {
         const int q = warp & 3;                                 // this warp's quarter of the TMEM lanes
@@ -172,9 +196,9 @@ gemm_tc(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtens
         uint32_t cc = 0;                                        // chunks so far: buffer cc & 1
         const bool staged = a.splits == 1, tma = staged && !a.direct;
         int t = 0;
-        for (long long w = blockIdx.x; w < works; w += gridDim.x, ++t) {
+        for (long long w = first; w < works; w += step, ++t) {
             const int tile = (int)(w % ((long long)a.mt * a.nt)), sp = (int)(w / ((long long)a.mt * a.nt));
-            const long long row0 = (long long)(tile / a.nt) * kBM + q * 32, n0 = (long long)(tile % a.nt) * BN;
+            const long long row0 = ((long long)(tile / a.nt) * CG + rank) * kBM + q * 32, n0 = (long long)(tile % a.nt) * BN;
             const long long left = a.N - n0;
             const int chunks = row0 >= a.M ? 0 : (int)(left >= BN ? BN / kChunk : (left + kChunk - 1) / kChunk);
             if (tma && a.res && chunks > 0 && lane == 0) {
@@ -282,13 +306,15 @@ gemm_tc(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtens
             }
             if (!ok) break;
             tc_fence_before();
-            mbar_arrive(&acc_empty[buf]);
+            if constexpr (CG == 2) mbar_arrive_leader(&acc_empty[buf]);
+            else mbar_arrive(&acc_empty[buf]);
         }
         if (tma && lane == 0) bulk_wait_all();
     }
-    // after an abort: let copies and MMAs in flight finish before shared memory and TMEM go
+    // after an abort: let copies and MMAs in flight finish before shared memory and TMEM go (a pair's
+    // copies count on the leader, whose stage is freed on both sides by the MMAs)
     if (*abort_word) {
-        if (warp == 0 && lane == 0)
+        if (warp == 0 && lane == 0 && rank == 0)
             for (int i = issued > C::kStages ? issued - C::kStages : 0; i < issued; ++i)
                 final_wait(&full[i % C::kStages], (uint32_t)(i / C::kStages) & 1u);
         if (warp == 1 && lane == 0 && issued > 0)
@@ -296,9 +322,12 @@ gemm_tc(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtens
     }
     __syncwarp();
     __syncthreads();
-    if (warp == 1) {
-        tc_fence_after();
-        tmem_dealloc(tmem, C::kTmem);
+    tc_fence_after();
+    if constexpr (CG == 2) {
+        cluster_sync();   // the peer's arrivals and copies that reach this CTA are over
+        if (warp == 1) tmem_dealloc_pair(tmem, C::kTmem);
+    } else {
+        if (warp == 1) tmem_dealloc(tmem, C::kTmem);
     }
 }
 
@@ -328,27 +357,27 @@ repack(const __nv_bfloat16 *__restrict__ x, __nv_bfloat16 *__restrict__ o, long 
 // ---------------------------------------------------------------- host
 
 struct TcPlan {
-    int bn, mt, nt, kiters, splits, kper;
+    int cg, bn, mt, nt, kiters, splits, kper;
     size_t part;         // bytes of the splits' sums
 };
 
-// The tile width, by the time of the waves that 148 SMs need: a wave of
-// narrower tiles is shorter, but not in proportion (measured below the table
-// in DESIGN): 256 columns cost 256, 128 cost 148, 64 cost 96.  Few tiles over
-// a long k are split along it, at least 4 stages a piece.
+// The tile, by the time of the waves that it needs on 148 SMs: a tile's cost
+// is its time for the same k, measured; 256 x 256 on a pair of CTAs is the
+// cheapest an output, smaller ones waste less where there are few.  Few tiles
+// over a long k are split along it, at least 4 stages a piece.
 TcPlan tc_plan(long long M, long long N, long long K) {
     TcPlan p{};
-    p.mt = (int)((M + kBM - 1) / kBM);
     p.kiters = (int)((K + kBK - 1) / kBK);
-    const int width[3] = {256, 128, 64}, cost[3] = {256, 148, 96};
+    const int group[4] = {2, 2, 1, 1}, width[4] = {256, 128, 128, 64}, cost[4] = {176, 110, 148, 96};
     long long best = -1;
-    for (int i = 0; i < 3; ++i) {
-        const long long nt = (N + width[i] - 1) / width[i];
-        const long long c = (p.mt * nt + kSmCount - 1) / kSmCount * cost[i];
-        if (best < 0 || c < best) best = c, p.bn = width[i], p.nt = (int)nt;
+    for (int i = 0; i < 4; ++i) {
+        const long long mt = (M + group[i] * kBM - 1) / (group[i] * kBM), nt = (N + width[i] - 1) / width[i];
+        const int slots = kSmCount / group[i];
+        const long long c = (mt * nt + slots - 1) / slots * cost[i];
+        if (best < 0 || c < best) best = c, p.cg = group[i], p.bn = width[i], p.mt = (int)mt, p.nt = (int)nt;
     }
-    const long long tiles = (long long)p.mt * p.nt;
-    long long s = tiles <= kSmCount / 2 ? kSmCount / tiles : 1;
+    const long long tiles = (long long)p.mt * p.nt, slots = kSmCount / p.cg;
+    long long s = tiles <= slots / 2 ? slots / tiles : 1;
     if (s > p.kiters / 4) s = p.kiters / 4;
     if (s < 1) s = 1;
     p.kper = (int)((p.kiters + s - 1) / s);
@@ -358,8 +387,10 @@ TcPlan tc_plan(long long M, long long N, long long K) {
 }
 
 bool setup() {
-    return set_smem((const void *)gemm_tc<256>, Cfg<256>::kSmem) && set_smem((const void *)gemm_tc<128>, Cfg<128>::kSmem) &&
-           set_smem((const void *)gemm_tc<64>, Cfg<64>::kSmem);
+    return set_smem((const void *)gemm_tc<256, 2>, Cfg<256, 2>::kSmem) &&
+           set_smem((const void *)gemm_tc<128, 2>, Cfg<128, 2>::kSmem) &&
+           set_smem((const void *)gemm_tc<128, 1>, Cfg<128, 1>::kSmem) &&
+           set_smem((const void *)gemm_tc<64, 1>, Cfg<64, 1>::kSmem);
 }
 bool g_ready[128] = {};
 
@@ -370,12 +401,12 @@ bool operand_map(CUtensorMap *m, const void *base, long long inner, long long ro
     return make_dit_map(m, base, 2, dims, strides, box, 128);
 }
 
-template <int BN>
+template <int BN, int CG>
 int run_tc(const GemmPlan &g, const TcPlan &p, TcArgs &a, cudaStream_t s) {
     CUtensorMap ma, mb, my, mp, mr;
     // K-major: rows are m (n), boxes 64 k x tile rows; MN-major: rows are k, boxes 64 m (n) x 64 k
     if (!(g.a_mn ? operand_map(&ma, g.a, g.M, g.K, g.lda, kBK) : operand_map(&ma, g.a, g.K, g.M, g.lda, kBM))) return -1;
-    if (!(g.b_mn ? operand_map(&mb, g.b, g.N, g.K, g.ldb, kBK) : operand_map(&mb, g.b, g.K, g.N, g.ldb, BN))) return -1;
+    if (!(g.b_mn ? operand_map(&mb, g.b, g.N, g.K, g.ldb, kBK) : operand_map(&mb, g.b, g.K, g.N, g.ldb, BN / CG))) return -1;
     my = mp = mr = ma;
     if (p.splits == 1 && !a.direct) {
         const cuuint64_t dims[2] = {(cuuint64_t)g.N, (cuuint64_t)g.M}, strides[1] = {(cuuint64_t)g.N * 2};
@@ -385,8 +416,18 @@ int run_tc(const GemmPlan &g, const TcPlan &p, TcArgs &a, cudaStream_t s) {
         if (g.res && !make_dit_map(&mr, g.res, 2, dims, strides, box, 64)) return -1;
     }
     const long long works = (long long)p.mt * p.nt * p.splits;
-    gemm_tc<BN><<<(unsigned)(works < kSmCount ? works : kSmCount), kThreads, Cfg<BN>::kSmem, s>>>(ma, mb, my, mp, mr, a);
-    if (cudaGetLastError() != cudaSuccess) return -1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(works < kSmCount / CG ? works : kSmCount / CG) * CG);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Cfg<BN, CG>::kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = CG;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, gemm_tc<BN, CG>, ma, mb, my, mp, mr, a) != cudaSuccess) return -1;
     if (p.splits == 1) return 1;
     const long long want = (g.M * g.N + 255) / 256;
     gemm_finish<<<(unsigned)(want < 16 * kSmCount ? want : 16 * kSmCount), 256, 0, s>>>(a);
@@ -475,7 +516,8 @@ int launch_gemm_tc(const GemmPlan &g0, void *ws, cudaStream_t s) {
     a.part = (float *)ws; a.ldp = (g.N + 3) / 4 * 4;
     a.act = g.act;
     a.direct = g.N % 8 != 0;
-    return p.bn == 256 ? run_tc<256>(g, p, a, s) : (p.bn == 128 ? run_tc<128>(g, p, a, s) : run_tc<64>(g, p, a, s));
+    if (p.cg == 2) return p.bn == 256 ? run_tc<256, 2>(g, p, a, s) : run_tc<128, 2>(g, p, a, s);
+    return p.bn == 128 ? run_tc<128, 1>(g, p, a, s) : run_tc<64, 1>(g, p, a, s);
 }
 
 int read_and_clear_linear_flag(unsigned *flag_out) {

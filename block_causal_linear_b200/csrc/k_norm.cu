@@ -6,12 +6,19 @@
 // Bound by HBM: each element is read once (x; x and dy) and written once.  The
 // row stays in registers between the statistics and the result; the vectors
 // come from L1.
-#include "la_dit.cuh"
+#include "la_sm100_dit.cuh"
 
 namespace la {
+
+using namespace sm100;
+
 namespace {
 
+// Raised by a bounded wait that gave up; read by la_device_status.
+__device__ unsigned int g_norm_flag = 0;
+
 constexpr int kThreads = 256;
+constexpr int kRing = 8;       // most stages of the backward pass's ring
 
 // VEC elements moved by one load or store.
 template <typename T, int VEC>
@@ -34,17 +41,15 @@ norm_fwd(const T *__restrict__ x, const T *__restrict__ w, const T *__restrict__
     const long long r = (long long)blockIdx.x * RPC + threadIdx.x / TPR;
     const bool ok = r < p.rows;
     const T *xr = x + (ok ? r : 0) * p.C;
-    float v[EPT];
+    Pack<T, VEC> v[NV];   // as loaded: a bf16 row takes half the registers, so twice the rows are in flight
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = (i * TPR + t) * VEC;
         if (ok && c < p.C) {
-            const Pack<T, VEC> k = load_pack<T, VEC>(xr + c);
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) v[i * VEC + j] = to_f(k.v[j]);
+            v[i] = load_pack<T, VEC>(xr + c);
         } else {
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) v[i * VEC + j] = 0.f;
+            for (int j = 0; j < VEC; ++j) v[i].v[j] = from_f<T>(0.f);
         }
     }
     auto row_sum = [&](float s, int which) {
@@ -60,14 +65,14 @@ norm_fwd(const T *__restrict__ x, const T *__restrict__ w, const T *__restrict__
     };
     float s = 0.f;
 #pragma unroll
-    for (int i = 0; i < EPT; ++i) s += v[i];
+    for (int i = 0; i < EPT; ++i) s += to_f(v[i / VEC].v[i % VEC]);
     const float mean = row_sum(s, 0) / (float)p.C;
     s = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
-            const float d = v[i * VEC + j] - mean;
+            const float d = to_f(v[i].v[j]) - mean;
             s += (i * TPR + t) * VEC < p.C ? d * d : 0.f;
         }
     const float rstd = rsqrtf(row_sum(s, 1) / (float)p.C + p.eps);
@@ -82,7 +87,7 @@ norm_fwd(const T *__restrict__ x, const T *__restrict__ w, const T *__restrict__
         if (b) bk = load_pack<T, VEC>(b + vo + c);
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
-            float f = (v[i * VEC + j] - mean) * rstd;
+            float f = (to_f(v[i].v[j]) - mean) * rstd;
             if (w) f *= to_f(wk.v[j]);
             if (b) f += to_f(bk.v[j]);
             o.v[j] = from_f<T>(f);
@@ -142,14 +147,144 @@ norm_fwd_wide(const T *__restrict__ x, const T *__restrict__ w, const T *__restr
 // Backward in one pass over x and dy.  A CTA of TPR x TY threads walks the
 // rows of its range, TY at a time, kEpt channels a thread; the channels' sums
 // of dy xh and dy stay in registers until the range ends and leave as one
-// piece, part[group][split][2][C].  The next rows are loaded before the
-// current ones are reduced.
-template <typename T, int VEC, int kEpt, int MAXT>
+// piece, part[group][split][2][C].  Rows arrive by bulk copies in a ring of
+// `stages` stages of TY rows (each a contiguous piece of x and of dy): the
+// loads in flight do not depend on registers or on the one barrier an
+// iteration, which joins the row sums and frees the stage.
+template <typename T, int kEpt, int MAXT>
+__global__ void __launch_bounds__(MAXT)
+norm_bwd_ring(const T *__restrict__ dy, const T *__restrict__ x, const T *__restrict__ w,
+              const float *__restrict__ mean, const float *__restrict__ rstd, T *__restrict__ dx,
+              float *__restrict__ part, const NormPlan p, int tpr, int splits, int stages) {
+    constexpr int VEC = 16 / sizeof(T), NV = kEpt / VEC;
+    extern __shared__ __align__(128) uint8_t ring[];     // [stages][2][TY][C]; at the end [2 kEpt][threads] floats
+    __shared__ uint64_t full[kRing];
+    __shared__ float red[2][2][MAXT / 32];
+    __shared__ int abort_word;
+    const int warps = blockDim.x >> 5, wpr = tpr >> 5, ty = blockDim.x / tpr;
+    const int t = threadIdx.x % tpr, yy = threadIdx.x / tpr, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = blockIdx.x / splits, sp = blockIdx.x % splits;
+    const long long rows = p.per_batch ? p.N : p.rows;
+    const long long r0 = g * rows + rows * sp / splits, r1 = g * rows + rows * (sp + 1) / splits;
+    const uint32_t rowb = (uint32_t)p.C * sizeof(T), half = rowb * ty;
+    const int iters = (int)((r1 - r0 + ty - 1) / ty);
+    const float inv = 1.f / (float)p.C;
+    auto issue = [&](int i) {      // one thread: the copies of iteration i
+        const long long r = r0 + (long long)i * ty;
+        const uint32_t bytes = rowb * (uint32_t)(r1 - r < ty ? r1 - r : ty);
+        uint8_t *st = ring + (size_t)(i % stages) * 2 * half;
+        mbar_arrive_expect_tx(&full[i % stages], 2 * bytes);
+        bulk_load(st, x + r * p.C, bytes, &full[i % stages]);
+        bulk_load(st + half, dy + r * p.C, bytes, &full[i % stages]);
+    };
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1);
+        abort_word = 0;
+        fence_barrier_init();
+    }
+    __syncthreads();
+    if (threadIdx.x == 0)
+        for (int i = 0; i < stages && i < iters; ++i) issue(i);
+    float wv[kEpt], aw[kEpt] = {}, ab[kEpt] = {};
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * tpr + t) * VEC;
+        Pack<T, VEC> k;
+        if (w && c < p.C) k = load_pack<T, VEC>(w + (p.per_batch ? (long long)g * p.C : 0) + c);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) wv[i * VEC + j] = c < p.C ? (w ? to_f(k.v[j]) : 1.f) : 0.f;
+    }
+    int i = 0;
+    float m1 = r0 + yy < r1 ? mean[r0 + yy] : 0.f, rs1 = r0 + yy < r1 ? rstd[r0 + yy] : 0.f;
+    for (; i < iters; ++i) {
+        const long long r = r0 + (long long)i * ty + yy;
+        const bool ok = r < r1;
+        const float m = m1, rs = rs1;
+        if (r + ty < r1) m1 = mean[r + ty], rs1 = rstd[r + ty];      // the next row's, a latency ahead
+        mbar_wait(&full[i % stages], (uint32_t)(i / stages) & 1u, &abort_word, &g_norm_flag, 1);
+        const T *xs = reinterpret_cast<const T *>(ring + (size_t)(i % stages) * 2 * half + (size_t)yy * rowb);
+        const T *ds = reinterpret_cast<const T *>(reinterpret_cast<const uint8_t *>(xs) + half);
+        float xh[kEpt], d[kEpt], s1 = 0.f, s2 = 0.f;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int c = (k * tpr + t) * VEC;
+            const bool in = ok && c < p.C;
+            Pack<T, VEC> xp, dp;
+            if (in) xp = load_pack<T, VEC>(xs + c), dp = load_pack<T, VEC>(ds + c);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                const int e = k * VEC + j;
+                xh[e] = in ? (to_f(xp.v[j]) - m) * rs : 0.f;
+                d[e] = in ? to_f(dp.v[j]) : 0.f;
+                const float gi = d[e] * wv[e];
+                s1 += gi;
+                s2 += gi * xh[e];
+                aw[e] += d[e] * xh[e];
+                ab[e] += d[e];
+            }
+        }
+        s1 = warp_sum(s1);
+        s2 = warp_sum(s2);
+        if (lane == 0) red[i & 1][0][warp] = s1, red[i & 1][1][warp] = s2;
+        __syncthreads();           // the sums are there, and the stage has been read
+        if (abort_word) break;
+        if (threadIdx.x == 0 && i + stages < iters) issue(i + stages);
+        if (wpr > 1) {
+            s1 = s2 = 0.f;
+            for (int k = 0; k < wpr; ++k) s1 += red[i & 1][0][yy * wpr + k], s2 += red[i & 1][1][yy * wpr + k];
+        }
+        s1 *= inv;
+        s2 *= inv;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int c = (k * tpr + t) * VEC;
+            Pack<T, VEC> o;
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                const int e = k * VEC + j;
+                o.v[j] = from_f<T>(rs * (d[e] * wv[e] - s1 - xh[e] * s2));
+            }
+            if (ok && c < p.C) *reinterpret_cast<Pack<T, VEC> *>(dx + r * p.C + c) = o;
+        }
+    }
+    if (i < iters) {               // gave up: let the copies in flight land before the shared memory goes
+        if (threadIdx.x == 0)
+            for (int k = i; k < i + stages && k < iters; ++k) final_wait(&full[k % stages], (uint32_t)(k / stages) & 1u);
+        __syncthreads();
+        return;
+    }
+    if (!part) return;
+    float *o = part + ((long long)g * splits + sp) * 2 * p.C;
+    float *sh = reinterpret_cast<float *>(ring);
+    if (ty > 1) {                  // the TY rows' sums, added in row order
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < kEpt; ++k)
+            sh[k * blockDim.x + threadIdx.x] = aw[k], sh[(kEpt + k) * blockDim.x + threadIdx.x] = ab[k];
+        __syncthreads();
+        if (yy) return;
+#pragma unroll
+        for (int k = 0; k < kEpt; ++k) {
+            aw[k] = ab[k] = 0.f;
+            for (int y = 0; y < ty; ++y)
+                aw[k] += sh[k * blockDim.x + y * tpr + t], ab[k] += sh[(kEpt + k) * blockDim.x + y * tpr + t];
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < kEpt; ++k) {
+        const int c = (k / VEC * tpr + t) * VEC + k % VEC;
+        if (c < p.C) o[c] = aw[k], o[p.C + c] = ab[k];
+    }
+}
+
+// The same for rows that are not whole 16 bytes: element loads, the next rows
+// loaded before the current ones are reduced.
+template <typename T, int kEpt, int MAXT>
 __global__ void __launch_bounds__(MAXT)
 norm_bwd(const T *__restrict__ dy, const T *__restrict__ x, const T *__restrict__ w, const float *__restrict__ mean,
          const float *__restrict__ rstd, T *__restrict__ dx, float *__restrict__ part, const NormPlan p, int tpr,
          int splits) {
-    constexpr int NV = kEpt / VEC;
+    constexpr int VEC = 1, NV = kEpt;
     extern __shared__ float sh[];          // [2][2][warps], then (at the end) [threads][2 kEpt]
     const int warps = blockDim.x >> 5, wpr = tpr >> 5, ty = blockDim.x / tpr;
     const int t = threadIdx.x % tpr, yy = threadIdx.x / tpr, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -347,6 +482,15 @@ BwdShape bwd_shape(const NormPlan &p) {
     return b;
 }
 
+constexpr int kRingBytes = 48 << 10;
+constexpr int kRingMost = 2 * 2 * kWideBwd * 4;   // two stages of the widest fp32 row
+template <typename T> bool g_norm_ready[128] = {};
+template <typename T> bool norm_setup() {
+    return set_smem((const void *)norm_bwd_ring<T, 16, 512>, kRingMost) &&
+           set_smem((const void *)norm_bwd_ring<T, 8, 512>, kRingMost) &&
+           set_smem((const void *)norm_bwd_ring<T, 8, 256>, kRingMost);
+}
+
 template <typename T, int VEC, int EPT, int WPR>
 int fwd_launch(const T *x, const T *w, const T *b, T *y, float *mean, float *rstd, const NormPlan &p, cudaStream_t s) {
     constexpr int RPC = kThreads / (32 * WPR);
@@ -388,11 +532,20 @@ int norm_bwd_t(const T *dy, const T *x, const T *w, const float *mean, const flo
         // the CTA's pieces at the end, or two rounds of two sums a warp
         const int smem = b.threads > b.tpr ? b.threads * 2 * b.ept * 4 : b.threads / 32 * 16;
         const unsigned grid = (unsigned)(groups * b.splits);
-        const bool vec = p.C % V == 0;
-        auto f = b.ept == 16      ? (vec ? norm_bwd<T, V, 16, 512> : norm_bwd<T, 1, 16, 512>)
-                 : b.threads > 256 ? (vec ? norm_bwd<T, V, 8, 512> : norm_bwd<T, 1, 8, 512>)
-                                   : (vec ? norm_bwd<T, V, 8, 256> : norm_bwd<T, 1, 8, 256>);
-        f<<<grid, b.threads, smem, s>>>(dy, x, w, mean, rstd, dx, part, p, b.tpr, b.splits);
+        if (p.C % V == 0) {
+            // a stage is two pieces of TY rows; about 48 KiB of them, so that every resident CTA has its own
+            const int stage = 2 * (b.threads / b.tpr) * p.C * (int)sizeof(T);
+            int stages = kRingBytes / stage;
+            stages = stages < 2 ? 2 : (stages > kRing ? kRing : stages);
+            const int sums = b.threads > b.tpr ? b.threads * 2 * b.ept * 4 : 0;
+            const int bytes = stages * stage > sums ? stages * stage : sums;
+            if (!once_per_device(&g_norm_ready<T>, norm_setup<T>)) return -1;
+            auto f = b.ept == 16 ? norm_bwd_ring<T, 16, 512> : (b.threads > 256 ? norm_bwd_ring<T, 8, 512> : norm_bwd_ring<T, 8, 256>);
+            f<<<grid, b.threads, bytes, s>>>(dy, x, w, mean, rstd, dx, part, p, b.tpr, b.splits, stages);
+        } else {
+            auto f = b.ept == 16 ? norm_bwd<T, 16, 512> : (b.threads > 256 ? norm_bwd<T, 8, 512> : norm_bwd<T, 8, 256>);
+            f<<<grid, b.threads, smem, s>>>(dy, x, w, mean, rstd, dx, part, p, b.tpr, b.splits);
+        }
     } else {
         const long long grid = p.rows < (1 << 30) ? p.rows : (1 << 30);
         norm_dx_wide<T><<<(unsigned)grid, kThreads, 0, s>>>(dy, x, w, mean, rstd, dx, p);
@@ -436,6 +589,13 @@ int launch_split_sum(int is_bf16, const float *part, void *out, long long width,
     if (is_bf16) split_sum<bf><<<grid, kThreads, 0, s>>>(part, (bf *)out, nullptr, width, width, splits);
     else split_sum<float><<<grid, kThreads, 0, s>>>(part, (float *)out, nullptr, width, width, splits);
     return cudaGetLastError() == cudaSuccess ? 1 : -1;
+}
+
+int read_and_clear_norm_flag(unsigned *flag_out) {
+    if (cudaMemcpyFromSymbol(flag_out, g_norm_flag, sizeof(unsigned)) != cudaSuccess) return -1;
+    const unsigned zero = 0;
+    if (*flag_out && cudaMemcpyToSymbol(g_norm_flag, &zero, sizeof(zero)) != cudaSuccess) return -1;
+    return 0;
 }
 
 }  // namespace la

@@ -25,6 +25,8 @@ int launch_norm_fwd(int is_bf16, const void *x, const void *w, const void *b, vo
 int launch_norm_bwd(int is_bf16, const void *dy, const void *x, const void *w, const float *mean, const float *rstd,
                     void *dx, void *dw, void *db, void *ws, const NormPlan &p, cudaStream_t s);
 
+int read_and_clear_norm_flag(unsigned *flag_out);
+
 // ---------------------------------------------------------------- linear
 
 // One product C[m][n] = sum_k A(m, k) B(n, k), row-major C, with the epilogue
