@@ -8,7 +8,7 @@
 // stage's copies and the MMA's reads stay within a SM's 128 bytes of shared
 // memory a clock: a 128 x 256 tile on one CTA needs 192, and ran at 66%), or
 // 128 x 128 and 128 x 64 on one CTA for small outputs.  Warp 0 fills a ring of K = 64 stages by TMA, warp 1 issues the MMAs, warps
-// 2-5 run the epilogue of one tile while the MMAs of the next fill the other
+// 2-9 run the epilogue of one tile while the MMAs of the next fill the other
 // half of TMEM.  Either operand may be stored with its k index contiguous
 // (K-major boxes of 64 x rows) or with its row index contiguous (MN-major
 // boxes of 64 rows x 64 k): the three products of a linear layer need no
@@ -29,7 +29,8 @@ namespace {
 __device__ unsigned int g_linear_flag = 0;
 
 constexpr int kBM = 128, kBK = 64;
-constexpr int kThreads = 192;
+constexpr int kEpi = 8;                           // epilogue warps: two a quarter of the TMEM lanes, half the columns each
+constexpr int kThreads = 64 + 32 * kEpi;
 constexpr int kChunk = 32;                        // output columns an epilogue step
 constexpr int kBuf = 32 * kChunk * 2;             // one warp's 32 x 32 bf16 buffer
 
@@ -39,9 +40,9 @@ struct Cfg {
     static constexpr int kBRows = BN / CG;
     static constexpr int kA = kBM * kBK * 2, kB = kBRows * kBK * 2, kStage = kA + kB;
     static constexpr int kStages = kBRows == 256 ? 4 : (kBRows == 128 ? 6 : 8);
-    static constexpr int kStg = kStages * kStage;            // 4 warps x (2 y + 2 pre) buffers
-    static constexpr int kBar = kStg + 4 * 4 * kBuf;
-    static constexpr int kBars = 2 * kStages + 4 + 8;
+    static constexpr int kStg = kStages * kStage;            // two buffers a warp
+    static constexpr int kBar = kStg + kEpi * 2 * kBuf;
+    static constexpr int kBars = 2 * kStages + 4 + 2 * kEpi;
     static constexpr int kSmem = kBar + kBars * 8 + 16 + 1024;
     static constexpr uint32_t kTmem = 2 * BN;
     static_assert(kSmem <= 232448, "227 KiB of shared memory");
@@ -50,12 +51,12 @@ struct Cfg {
 struct TcArgs {
     long long M, N;
     int kiters;              // K in stages of 64
-    int mt, nt, splits, kper;
+    int mt, nt;
+    int tail, splits, kper;  // tiles from `tail` on are cut into `splits` pieces of kper stages each
     int a_mn, b_mn;
     const __nv_bfloat16 *bias, *res;
     __nv_bfloat16 *pre, *y;
-    float *part;             // splits > 1: fp32 [splits][M][ldp]
-    long long ldp;
+    float *part;             // the pieces' sums, fp32 [tile - tail][piece][CG * 128][BN]
     int act;
     int direct;              // rows of y are not whole 16 bytes: no TMA on y, pre, res
 };
@@ -79,6 +80,43 @@ __device__ __forceinline__ void block_out(const uint8_t *buf, __nv_bfloat16 *dst
                 *reinterpret_cast<const __nv_bfloat16 *>(buf + sw64(r, lane >> 3) + (lane & 7) * 2);
 }
 
+// One piece of work: a whole tile, or one of the pieces along k of a tail tile.
+struct Work {
+    int tile, piece, k0, k1;   // piece < 0: a whole tile
+};
+__device__ __forceinline__ Work work_of(const TcArgs &a, int w) {
+    if (w < a.tail) return {w, -1, 0, a.kiters};
+    const int i = w - a.tail, piece = i % a.splits, k0 = piece * a.kper;
+    return {a.tail + i / a.splits, a.splits > 1 ? piece : -1, k0, k0 + a.kper < a.kiters ? k0 + a.kper : a.kiters};
+}
+
+// act over a chunk, the choice made once
+__device__ __forceinline__ void act_chunk(float (&v)[32], int act) {
+    if (act == 1) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = act_f(v[j], 1);
+    } else if (act == 2) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = act_f(v[j], 2);
+    } else if (act == 3) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = act_f(v[j], 3);
+    }
+}
+
+__device__ __forceinline__ void add8(float *v, uint4 x) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[2 * i] += bf_lo(w[i]), v[2 * i + 1] += bf_hi(w[i]);
+}
+__device__ __forceinline__ void put_chunk(uint8_t *buf, const float (&v)[32], int lane) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<uint4 *>(buf + sw64(lane, j)) =
+            make_uint4(pack_bf2(v[8 * j], v[8 * j + 1]), pack_bf2(v[8 * j + 2], v[8 * j + 3]),
+                       pack_bf2(v[8 * j + 4], v[8 * j + 5]), pack_bf2(v[8 * j + 6], v[8 * j + 7]));
+}
+
 template <int BN, int CG>
 __global__ void __launch_bounds__(kThreads, 1)
 gemm_tc(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
@@ -89,17 +127,22 @@ gemm_tc(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtens
     uint8_t *smem = align1024(smem_raw);
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::kBar), *empty = full + C::kStages;
     uint64_t *acc_full = empty + C::kStages, *acc_empty = acc_full + 2, *rbar = acc_empty + 2;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(rbar + 8);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(rbar + 2 * kEpi);
     volatile int *abort_word = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const long long works = (long long)a.mt * a.nt * a.splits;
+    const int warp = uniform_warp(), lane = threadIdx.x & 31;
+    const int works = a.tail + (a.mt * a.nt - a.tail) * a.splits;
     const int rank = CG == 2 ? (int)cluster_ctarank() : 0;         // the even CTA of a pair leads
     const int first = blockIdx.x / CG, step = gridDim.x / CG;      // this CTA's (pair's) tiles
 
+    if (threadIdx.x == 64) {
+        prefetch_tmap(&tm_a);
+        prefetch_tmap(&tm_b);
+        prefetch_tmap(&tm_y);
+    }
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::kStages; ++s) mbar_init(&full[s], 1), mbar_init(&empty[s], 1);
-        for (int s = 0; s < 2; ++s) mbar_init(&acc_full[s], 1), mbar_init(&acc_empty[s], 128 * CG);
-        for (int s = 0; s < 8; ++s) mbar_init(&rbar[s], 1);
+        for (int s = 0; s < 2; ++s) mbar_init(&acc_full[s], 1), mbar_init(&acc_empty[s], 32 * kEpi * CG);
+        for (int s = 0; s < 2 * kEpi; ++s) mbar_init(&rbar[s], 1);
         *abort_word = 0;
         fence_barrier_init();
     }
@@ -116,179 +159,177 @@ gemm_tc(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtens
     if constexpr (CG == 2) cluster_sync();   // the pair's barriers are set up
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    int issued = 0;   // stages filled (warp 0 lane 0) or read (warp 1 lane 0)
-    int tiles = 0;    // tiles accumulated (warp 1 lane 0)
+    pdl_wait();      // everything above overlaps the previous kernel's end
+    pdl_trigger();
+    int issued = 0;   // stages filled (warp 0) or read (warp 1)
+    int tiles = 0;    // tiles accumulated (warp 1)
 
-    if (warp == 0 && lane == 0) {
-        prefetch_tmap(&tm_a);
-        prefetch_tmap(&tm_b);
-        for (long long w = first; w < works; w += step) {
-            const int tile = (int)(w % ((long long)a.mt * a.nt)), sp = (int)(w / ((long long)a.mt * a.nt));
-            const int m0 = (tile / a.nt * CG + rank) * kBM, n0 = tile % a.nt * BN + rank * C::kBRows;
-            const int k1 = (sp + 1) * a.kper < a.kiters ? (sp + 1) * a.kper : a.kiters;
+    if (warp == 0) {
+        const bool one = elect_one();
+        for (int w = first; w < works; w += step) {
+            const Work k_ = work_of(a, w);
+            const int m0 = (k_.tile / a.nt * CG + rank) * kBM, n0 = k_.tile % a.nt * BN + rank * C::kBRows;
             bool ok = true;
-            for (int k = sp * a.kper; k < k1; ++k, ++issued) {
+            for (int k = k_.k0; k < k_.k1; ++k, ++issued) {
                 const int s = issued % C::kStages;
                 const uint32_t ph = (uint32_t)(issued / C::kStages) & 1u;
-                if (!(ok = mbar_wait(&empty[s], ph ^ 1u, abort_word, &g_linear_flag, 1))) break;
+                if (!(ok = mbar_poll(&empty[s], ph ^ 1u, abort_word, &g_linear_flag, 1))) break;
                 uint8_t *sa = smem + s * C::kStage, *sb = sa + C::kA;
-                // the leader's barrier counts both CTAs' copies
-                if (rank == 0) mbar_arrive_expect_tx(&full[s], CG * C::kStage);
-                auto load = [&](void *dst, const CUtensorMap *m, int c0, int c1) {
-                    if constexpr (CG == 2) tma_load_2d_pair(dst, m, &full[s], c0, c1);
-                    else tma_load_2d(dst, m, &full[s], c0, c1);
-                };
-                if (a.a_mn) {
-                    load(sa, &tm_a, m0, k * kBK);
-                    load(sa + 8192, &tm_a, m0 + 64, k * kBK);
-                } else {
-                    load(sa, &tm_a, k * kBK, m0);
-                }
-                if (a.b_mn) {
+                if (one) {
+                    // the leader's barrier counts both CTAs' copies
+                    if (rank == 0) mbar_arrive_expect_tx(&full[s], CG * C::kStage);
+                    auto load = [&](void *dst, const CUtensorMap *m, int c0, int c1) {
+                        if constexpr (CG == 2) tma_load_2d_pair(dst, m, &full[s], c0, c1);
+                        else tma_load_2d(dst, m, &full[s], c0, c1);
+                    };
+                    if (a.a_mn) {
+                        load(sa, &tm_a, m0, k * kBK);
+                        load(sa + 8192, &tm_a, m0 + 64, k * kBK);
+                    } else {
+                        load(sa, &tm_a, k * kBK, m0);
+                    }
+                    if (a.b_mn) {
 #pragma unroll
-                    for (int j = 0; j < C::kBRows / 64; ++j) load(sb + j * 8192, &tm_b, n0 + j * 64, k * kBK);
-                } else {
-                    load(sb, &tm_b, k * kBK, n0);
+                        for (int j = 0; j < C::kBRows / 64; ++j) load(sb + j * 8192, &tm_b, n0 + j * 64, k * kBK);
+                    } else {
+                        load(sb, &tm_b, k * kBK, n0);
+                    }
                 }
+                __syncwarp();
             }
             if (!ok) break;
         }
-    } else if (warp == 1 && lane == 0 && rank == 0) {
+    } else if (warp == 1 && rank == 0) {
+        const bool one = elect_one();
         const uint32_t id = idesc_bf16(CG * kBM, BN, a.a_mn, a.b_mn);
-        // one MMA's 16 k: 32 bytes along a K-major row, two 8-k groups of 1024 bytes MN-major
-        const uint32_t astep = a.a_mn ? 2048 : 32, bstep = a.b_mn ? 2048 : 32;
+        // one MMA's 16 k: 32 bytes along a K-major row, two 8-k groups of 1024 bytes MN-major (in 16-byte units)
+        const uint64_t astep = (a.a_mn ? 2048 : 32) >> 4, bstep = (a.b_mn ? 2048 : 32) >> 4;
         bool ok = true;
-        for (long long w = first; ok && w < works; w += step, ++tiles) {
-            const int sp = (int)(w / ((long long)a.mt * a.nt));
-            const int k0 = sp * a.kper, k1 = k0 + a.kper < a.kiters ? k0 + a.kper : a.kiters;
+        for (int w = first; ok && w < works; w += step, ++tiles) {
+            const Work k_ = work_of(a, w);
+            const int k0 = k_.k0, k1 = k_.k1;
             const int buf = tiles & 1;
-            if (!(ok = mbar_wait(&acc_empty[buf], ((uint32_t)(tiles >> 1) & 1u) ^ 1u, abort_word, &g_linear_flag, 2)))
+            if (!(ok = mbar_poll(&acc_empty[buf], ((uint32_t)(tiles >> 1) & 1u) ^ 1u, abort_word, &g_linear_flag, 2)))
                 break;
             tc_fence_after();
             for (int k = k0; k < k1; ++k, ++issued) {
                 const int s = issued % C::kStages;
-                if (!(ok = mbar_wait(&full[s], (uint32_t)(issued / C::kStages) & 1u, abort_word, &g_linear_flag, 3)))
+                if (!(ok = mbar_poll(&full[s], (uint32_t)(issued / C::kStages) & 1u, abort_word, &g_linear_flag, 3)))
                     break;
                 tc_fence_after();
-                const uint32_t sa = smem_u32(smem + s * C::kStage), sb = sa + C::kA;
+                const uint32_t sa = smem_u32(smem + s * C::kStage);
+                uint64_t da = smem_desc(sa, a.a_mn ? 8192 : 16, 1024, kLayoutSw128);
+                uint64_t db = smem_desc(sa + C::kA, a.b_mn ? 8192 : 16, 1024, kLayoutSw128);
+                if (one) {
 #pragma unroll
-                for (int kk = 0; kk < kBK / 16; ++kk)
-                {
-                    const uint64_t da = smem_desc(sa + kk * astep, a.a_mn ? 8192 : 16, 1024, kLayoutSw128);
-                    const uint64_t db = smem_desc(sb + kk * bstep, a.b_mn ? 8192 : 16, 1024, kLayoutSw128);
-                    const uint32_t acc = k > k0 || kk > 0 ? 1u : 0u;
-                    if constexpr (CG == 2) mma_bf16_pair(tmem + buf * BN, da, db, id, acc);
-                    else mma_bf16(tmem + buf * BN, da, db, id, acc);
+                    for (int kk = 0; kk < kBK / 16; ++kk, da += astep, db += bstep) {
+                        const uint32_t acc = k > k0 || kk > 0 ? 1u : 0u;
+                        if constexpr (CG == 2) mma_bf16_pair(tmem + buf * BN, da, db, id, acc);
+                        else mma_bf16(tmem + buf * BN, da, db, id, acc);
+                    }
+                    if constexpr (CG == 2) mma_commit_pair(&empty[s]);
+                    else mma_commit(&empty[s]);
                 }
-                if constexpr (CG == 2) mma_commit_pair(&empty[s]);
-                else mma_commit(&empty[s]);
+                __syncwarp();
             }
-            if (ok) {
+            if (ok && one) {
                 if constexpr (CG == 2) mma_commit_pair(&acc_full[buf]);
                 else mma_commit(&acc_full[buf]);
             }
+            __syncwarp();
         }
     } else if (warp >= 2) {
-        const int q = warp & 3;                                 // this warp's quarter of the TMEM lanes
-        uint8_t *ybuf = smem + C::kStg + (warp - 2) * 4 * kBuf, *pbuf = ybuf + 2 * kBuf;
-        uint64_t *rb = rbar + (warp - 2) * 2;
+        constexpr int NC = BN / (2 * kChunk);                   // column chunks of this warp in a tile
+        const int e = warp - 2, q = warp & 3;                   // q: this warp's quarter of the TMEM lanes
+        uint8_t *bufs = smem + C::kStg + e * 2 * kBuf;
+        uint64_t *rb = rbar + e * 2;
         uint32_t rphase = 0;                                    // bit i: the next phase of rb[i]
-        uint32_t cc = 0;                                        // chunks so far: buffer cc & 1
-        const bool staged = a.splits == 1, tma = staged && !a.direct;
+        uint32_t cc = 0;                                        // chunks so far
+        const bool two = !a.pre;                                // both buffers take y in turn; else y and pre
         int t = 0;
-        for (long long w = first; w < works; w += step, ++t) {
-            const int tile = (int)(w % ((long long)a.mt * a.nt)), sp = (int)(w / ((long long)a.mt * a.nt));
-            const long long row0 = ((long long)(tile / a.nt) * CG + rank) * kBM + q * 32, n0 = (long long)(tile % a.nt) * BN;
-            const long long left = a.N - n0;
-            const int chunks = row0 >= a.M ? 0 : (int)(left >= BN ? BN / kChunk : (left + kChunk - 1) / kChunk);
-            if (tma && a.res && chunks > 0 && lane == 0) {
+        for (int w = first; w < works; w += step, ++t) {
+            const Work k_ = work_of(a, w);
+            const bool tma = k_.piece < 0 && !a.direct;
+            const long long row0 = ((long long)(k_.tile / a.nt) * CG + rank) * kBM + q * 32;
+            const long long n0 = (long long)(k_.tile % a.nt) * BN + (e >> 2) * (BN / 2), left = a.N - n0;
+            const int chunks = row0 >= a.M || left <= 0 ? 0 : (left >= BN / 2 ? NC : (int)((left + kChunk - 1) / kChunk));
+            auto fetch_res = [&](int b, long long col) {        // lane 0: the residual's block into buffer b
+                mbar_arrive_expect_tx(&rb[b], kBuf);
+                tma_load_2d(bufs + b * kBuf, &tm_res, &rb[b], (int)col, (int)row0);
+            };
+            if (tma && a.res && two && chunks > 0 && lane == 0) {
                 bulk_wait_read<0>();                            // the buffer's last store has been read out
-                mbar_arrive_expect_tx(&rb[cc & 1], kBuf);
-                tma_load_2d(ybuf + (cc & 1) * kBuf, &tm_res, &rb[cc & 1], (int)n0, (int)row0);
+                fetch_res(cc & 1, n0);
             }
             const int buf = t & 1;
-            if (!mbar_wait(&acc_full[buf], (uint32_t)(t >> 1) & 1u, abort_word, &g_linear_flag, 4)) break;
+            if (!mbar_poll(&acc_full[buf], (uint32_t)(t >> 1) & 1u, abort_word, &g_linear_flag, 4)) break;
             tc_fence_after();
             __syncwarp();
+            const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + buf * BN + (e >> 2) * (BN / 2);
             bool ok = true;
-            for (int c = 0; c < chunks; ++c, ++cc) {
-                const int par = cc & 1;
+            // (not unrolled: four copies of the body overflow the instruction cache, which cost a third of the time)
+#pragma unroll 1
+            for (int c = 0; c < chunks && ok; ++c) {
+                float x[32];
+                tmem_ld32(acc + c * kChunk, x);
                 const long long col = n0 + c * kChunk;
-                float v[32];
-                tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + buf * BN + c * kChunk, v);
-                uint8_t *yb = ybuf + par * kBuf, *pb = pbuf + par * kBuf;
+                const int par = two ? (int)(cc++ & 1) : 0;
+                uint8_t *yb = bufs + par * kBuf, *pb = bufs + kBuf;
+                uint4 bb[4];
+                const bool vec_bias = a.bias && !a.direct && k_.piece < 0;
+                if (vec_bias) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        bb[j] = col + 8 * j < a.N ? __ldg(reinterpret_cast<const uint4 *>(a.bias + col) + j) : make_uint4(0, 0, 0, 0);
+                }
                 if (tma && lane == 0) {
-                    if (a.res) {
+                    if (!two) {
                         bulk_wait_read<0>();
-                        if (c + 1 < chunks) {
-                            mbar_arrive_expect_tx(&rb[par ^ 1], kBuf);
-                            tma_load_2d(ybuf + (par ^ 1) * kBuf, &tm_res, &rb[par ^ 1], (int)(col + kChunk), (int)row0);
-                        }
-                    } else {
+                        if (a.res) fetch_res(0, col);
+                    } else if (!a.res) {
                         bulk_wait_read<1>();
+                    } else if (c + 1 < chunks) {
+                        bulk_wait_read<0>();
+                        fetch_res(par ^ 1, col + kChunk);
                     }
                 }
                 tmem_wait_ld();
+                if (c + 1 == chunks) {                          // all read: the MMAs may have this half of TMEM
+                    tc_fence_before();
+                    if constexpr (CG == 2) mbar_arrive_leader(&acc_empty[buf]);
+                    else mbar_arrive(&acc_empty[buf]);
+                }
                 __syncwarp();
-                if (!staged) {
-                    if (row0 + lane < a.M) {
-                        float *o = a.part + ((long long)sp * a.M + row0 + lane) * a.ldp + col;
+                if (k_.piece >= 0) {
+                    float *o = a.part + (((long long)(k_.tile - a.tail) * a.splits + k_.piece) * (CG * kBM) + rank * kBM + q * 32 + lane) * BN +
+                               (e >> 2) * (BN / 2) + c * kChunk;
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            if (col + 4 * j < a.ldp)
-                                reinterpret_cast<float4 *>(o)[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-                    }
+                    for (int j = 0; j < 8; ++j)
+                        reinterpret_cast<float4 *>(o)[j] = make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
                     continue;
                 }
-                if (a.bias) {
-                    if (!a.direct) {
+                if (vec_bias) {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            if (col + 8 * j >= a.N) break;
-                            const uint4 b = __ldg(reinterpret_cast<const uint4 *>(a.bias + col) + j);
-                            const uint32_t bw[4] = {b.x, b.y, b.z, b.w};
+                    for (int j = 0; j < 4; ++j) add8(x + 8 * j, bb[j]);
+                } else if (a.bias) {
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) v[8 * j + 2 * i] += bf_lo(bw[i]), v[8 * j + 2 * i + 1] += bf_hi(bw[i]);
-                        }
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (col + j < a.N) v[j] += __bfloat162float(a.bias[col + j]);
-                    }
+                    for (int j = 0; j < 32; ++j)
+                        if (col + j < a.N) x[j] += __bfloat162float(a.bias[col + j]);
                 }
-                if (a.pre) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        *reinterpret_cast<uint4 *>(pb + sw64(lane, j)) =
-                            make_uint4(pack_bf2(v[8 * j], v[8 * j + 1]), pack_bf2(v[8 * j + 2], v[8 * j + 3]),
-                                       pack_bf2(v[8 * j + 4], v[8 * j + 5]), pack_bf2(v[8 * j + 6], v[8 * j + 7]));
-                }
-                if (a.act) {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = act_f(v[j], a.act);
-                }
+                if (a.pre) put_chunk(pb, x, lane);
+                act_chunk(x, a.act);
                 if (a.res) {
                     if (tma) {
-                        if (!(ok = mbar_wait(&rb[par], (rphase >> par) & 1u, abort_word, &g_linear_flag, 5))) break;
+                        ok = mbar_poll(&rb[par], (rphase >> par) & 1u, abort_word, &g_linear_flag, 5);
                         rphase ^= 1u << par;
-                        __syncwarp();
                     } else {
                         block_in(yb, a.res, row0, col, a, lane);
-                        __syncwarp();
                     }
+                    __syncwarp();
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint4 r = *reinterpret_cast<const uint4 *>(yb + sw64(lane, j));
-                        const uint32_t rw[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) v[8 * j + 2 * i] += bf_lo(rw[i]), v[8 * j + 2 * i + 1] += bf_hi(rw[i]);
-                    }
+                    for (int j = 0; j < 4; ++j) add8(x + 8 * j, *reinterpret_cast<const uint4 *>(yb + sw64(lane, j)));
                 }
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    *reinterpret_cast<uint4 *>(yb + sw64(lane, j)) =
-                        make_uint4(pack_bf2(v[8 * j], v[8 * j + 1]), pack_bf2(v[8 * j + 2], v[8 * j + 3]),
-                                   pack_bf2(v[8 * j + 4], v[8 * j + 5]), pack_bf2(v[8 * j + 6], v[8 * j + 7]));
+                put_chunk(yb, x, lane);
                 if (tma) {
                     fence_proxy_async_smem();
                     __syncwarp();
@@ -305,11 +346,13 @@ gemm_tc(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtens
                 }
             }
             if (!ok) break;
-            tc_fence_before();
-            if constexpr (CG == 2) mbar_arrive_leader(&acc_empty[buf]);
-            else mbar_arrive(&acc_empty[buf]);
+            if (chunks == 0) {
+                tc_fence_before();
+                if constexpr (CG == 2) mbar_arrive_leader(&acc_empty[buf]);
+                else mbar_arrive(&acc_empty[buf]);
+            }
         }
-        if (tma && lane == 0) bulk_wait_all();
+        if (lane == 0) bulk_wait_read<0>();                     // the buffers have been read out
     }
     // after an abort: let copies and MMAs in flight finish before shared memory and TMEM go (a pair's
     // copies count on the leader, whose stage is freed on both sides by the MMAs)
@@ -331,18 +374,58 @@ gemm_tc(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtens
     }
 }
 
-// y, pre from the splits' sums, in split order
+// y, pre of the tail tiles from their pieces' sums, in piece order: a thread 4
+// columns, a CTA 1024 outputs of one tile.
+template <int BN, int CG>
 __global__ void __launch_bounds__(256)
 gemm_finish(const TcArgs a) {
-    for (long long e = (long long)blockIdx.x * 256 + threadIdx.x; e < a.M * a.N; e += (long long)gridDim.x * 256) {
-        const long long m = e / a.N, n = e - m * a.N;
-        float z = 0.f;
-        for (int s = 0; s < a.splits; ++s) z += a.part[((long long)s * a.M + m) * a.ldp + n];
-        if (a.bias) z += __bfloat162float(a.bias[n]);
-        if (a.pre) a.pre[e] = __float2bfloat16_rn(z);
-        z = act_f(z, a.act);
-        if (a.res) z += __bfloat162float(a.res[e]);
-        a.y[e] = __float2bfloat16_rn(z);
+    pdl_wait();
+    constexpr int kPer = CG * kBM * BN / 1024;                  // CTAs a tile
+    const int i = blockIdx.x / kPer, tile = a.tail + i;
+    const int o = (blockIdx.x % kPer) * 1024 + threadIdx.x * 4;
+    const long long m = (long long)(tile / a.nt) * CG * kBM + o / BN, n = (long long)(tile % a.nt) * BN + o % BN;
+    if (m >= a.M || n >= a.N) return;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float *src = a.part + (long long)i * a.splits * (CG * kBM * BN) + o;
+#pragma unroll 4
+    for (int p = 0; p < a.splits; ++p) {
+        const float4 f = *reinterpret_cast<const float4 *>(src + (long long)p * (CG * kBM * BN));
+        s.x += f.x, s.y += f.y, s.z += f.z, s.w += f.w;
+    }
+    float z[4] = {s.x, s.y, s.z, s.w};
+    const long long e = m * a.N + n;
+    if (a.N % 4 == 0) {                                         // whole 8-byte groups
+        auto get = [&](const __nv_bfloat16 *p, float (&f)[4]) {
+            const uint2 u = *reinterpret_cast<const uint2 *>(p);
+            f[0] = bf_lo(u.x), f[1] = bf_hi(u.x), f[2] = bf_lo(u.y), f[3] = bf_hi(u.y);
+        };
+        auto put = [&](__nv_bfloat16 *p) { *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf2(z[0], z[1]), pack_bf2(z[2], z[3])); };
+        float f[4];
+        if (a.bias) {
+            get(a.bias + n, f);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) z[j] += f[j];
+        }
+        if (a.pre) put(a.pre + e);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) z[j] = act_f(z[j], a.act);
+        if (a.res) {
+            get(a.res + e, f);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) z[j] += f[j];
+        }
+        put(a.y + e);
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (n + j >= a.N) break;
+        float f = z[j];
+        if (a.bias) f += __bfloat162float(a.bias[n + j]);
+        if (a.pre) a.pre[e + j] = __float2bfloat16_rn(f);
+        f = act_f(f, a.act);
+        if (a.res) f += __bfloat162float(a.res[e + j]);
+        a.y[e + j] = __float2bfloat16_rn(f);
     }
 }
 
@@ -357,33 +440,51 @@ repack(const __nv_bfloat16 *__restrict__ x, __nv_bfloat16 *__restrict__ o, long 
 // ---------------------------------------------------------------- host
 
 struct TcPlan {
-    int cg, bn, mt, nt, kiters, splits, kper;
-    size_t part;         // bytes of the splits' sums
+    int cg, bn, mt, nt, kiters, tail, splits, kper;
+    size_t part;         // bytes of the pieces' sums
 };
 
-// The tile, by the time of the waves that it needs on 148 SMs: a tile's cost
-// is its time for the same k, measured; 256 x 256 on a pair of CTAs is the
-// cheapest an output, smaller ones waste less where there are few.  Few tiles
-// over a long k are split along it, at least 4 stages a piece.
+// The tile and the cut, by a model of the time in us: whole waves of tiles over
+// the GPU's slots (74 pairs or 148 CTAs), then the tiles that are left, cut
+// along k into pieces that fill the slots (at least 4 stages each), whose sums
+// a second kernel joins.  A tile's time is `us` a stage plus 1.5 to fill and
+// drain; joining costs 4 and the pieces' bytes.
 TcPlan tc_plan(long long M, long long N, long long K) {
-    TcPlan p{};
-    p.kiters = (int)((K + kBK - 1) / kBK);
-    const int group[4] = {2, 2, 1, 1}, width[4] = {256, 128, 128, 64}, cost[4] = {176, 110, 148, 96};
-    long long best = -1;
-    for (int i = 0; i < 4; ++i) {
-        const long long mt = (M + group[i] * kBM - 1) / (group[i] * kBM), nt = (N + width[i] - 1) / width[i];
-        const int slots = kSmCount / group[i];
-        const long long c = (mt * nt + slots - 1) / slots * cost[i];
-        if (best < 0 || c < best) best = c, p.cg = group[i], p.bn = width[i], p.mt = (int)mt, p.nt = (int)nt;
+    static const struct { int cg, bn; float us; } kTile[4] = {{2, 256, 0.31f}, {2, 128, 0.19f}, {1, 128, 0.21f}, {1, 64, 0.14f}};
+    TcPlan best{};
+    float best_us = -1.f;
+    for (const auto &k : kTile) {
+        TcPlan p{};
+        p.cg = k.cg;
+        p.bn = k.bn;
+        p.kiters = (int)((K + kBK - 1) / kBK);
+        p.mt = (int)((M + k.cg * kBM - 1) / (k.cg * kBM));
+        p.nt = (int)((N + k.bn - 1) / k.bn);
+        const long long tiles = (long long)p.mt * p.nt, slots = kSmCount / k.cg, left = tiles % slots;
+        const float whole = p.kiters * k.us + 1.5f;
+        float us = (float)(tiles / slots) * whole + (left ? whole : 0.f);
+        p.tail = (int)tiles;
+        p.splits = 1;
+        p.kper = p.kiters;
+        if (left) {
+            long long s = slots / left;
+            if (s > p.kiters / 4) s = p.kiters / 4;
+            if (s > 1) {
+                const int kper = (int)((p.kiters + s - 1) / s), pieces = (p.kiters + kper - 1) / kper;
+                const double bytes = (double)left * pieces * k.cg * kBM * k.bn * 4;
+                const float cut = (float)(tiles / slots) * whole + kper * k.us + 1.5f + 4.f + (float)(2 * bytes / 5e6);
+                if (cut < us) {
+                    us = cut;
+                    p.tail = (int)(tiles - left);
+                    p.splits = pieces;
+                    p.kper = kper;
+                    p.part = align256((size_t)bytes);
+                }
+            }
+        }
+        if (best_us < 0.f || us < best_us) best_us = us, best = p;
     }
-    const long long tiles = (long long)p.mt * p.nt, slots = kSmCount / p.cg;
-    long long s = tiles <= slots / 2 ? slots / tiles : 1;
-    if (s > p.kiters / 4) s = p.kiters / 4;
-    if (s < 1) s = 1;
-    p.kper = (int)((p.kiters + s - 1) / s);
-    p.splits = (p.kiters + p.kper - 1) / p.kper;
-    p.part = p.splits > 1 ? align256(size_t(p.splits) * M * ((N + 3) / 4 * 4) * sizeof(float)) : 0;
-    return p;
+    return best;
 }
 
 bool setup() {
@@ -408,30 +509,30 @@ int run_tc(const GemmPlan &g, const TcPlan &p, TcArgs &a, cudaStream_t s) {
     if (!(g.a_mn ? operand_map(&ma, g.a, g.M, g.K, g.lda, kBK) : operand_map(&ma, g.a, g.K, g.M, g.lda, kBM))) return -1;
     if (!(g.b_mn ? operand_map(&mb, g.b, g.N, g.K, g.ldb, kBK) : operand_map(&mb, g.b, g.K, g.N, g.ldb, BN / CG))) return -1;
     my = mp = mr = ma;
-    if (p.splits == 1 && !a.direct) {
+    if (p.tail > 0 && !a.direct) {
         const cuuint64_t dims[2] = {(cuuint64_t)g.N, (cuuint64_t)g.M}, strides[1] = {(cuuint64_t)g.N * 2};
         const cuuint32_t box[2] = {kChunk, 32};
         if (!make_dit_map(&my, g.y, 2, dims, strides, box, 64)) return -1;
         if (g.pre && !make_dit_map(&mp, g.pre, 2, dims, strides, box, 64)) return -1;
         if (g.res && !make_dit_map(&mr, g.res, 2, dims, strides, box, 64)) return -1;
     }
-    const long long works = (long long)p.mt * p.nt * p.splits;
+    const int left = p.mt * p.nt - p.tail, works = p.tail + left * p.splits;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(works < kSmCount / CG ? works : kSmCount / CG) * CG);
+    cfg.gridDim = dim3((unsigned)((works < kSmCount / CG ? works : kSmCount / CG) * CG));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = Cfg<BN, CG>::kSmem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = CG;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     if (cudaLaunchKernelEx(&cfg, gemm_tc<BN, CG>, ma, mb, my, mp, mr, a) != cudaSuccess) return -1;
-    if (p.splits == 1) return 1;
-    const long long want = (g.M * g.N + 255) / 256;
-    gemm_finish<<<(unsigned)(want < 16 * kSmCount ? want : 16 * kSmCount), 256, 0, s>>>(a);
-    return cudaGetLastError() == cudaSuccess ? 2 : -1;
+    if (!left) return 1;
+    return launch_pdl(gemm_finish<BN, CG>, (unsigned)left * (CG * kBM * BN / 1024), 256, 0, s, a) ? 2 : -1;
 }
 
 }  // namespace
@@ -467,7 +568,7 @@ bool once_per_device(bool (*done)[128], bool (*f)()) {
 
 bool gemm_tc_fits(long long M, long long N, long long K) {
     return M < (1LL << 31) - 256 && N < (1LL << 31) - 256 && K < (1LL << 31) - 256 &&
-           (M + kBM - 1) / kBM * ((N + 63) / 64) < (1LL << 31);
+           (M + kBM - 1) / kBM * ((N + 63) / 64) < (1LL << 30);
 }
 
 namespace {
@@ -509,11 +610,11 @@ int launch_gemm_tc(const GemmPlan &g0, void *ws, cudaStream_t s) {
     if (!packed(g.b, g.ldb, g.b_mn ? g.K : g.N, (char *)ws + w.b, s)) return -1;
     TcArgs a{};
     a.M = g.M; a.N = g.N;
-    a.kiters = p.kiters; a.mt = p.mt; a.nt = p.nt; a.splits = p.splits; a.kper = p.kper;
+    a.kiters = p.kiters; a.mt = p.mt; a.nt = p.nt; a.tail = p.tail; a.splits = p.splits; a.kper = p.kper;
     a.a_mn = g.a_mn; a.b_mn = g.b_mn;
     a.bias = (const __nv_bfloat16 *)g.bias; a.res = (const __nv_bfloat16 *)g.res;
     a.pre = (__nv_bfloat16 *)g.pre; a.y = (__nv_bfloat16 *)g.y;
-    a.part = (float *)ws; a.ldp = (g.N + 3) / 4 * 4;
+    a.part = (float *)ws;
     a.act = g.act;
     a.direct = g.N % 8 != 0;
     if (p.cg == 2) return p.bn == 256 ? run_tc<256, 2>(g, p, a, s) : run_tc<128, 2>(g, p, a, s);

@@ -201,7 +201,7 @@ norm_bwd_ring(const T *__restrict__ dy, const T *__restrict__ x, const T *__rest
         const bool ok = r < r1;
         const float m = m1, rs = rs1;
         if (r + ty < r1) m1 = mean[r + ty], rs1 = rstd[r + ty];      // the next row's, a latency ahead
-        mbar_wait(&full[i % stages], (uint32_t)(i / stages) & 1u, &abort_word, &g_norm_flag, 1);
+        mbar_poll(&full[i % stages], (uint32_t)(i / stages) & 1u, &abort_word, &g_norm_flag, 1);
         const T *xs = reinterpret_cast<const T *>(ring + (size_t)(i % stages) * 2 * half + (size_t)yy * rowb);
         const T *ds = reinterpret_cast<const T *>(reinterpret_cast<const uint8_t *>(xs) + half);
         float xh[kEpt], d[kEpt], s1 = 0.f, s2 = 0.f;

@@ -11,6 +11,37 @@ namespace sm100 {
 
 constexpr uint32_t kLayoutSw64 = 4;
 
+// A bounded wait as mbar_wait, for short waits on a kernel's critical path: it
+// polls without a sleep hint and takes its time from the SM's clock (2^32
+// cycles, about 2 s), whose reads cost tens of cycles.
+__device__ __forceinline__ bool mbar_poll(uint64_t *bar, uint32_t parity, volatile int *abort_word,
+                                          unsigned int *dev_flag, int where) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    for (uint32_t i = 1; i < kWaitIters; ++i) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((i & 63u) == 0) {
+            if (*abort_word) return false;
+            if (clock64() - t0 > (1LL << 32)) break;
+        }
+    }
+    *abort_word = 1;
+    atomicCAS(dev_flag, 0u, 0x100u | (unsigned)where);
+    return false;
+}
+
+// One lane of the (converged) warp.  Roles that issue copies or MMAs run on the
+// whole warp with only the issuing instructions under this predicate, so that
+// addresses and descriptors stay in uniform registers: under `lane == 0` the
+// compiler moves each operand there one by one, which made a K = 64 step of the
+// matrix product cost 500 cycles whatever its tile.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(p));
+    return p != 0;
+}
+__device__ __forceinline__ int uniform_warp() { return __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0); }
+
 __device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *m, uint64_t *bar, int c0, int c1) {
     asm volatile(
         "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
