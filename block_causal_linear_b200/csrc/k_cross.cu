@@ -210,16 +210,18 @@ int bwd_t(const void *q, const void *k, const void *v, const void *out, const vo
 
 }  // namespace
 
-size_t cross_fwd_ws(int, const CrossPlan &) { return 256; }
+size_t cross_fwd_ws(int is_bf16, const CrossPlan &p) {
+    const size_t n = is_bf16 ? cross_fwd_tc_ws(p) : 0;
+    return n ? n : 256;
+}
 
 size_t cross_bwd_ws(int, const CrossPlan &p) {
     return dkv_part_bytes(p, dkv_splits(p)) + align256(size_t(p.B) * p.H * p.N * sizeof(float));
 }
 
 int launch_cross_fwd(int is_bf16, const void *q, const void *k, const void *v, void *out, float *lse,
-                     const CrossPlan &p, void *, cudaStream_t s) {
-    using bf = __nv_bfloat16;
-    if (is_bf16) return p.d == 32 ? fwd_t<bf, 32>(q, k, v, out, lse, p, s) : fwd_t<bf, 64>(q, k, v, out, lse, p, s);
+                     const CrossPlan &p, void *ws, cudaStream_t s) {
+    if (is_bf16) return launch_cross_fwd_tc(q, k, v, out, lse, p, ws, s);
     return p.d == 32 ? fwd_t<float, 32>(q, k, v, out, lse, p, s) : fwd_t<float, 64>(q, k, v, out, lse, p, s);
 }
 

@@ -1,0 +1,589 @@
+// k_cross_tc.cu -- bf16 cross attention, forward, on the tensor cores, and the
+// form for few queries.
+//
+//   s_j = scale q . k_j over the valid states j < len;  p = softmax(s);  o = sum p_j v_j
+//
+// One CTA (two a SM) carries two streams, each a tile of 128 queries of one
+// (b, h), through the states in tiles of 64: S = Q K^T into TMEM, the softmax
+// warps (a thread a query) turn it into P = exp2(c s - m) in bf16 over the same
+// columns, O += P V takes P from TMEM.  The maximum m in use moves, and O in
+// TMEM is rescaled, only when a row's maximum outgrows it by 2^8: P is then at
+// most 256, which costs bf16 and the fp32 sum no precision.  Heads are 32 or 64
+// wide, so the exponentials (16 a clock and SM) bound it, not the products or
+// HBM: the streams of a SM overlap so that some warp always has exponentials.
+//
+// Few queries against many states are cut along the states into pieces whose
+// unnormalised sums a second kernel joins.
+#include "la_sm100_dit.cuh"
+
+namespace la {
+
+using namespace sm100;
+
+namespace {
+
+// Raised by a bounded wait that gave up; read by la_device_status.
+__device__ unsigned int g_cross_flag = 0;
+
+constexpr int kQT = 128, kKT = 64;         // queries a stream's tile, states a step
+constexpr int kThreads = 64 + 256;         // TMA warp, MMA warp, 2 x 4 softmax warps
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kGrow = 8.f;               // log2 of the growth that moves the maximum in use
+
+template <int D>
+struct FC {
+    static constexpr int kQ = kQT * D * 2, kKV = kKT * D * 2, kStage = 2 * kKV;
+    static constexpr int kStages = D == 32 ? 4 : 2;
+    static constexpr int kRing = 4 * kQ;                       // [stream][buffer] query tiles first
+    static constexpr int kBar = kRing + kStages * kStage;
+    // q_full[2][2], q_empty[2][2], kv_full, kv_empty, r[2], p[2], fin
+    static constexpr int kBars = 8 + 2 * kStages + 5;
+    static constexpr int kSmem = kBar + kBars * 8 + 16 + 1024;
+    static constexpr uint32_t kLayout = D == 32 ? kLayoutSw64 : kLayoutSw128;
+    static constexpr int kGroup = 8 * D * 2;                   // bytes of 8 rows
+};
+
+struct FwdArgs {
+    CrossPlan p;
+    int pairs, items;        // query tile pairs a (b, h); items = B * H * pairs * splits
+    int splits;              // pieces along the states (in whole steps)
+    __nv_bfloat16 *out;
+    float *lse;
+    float *part;             // splits > 1: [split][B][H][N][D] sums, then [split][B][H][N][2] (m, l)
+};
+
+struct Item {
+    int b, h, pair, j0, j1, len;
+};
+
+// Item w, its sample's length kept from the last item where the sample is the same.
+__device__ __forceinline__ Item item_of(const FwdArgs &a, int w, int &last_b, int &last_len) {
+    Item i;
+    i.pair = w % a.pairs;
+    int r = w / a.pairs;
+    const int sp = r % a.splits;
+    r /= a.splits;
+    i.h = r % a.p.H;
+    i.b = r / a.p.H;
+    if (i.b != last_b) last_b = i.b, last_len = cross_len(a.p, i.b);
+    i.len = last_len;
+    const int steps = (i.len + kKT - 1) / kKT;
+    i.j0 = (int)((long long)steps * sp / a.splits);
+    i.j1 = (int)((long long)steps * (sp + 1) / a.splits);
+    return i;
+}
+
+// No score from element lim on.
+__device__ __forceinline__ void hide(float (&s)[32], int lim) {
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+        if (e >= lim) s[e] = -INFINITY;
+}
+
+// p = exp2(c s - m) of 32 scores: their sum (unrounded) and their bf16 pairs.
+__device__ __forceinline__ void exp_half(const float (&s)[32], uint32_t *pk, float2 &sum, float c, float m) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+        const float2 x = ffma2(make_float2(s[2 * e], s[2 * e + 1]), make_float2(c, c), make_float2(-m, -m));
+        const float2 p = make_float2(ex2(x.x), ex2(x.y));
+        sum.x += p.x;
+        sum.y += p.y;
+        pk[e] = pack_bf2(p.x, p.y);
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 2)
+cross_fwd_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+             const __grid_constant__ CUtensorMap tm_v, const FwdArgs a) {
+    using C = FC<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = align1024(smem_raw);
+    uint64_t *q_full = reinterpret_cast<uint64_t *>(smem + C::kBar), *q_empty = q_full + 4;
+    uint64_t *kv_full = q_empty + 4, *kv_empty = kv_full + C::kStages, *rb = kv_empty + C::kStages, *pb = rb + 2, *fin = pb + 2;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(fin + 1);
+    volatile int *abort_word = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    const int warp = uniform_warp(), lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 32) {
+        prefetch_tmap(&tm_q);
+        prefetch_tmap(&tm_k);
+        prefetch_tmap(&tm_v);
+    }
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 4; ++i) mbar_init(&q_full[i], 1), mbar_init(&q_empty[i], 1);
+        for (int i = 0; i < C::kStages; ++i) mbar_init(&kv_full[i], 1), mbar_init(&kv_empty[i], 1);
+        for (int i = 0; i < 2; ++i) mbar_init(&rb[i], 1), mbar_init(&pb[i], 128);
+        mbar_init(fin, 1);
+        *abort_word = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, 256);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;     // stream t: S and P at 128 t, O at 128 t + 64
+    pdl_wait();
+    pdl_trigger();
+    int last_b = -1, last_len = 0;
+
+    if (warp == 0) {
+        const bool one = elect_one();
+        int kv = 0, uses[2] = {0, 0};
+        bool ok = true;
+        for (int w = blockIdx.x; ok && w < a.items; w += gridDim.x) {
+            const Item i = item_of(a, w, last_b, last_len);
+            if (i.j0 == i.j1) continue;
+            for (int t = 0; ok && t < 2; ++t) {
+                const int q0 = (2 * i.pair + t) * kQT;
+                if (q0 >= a.p.N) break;
+                const int s = 2 * t + (uses[t] & 1);
+                if (!(ok = mbar_poll(&q_empty[s], ((uint32_t)(uses[t] >> 1) & 1u) ^ 1u, abort_word, &g_cross_flag, 1))) break;
+                if (one) {
+                    mbar_arrive_expect_tx(&q_full[s], C::kQ);
+                    tma_load_3d(smem + s * C::kQ, &tm_q, &q_full[s], i.h * D, q0, i.b);
+                }
+                ++uses[t];
+                __syncwarp();
+            }
+            for (int j = i.j0; ok && j < i.j1; ++j, ++kv) {
+                const int s = kv % C::kStages;
+                if (!(ok = mbar_poll(&kv_empty[s], ((uint32_t)(kv / C::kStages) & 1u) ^ 1u, abort_word, &g_cross_flag, 2))) break;
+                if (one) {
+                    uint8_t *st = smem + C::kRing + s * C::kStage;
+                    mbar_arrive_expect_tx(&kv_full[s], C::kStage);
+                    tma_load_3d(st, &tm_k, &kv_full[s], i.h * D, j * kKT, i.b);
+                    tma_load_3d(st + C::kKV, &tm_v, &kv_full[s], i.h * D, j * kKT, i.b);
+                }
+                __syncwarp();
+            }
+        }
+        if (*abort_word && one) {          // let the copies in flight land
+            for (int k = kv > C::kStages ? kv - C::kStages : 0; k < kv; ++k)
+                final_wait(&kv_full[k % C::kStages], (uint32_t)(k / C::kStages) & 1u);
+            for (int t = 0; t < 2; ++t)
+                for (int k = uses[t] > 2 ? uses[t] - 2 : 0; k < uses[t]; ++k)
+                    final_wait(&q_full[2 * t + (k & 1)], (uint32_t)(k >> 1) & 1u);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        const bool one = elect_one();
+        const uint32_t id_s = idesc_bf16(kQT, kKT, 0, 0), id_o = idesc_bf16(kQT, D, 0, 1);
+        int kv = 0, uses[2] = {0, 0};
+        uint32_t pph = 0;                  // bit t: the next phase of pb[t]
+        bool ok = true;
+        // S of stream t from query buffer qs and the states of ring position k; then tell the stream
+        auto issue_s = [&](int t, int qs, int k) {
+            const uint64_t da = smem_desc(smem_u32(smem + qs * C::kQ), 16, C::kGroup, C::kLayout);
+            const uint64_t db = smem_desc(smem_u32(smem + C::kRing + (k % C::kStages) * C::kStage), 16, C::kGroup, C::kLayout);
+            if (one) {
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) mma_bf16(tmem + 128 * t, da + 2 * kk, db + 2 * kk, id_s, kk > 0);
+            }
+        };
+        for (int w = blockIdx.x; ok && w < a.items; w += gridDim.x) {
+            const Item i = item_of(a, w, last_b, last_len);
+            const int n = i.j1 - i.j0;
+            if (n == 0) continue;
+            const int nt = (2 * i.pair + 1) * kQT < a.p.N ? 2 : 1;
+            if (!(ok = mbar_poll(&kv_full[kv % C::kStages], (uint32_t)(kv / C::kStages) & 1u, abort_word, &g_cross_flag, 3))) break;
+            for (int t = 0; t < nt; ++t) {
+                if (!(ok = mbar_poll(&q_full[2 * t + (uses[t] & 1)], (uint32_t)(uses[t] >> 1) & 1u, abort_word, &g_cross_flag, 4))) break;
+                tc_fence_after();
+                issue_s(t, 2 * t + (uses[t] & 1), kv);
+                if (one) mma_commit(&rb[t]);
+                __syncwarp();
+            }
+            for (int j = 0; ok && j < n; ++j, ++kv) {
+                const uint32_t v = smem_u32(smem + C::kRing + (kv % C::kStages) * C::kStage + C::kKV);
+                for (int t = 0; t < nt; ++t) {
+                    if (!(ok = mbar_poll(&pb[t], (pph >> t) & 1u, abort_word, &g_cross_flag, 5))) break;
+                    pph ^= 1u << t;
+                    tc_fence_after();
+                    // P (16 states = 8 columns a step) times V read along its rows
+                    const uint64_t dv = smem_desc(v, 8192, C::kGroup, C::kLayout);
+                    if (one) {
+#pragma unroll
+                        for (int kk = 0; kk < kKT / 16; ++kk)
+                            mma_bf16_ta(tmem + 128 * t + 64, tmem + 128 * t + 8 * kk, dv + kk * (2 * C::kGroup >> 4), id_o, j > 0 || kk > 0);
+                    }
+                    if (j + 1 < n) {
+                        if (t == 0 && !(ok = mbar_poll(&kv_full[(kv + 1) % C::kStages], (uint32_t)((kv + 1) / C::kStages) & 1u,
+                                                       abort_word, &g_cross_flag, 6)))
+                            break;
+                        tc_fence_after();
+                        issue_s(t, 2 * t + (uses[t] & 1), kv + 1);
+                    }
+                    if (one) {
+                        mma_commit(&rb[t]);        // the next S, or the finished O
+                        if (j + 1 == n) mma_commit(&q_empty[2 * t + (uses[t] & 1)]);
+                    }
+                    __syncwarp();
+                }
+                if (ok && one) mma_commit(&kv_empty[kv % C::kStages]);
+                __syncwarp();
+            }
+            for (int t = 0; t < nt; ++t) ++uses[t];
+        }
+        if (*abort_word && one) {
+            mma_commit(fin);
+            final_wait(fin, 0);
+        }
+        __syncwarp();
+    } else {
+        const int t = (warp - 2) >> 2, q = warp & 3;             // stream, quarter of the TMEM lanes
+        const uint32_t ts = tmem + 128 * t + ((uint32_t)(q * 32) << 16), to = ts + 64;
+        const float c = a.p.scale * kLog2e;
+        uint32_t rph = 0;
+        int kv = 0;
+        bool ok = true;
+        for (int w = blockIdx.x; ok && w < a.items; w += gridDim.x) {
+            const Item i = item_of(a, w, last_b, last_len);
+            const int n = i.j1 - i.j0;
+            if ((2 * i.pair + t) * kQT >= a.p.N) {
+                kv += n;
+                continue;
+            }
+            const int row = (2 * i.pair + t) * kQT + q * 32 + lane;
+            float m = -INFINITY, l = 0.f;
+            for (int j = 0; j < n; ++j) {
+                if (!(ok = mbar_poll(&rb[t], rph & 1u, abort_word, &g_cross_flag, 7))) break;
+                rph ^= 1u;
+                tc_fence_after();
+                __syncwarp();
+                const int lim = i.len - (i.j0 + j) * kKT;
+                float hi[32], mx;
+                {
+                    float lo[32];
+                    tmem_ld32(ts, lo);
+                    tmem_ld32(ts + 32, hi);
+                    tmem_wait_ld();
+                    if (lim < kKT) {
+                        hide(lo, lim);
+                        hide(hi, lim - 32);
+                    }
+                    mx = fmaxf(lo[0], hi[0]);
+#pragma unroll
+                    for (int e = 1; e < 32; ++e) mx = fmaxf(mx, fmaxf(lo[e], hi[e]));
+                }
+                if (lim < kKT) {
+                    // zeros for V behind the length (0 * NaN would reach every row)
+                    const int st = (kv + j) % C::kStages;
+                    if (!(ok = mbar_poll(&kv_full[st], (uint32_t)((kv + j) / C::kStages) & 1u, abort_word, &g_cross_flag, 8))) break;
+                    uint4 *v = reinterpret_cast<uint4 *>(smem + C::kRing + st * C::kStage + C::kKV + lim * D * 2);
+                    for (int e = q * 32 + lane; e < (kKT - lim) * (D / 8); e += 128) v[e] = make_uint4(0, 0, 0, 0);
+                    fence_proxy_async_smem();
+                }
+                mx = fmaxf(mx * c, -3.0e38f);
+                if (j == 0) {
+                    m = mx;
+                } else if (__any_sync(0xffffffffu, mx > m + kGrow)) {
+                    const float mn = fmaxf(m, mx), f = ex2(m - mn);
+                    m = mn;
+                    l *= f;
+#pragma unroll 1
+                    for (int h = 0; h < D / 32; ++h) {
+                        float o[32];
+                        uint32_t u[32];
+                        tmem_ld32(to + 32 * h, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(o[e] * f);
+                        tmem_st32(to + 32 * h, u);
+                    }
+                }
+                // P of the upper half first; the lower half of S is read again, which costs less than the
+                // registers to keep it
+                uint32_t pk[32];
+                float2 sum = make_float2(0.f, 0.f);
+                exp_half(hi, pk + 16, sum, c, m);
+                {
+                    float lo[32];
+                    tmem_ld32(ts, lo);
+                    tmem_wait_ld();
+                    if (lim < 32) hide(lo, lim);
+                    exp_half(lo, pk, sum, c, m);
+                }
+                l += sum.x + sum.y;
+                tmem_st32(ts, pk);
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(&pb[t]);
+            }
+            kv += n;
+            if (!ok) break;
+            if (n > 0) {
+                if (!(ok = mbar_poll(&rb[t], rph & 1u, abort_word, &g_cross_flag, 9))) break;
+                rph ^= 1u;
+                tc_fence_after();
+                __syncwarp();
+            }
+            const long long bhn = ((long long)i.b * a.p.H + i.h) * a.p.N + row, rows = (long long)a.p.B * a.p.H * a.p.N;
+            const int sp = (w / a.pairs) % a.splits;
+            const bool in = row < a.p.N;
+            const float inv = n > 0 ? 1.f / l : 0.f;
+#pragma unroll 1
+            for (int h = 0; h < D / 32; ++h) {
+                float o[32];
+                if (n > 0) {
+                    tmem_ld32(to + 32 * h, o);
+                    tmem_wait_ld();
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = 0.f;
+                }
+                if (in && a.splits > 1) {
+                    float4 *po = reinterpret_cast<float4 *>(a.part + (sp * rows + bhn) * D + 32 * h);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) po[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                } else if (in) {
+                    uint4 *go = reinterpret_cast<uint4 *>(a.out + (((long long)i.b * a.p.N + row) * a.p.H + i.h) * D + 32 * h);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        go[e] = make_uint4(pack_bf2(o[8 * e] * inv, o[8 * e + 1] * inv), pack_bf2(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
+                                           pack_bf2(o[8 * e + 4] * inv, o[8 * e + 5] * inv), pack_bf2(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+                }
+            }
+            tc_fence_before();
+            if (in && a.splits > 1) reinterpret_cast<float2 *>(a.part + a.splits * rows * D)[sp * rows + bhn] = make_float2(m, l);
+            else if (in && a.lse) a.lse[bhn] = n > 0 ? (m + __log2f(l)) * kLn2 : -INFINITY;
+        }
+    }
+    __syncwarp();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 256);
+    }
+}
+
+// A few queries (at most NQ a CTA) on the CUDA cores: K and V are streamed once,
+// D / 8 lanes a state with 16 bytes each, the CTA's 4 warps every 4th group of
+// states; each lane group keeps its own maximum and sums, joined at the end.
+template <int D, int NQ>
+__global__ void __launch_bounds__(128)
+cross_few(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restrict__ k, const __nv_bfloat16 *__restrict__ v,
+          const FwdArgs a) {
+    constexpr int LG = D / 8, G = 32 / LG, U = 4;      // lanes a state, states a warp and step, steps in flight
+    __shared__ float sm[4 * G][NQ], sl[4 * G][NQ], so[4 * G][NQ][D];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane / LG, part = lane % LG;
+    const int sp = blockIdx.x, b = blockIdx.y / a.p.H, h = blockIdx.y % a.p.H, n0 = blockIdx.z * NQ;
+    pdl_wait();
+    pdl_trigger();
+    const int len = cross_len(a.p, b);
+    const int j0 = (int)((long long)len * sp / a.splits), j1 = (int)((long long)len * (sp + 1) / a.splits);
+    const float c = a.p.scale * kLog2e;
+    float qr[NQ][8], o[NQ][8] = {}, m[NQ], l[NQ] = {};
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+        m[n] = -INFINITY;
+        const int row = n0 + n < a.p.N ? n0 + n : a.p.N - 1;
+        const uint4 u = *reinterpret_cast<const uint4 *>(q + (((long long)b * a.p.N + row) * a.p.H + h) * D + part * 8);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) qr[n][2 * e] = bf_lo(w[e]) * c, qr[n][2 * e + 1] = bf_hi(w[e]) * c;
+    }
+    const __nv_bfloat16 *kb = k + (long long)b * a.p.M * a.p.ldk + h * D + part * 8;
+    const __nv_bfloat16 *vb = v + (long long)b * a.p.M * a.p.ldv + h * D + part * 8;
+    for (int j = j0 + warp * G * U; j < j1; j += 4 * G * U) {
+        uint4 ku[U], vu[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int jj = j + u * G + g;
+            const bool in = jj < j1;
+            ku[u] = in ? *reinterpret_cast<const uint4 *>(kb + (long long)jj * a.p.ldk) : make_uint4(0, 0, 0, 0);
+            vu[u] = in ? *reinterpret_cast<const uint4 *>(vb + (long long)jj * a.p.ldv) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+            float s[U], mx = m[n];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const uint32_t w[4] = {ku[u].x, ku[u].y, ku[u].z, ku[u].w};
+                float x = 0.f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x += qr[n][2 * e] * bf_lo(w[e]) + qr[n][2 * e + 1] * bf_hi(w[e]);
+#pragma unroll
+                for (int sh = 1; sh < LG; sh <<= 1) x += __shfl_xor_sync(0xffffffffu, x, sh);
+                s[u] = j + u * G + g < j1 ? x : -INFINITY;
+                mx = fmaxf(mx, s[u]);
+            }
+            const float base = fmaxf(mx, -3.0e38f), f = ex2(m[n] - base);
+            m[n] = base;
+            l[n] *= f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[n][e] *= f;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const float p = ex2(s[u] - base);
+                const uint32_t w[4] = {vu[u].x, vu[u].y, vu[u].z, vu[u].w};
+                l[n] += p;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[n][2 * e] += p * bf_lo(w[e]), o[n][2 * e + 1] += p * bf_hi(w[e]);
+            }
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+        if (part == 0) sm[warp * G + g][n] = m[n], sl[warp * G + g][n] = l[n];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) so[warp * G + g][n][part * 8 + e] = o[n][e];
+    }
+    __syncthreads();
+    for (int x = threadIdx.x; x < NQ * D; x += 128) {
+        const int n = x / D, e = x % D;
+        if (n0 + n >= a.p.N) break;
+        float mx = -INFINITY, ls = 0.f, os = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4 * G; ++i) mx = fmaxf(mx, sm[i][n]);
+        const float base = fmaxf(mx, -3.0e38f);
+#pragma unroll
+        for (int i = 0; i < 4 * G; ++i) {
+            const float f = ex2(sm[i][n] - base);
+            ls += sl[i][n] * f;
+            os += so[i][n][e] * f;
+        }
+        const long long bhn = ((long long)b * a.p.H + h) * a.p.N + n0 + n;
+        if (a.splits > 1) {
+            const long long rows = (long long)a.p.B * a.p.H * a.p.N, r = sp * rows + bhn;
+            a.part[r * D + e] = os;
+            if (e == 0) reinterpret_cast<float2 *>(a.part + a.splits * rows * D)[r] = make_float2(base, ls);
+        } else {
+            a.out[(((long long)b * a.p.N + n0 + n) * a.p.H + h) * D + e] = __float2bfloat16_rn(len > 0 ? os / ls : 0.f);
+            if (e == 0 && a.lse) a.lse[bhn] = len > 0 ? (base + __log2f(ls)) * kLn2 : -INFINITY;
+        }
+    }
+}
+
+// out, lse from the pieces, in piece order: D / 4 threads a query.
+template <int D>
+__global__ void __launch_bounds__(256)
+cross_join(const FwdArgs a) {
+    pdl_wait();
+    const long long rows = (long long)a.p.B * a.p.H * a.p.N;
+    const long long x = (long long)blockIdx.x * 256 + threadIdx.x, r = x / (D / 4);
+    const int e = (int)(x % (D / 4));
+    if (r >= rows) return;
+    const float2 *ml = reinterpret_cast<const float2 *>(a.part + a.splits * rows * D);
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s = 0; s < a.splits; ++s)
+        if (ml[s * rows + r].y > 0.f) m = fmaxf(m, ml[s * rows + r].x);     // a piece without states has l = 0
+    for (int s = 0; s < a.splits; ++s) {
+        const float2 p = ml[s * rows + r];
+        if (!(p.y > 0.f)) continue;
+        const float f = ex2(p.x - m);
+        const float4 po = reinterpret_cast<const float4 *>(a.part + (s * rows + r) * D)[e];
+        l += p.y * f;
+        o.x += po.x * f, o.y += po.y * f, o.z += po.z * f, o.w += po.w * f;
+    }
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const int n = (int)(r % a.p.N), h = (int)(r / a.p.N % a.p.H), b = (int)(r / a.p.N / a.p.H);
+    reinterpret_cast<uint2 *>(a.out + (((long long)b * a.p.N + n) * a.p.H + h) * D)[e] =
+        make_uint2(pack_bf2(o.x * inv, o.y * inv), pack_bf2(o.z * inv, o.w * inv));
+    if (e == 0 && a.lse) a.lse[r] = l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
+}
+
+// ---------------------------------------------------------------- host
+
+constexpr int kFew = 8;          // queries up to which the CUDA-core form runs
+
+struct FwdShape {
+    bool few;
+    int nq, pairs, splits;
+    size_t part;
+};
+
+// Queries a CTA of the few-query form, and the pieces along the states: enough
+// items for two CTAs a SM (the few-query form: eight), with at least 4 steps
+// (128 states) each.
+FwdShape fwd_shape(const CrossPlan &p) {
+    FwdShape f{};
+    f.few = p.N <= kFew;
+    f.nq = p.N <= 1 ? 1 : (p.N <= 2 ? 2 : 4);
+    f.pairs = (p.N + 2 * kQT - 1) / (2 * kQT);
+    const long long items = (long long)p.B * p.H * (f.few ? (p.N + f.nq - 1) / f.nq : f.pairs);
+    const int want = (f.few ? 8 : 2) * kSmCount, per = f.few ? 128 : 4 * kKT;
+    long long s = want / items;
+    if (s > p.M / per) s = p.M / per;
+    f.splits = (int)(s < 1 ? 1 : s);
+    f.part = f.splits > 1 ? align256(size_t(f.splits) * p.B * p.H * p.N * (p.d + 2) * sizeof(float)) : 0;
+    return f;
+}
+
+// A [B][rows][H d] tensor with ld elements between rows: boxes of one head's d x box_rows.
+bool head_map(CUtensorMap *m, const void *base, const CrossPlan &p, int rows, long long ld, int box_rows) {
+    const cuuint64_t dims[3] = {(cuuint64_t)p.H * p.d, (cuuint64_t)rows, (cuuint64_t)p.B};
+    const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)ld * 2 * rows};
+    const cuuint32_t box[3] = {(cuuint32_t)p.d, (cuuint32_t)box_rows, 1};
+    return make_dit_map(m, base, 3, dims, strides, box, p.d == 32 ? 64 : 128);
+}
+
+bool g_ready[128] = {};
+bool setup() {
+    return set_smem((const void *)cross_fwd_tc<32>, FC<32>::kSmem) && set_smem((const void *)cross_fwd_tc<64>, FC<64>::kSmem);
+}
+
+template <int D>
+int fwd_t(const void *q, const void *k, const void *v, const FwdShape &f, FwdArgs &a, cudaStream_t s) {
+    using bf = __nv_bfloat16;
+    if (f.few) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)f.splits, (unsigned)(a.p.B * a.p.H), (unsigned)((a.p.N + f.nq - 1) / f.nq));
+        cfg.blockDim = dim3(128);
+        cfg.stream = s;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        auto fn = f.nq == 1 ? cross_few<D, 1> : (f.nq == 2 ? cross_few<D, 2> : cross_few<D, 4>);
+        if (cudaLaunchKernelEx(&cfg, fn, (const bf *)q, (const bf *)k, (const bf *)v, a) != cudaSuccess) return -1;
+    } else {
+        if (!once_per_device(&g_ready, setup)) return -1;
+        CUtensorMap mq, mk, mv;
+        if (!head_map(&mq, q, a.p, a.p.N, (long long)a.p.H * D, kQT) || !head_map(&mk, k, a.p, a.p.M, a.p.ldk, kKT) ||
+            !head_map(&mv, v, a.p, a.p.M, a.p.ldv, kKT))
+            return -1;
+        const int grid = a.items < 2 * kSmCount ? a.items : 2 * kSmCount;
+        if (!launch_pdl(cross_fwd_tc<D>, (unsigned)grid, kThreads, FC<D>::kSmem, s, mq, mk, mv, a)) return -1;
+    }
+    if (f.splits == 1) return 1;
+    const long long x = (long long)a.p.B * a.p.H * a.p.N * (D / 4);
+    return launch_pdl(cross_join<D>, (unsigned)((x + 255) / 256), 256, 0, s, a) ? 2 : -1;
+}
+
+}  // namespace
+
+// (items are counted in ints)
+bool cross_tc_fits(const CrossPlan &p) {
+    return (long long)p.B * p.H * ((p.N + 2 * kQT - 1) / (2 * kQT)) < (1LL << 29) / (2 * kSmCount);
+}
+
+size_t cross_fwd_tc_ws(const CrossPlan &p) { return fwd_shape(p).part; }
+
+int launch_cross_fwd_tc(const void *q, const void *k, const void *v, void *out, float *lse, const CrossPlan &p, void *ws,
+                        cudaStream_t s) {
+    const FwdShape f = fwd_shape(p);
+    FwdArgs a{};
+    a.p = p;
+    a.pairs = f.pairs;
+    a.splits = f.splits;
+    a.items = f.few ? 0 : p.B * p.H * f.pairs * f.splits;
+    a.out = (__nv_bfloat16 *)out;
+    a.lse = lse;
+    a.part = (float *)ws;
+    return p.d == 32 ? fwd_t<32>(q, k, v, f, a, s) : fwd_t<64>(q, k, v, f, a, s);
+}
+
+int read_and_clear_cross_flag(unsigned *flag_out) {
+    if (cudaMemcpyFromSymbol(flag_out, g_cross_flag, sizeof(unsigned)) != cudaSuccess) return -1;
+    const unsigned zero = 0;
+    if (*flag_out && cudaMemcpyToSymbol(g_cross_flag, &zero, sizeof(zero)) != cudaSuccess) return -1;
+    return 0;
+}
+
+}  // namespace la

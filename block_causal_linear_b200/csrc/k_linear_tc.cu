@@ -447,10 +447,15 @@ struct TcPlan {
 // The tile and the cut, by a model of the time in us: whole waves of tiles over
 // the GPU's slots (74 pairs or 148 CTAs), then the tiles that are left, cut
 // along k into pieces that fill the slots (at least 4 stages each), whose sums
-// a second kernel joins.  A tile's time is `us` a stage plus 1.5 to fill and
-// drain; joining costs 4 and the pieces' bytes.
+// a second kernel joins.  `stage` is a stage's time, `tile` what a tile costs
+// beside its stages, `fix` what the launch does, all measured on 13 shapes from
+// 16 x 2048 x 12288 to 8190 x 2048 x 5120: 256 x 256 on a pair wins from about
+// two full waves on (8190 x 2048 x 5120: 110 us, against 128, 138 and 191 for
+// the others), 128 x 64 where that is what fills the SMs (300 x 2048 x 2048:
+// 8.5 us against 15.2, 9.7 and 9.1).  Joining pieces costs 6 and their bytes.
 TcPlan tc_plan(long long M, long long N, long long K) {
-    static const struct { int cg, bn; float us; } kTile[4] = {{2, 256, 0.31f}, {2, 128, 0.19f}, {1, 128, 0.21f}, {1, 64, 0.14f}};
+    static const struct { int cg, bn; float stage, tile, fix; } kTile[4] = {
+        {2, 256, 0.31f, 1.7f, 4.5f}, {2, 128, 0.18f, 0.9f, 3.5f}, {1, 128, 0.18f, 0.9f, 3.f}, {1, 64, 0.155f, 0.4f, 3.f}};
     TcPlan best{};
     float best_us = -1.f;
     for (const auto &k : kTile) {
@@ -461,8 +466,8 @@ TcPlan tc_plan(long long M, long long N, long long K) {
         p.mt = (int)((M + k.cg * kBM - 1) / (k.cg * kBM));
         p.nt = (int)((N + k.bn - 1) / k.bn);
         const long long tiles = (long long)p.mt * p.nt, slots = kSmCount / k.cg, left = tiles % slots;
-        const float whole = p.kiters * k.us + 1.5f;
-        float us = (float)(tiles / slots) * whole + (left ? whole : 0.f);
+        const float whole = p.kiters * k.stage + k.tile;
+        float us = k.fix + (float)(tiles / slots) * whole + (left ? whole : 0.f);
         p.tail = (int)tiles;
         p.splits = 1;
         p.kper = p.kiters;
@@ -472,7 +477,7 @@ TcPlan tc_plan(long long M, long long N, long long K) {
             if (s > 1) {
                 const int kper = (int)((p.kiters + s - 1) / s), pieces = (p.kiters + kper - 1) / kper;
                 const double bytes = (double)left * pieces * k.cg * kBM * k.bn * 4;
-                const float cut = (float)(tiles / slots) * whole + kper * k.us + 1.5f + 4.f + (float)(2 * bytes / 5e6);
+                const float cut = k.fix + (float)(tiles / slots) * whole + kper * k.stage + k.tile + 6.f + (float)(2 * bytes / 5e6);
                 if (cut < us) {
                     us = cut;
                     p.tail = (int)(tiles - left);

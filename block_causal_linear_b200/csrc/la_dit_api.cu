@@ -47,7 +47,7 @@ la_status cross_plan(la::CrossPlan &p, la_dtype dt, int B, int N, int M, int H, 
     p.lddk = ldk; p.lddv = ldv;
     p.kv_len = kv_len;
     p.scale = scale;
-    return LA_OK;
+    return la::cross_tc_fits(p) ? LA_OK : LA_EUNSUPPORTED;
 }
 
 bool ws_ok(const void *ws, size_t have, size_t need) { return ws && have >= need && al256(ws); }
