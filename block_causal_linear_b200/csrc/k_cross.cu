@@ -215,7 +215,8 @@ size_t cross_fwd_ws(int is_bf16, const CrossPlan &p) {
     return n ? n : 256;
 }
 
-size_t cross_bwd_ws(int, const CrossPlan &p) {
+size_t cross_bwd_ws(int is_bf16, const CrossPlan &p) {
+    if (is_bf16) return cross_bwd_tc_ws(p);
     return dkv_part_bytes(p, dkv_splits(p)) + align256(size_t(p.B) * p.H * p.N * sizeof(float));
 }
 
@@ -227,10 +228,7 @@ int launch_cross_fwd(int is_bf16, const void *q, const void *k, const void *v, v
 
 int launch_cross_bwd(int is_bf16, const void *q, const void *k, const void *v, const void *out, const void *dout,
                      const float *lse, void *dq, void *dk, void *dv, const CrossPlan &p, void *ws, cudaStream_t s) {
-    using bf = __nv_bfloat16;
-    if (is_bf16)
-        return p.d == 32 ? bwd_t<bf, 32>(q, k, v, out, dout, lse, dq, dk, dv, p, ws, s)
-                         : bwd_t<bf, 64>(q, k, v, out, dout, lse, dq, dk, dv, p, ws, s);
+    if (is_bf16) return launch_cross_bwd_tc(q, k, v, out, dout, lse, dq, dk, dv, p, ws, s);
     return p.d == 32 ? bwd_t<float, 32>(q, k, v, out, dout, lse, dq, dk, dv, p, ws, s)
                      : bwd_t<float, 64>(q, k, v, out, dout, lse, dq, dk, dv, p, ws, s);
 }

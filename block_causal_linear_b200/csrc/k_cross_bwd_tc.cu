@@ -1,0 +1,628 @@
+// k_cross_bwd_tc.cu -- bf16 cross attention, backward, on the tensor cores.
+//
+//   p_ij = exp(scale q_i . k_j - lse_i),  D_i = dout_i . out_i
+//   dv_j = sum_i p_ij dout_i;  ds_ij = p_ij (dout_i . v_j - D_i)
+//   dq_i = scale sum_j ds_ij k_j;  dk_j = scale sum_i ds_ij q_i
+//
+// Encoder sequences are short and video sequences long, so a CTA keeps one
+// (b, h)'s states (up to 4 tiles of 128 at d = 32, 2 at d = 64) in shared
+// memory and their dk, dv in TMEM, and walks the queries in tiles of 128: each
+// score and its exponential is computed once, and dq of a query tile is whole
+// when its pass over the states ends.  The scores are held transposed, S^T = K
+// Q^T with a state a TMEM lane, 64 queries at a time: P^T and dS^T then are the
+// TMEM operands of dV += P^T dO and dK += dS^T Q as the softmax warps leave
+// them, and only dS goes through shared memory, for dQ += dS K.
+//
+// The call's work, (b, h, group of state tiles) units of all query tiles, is
+// one line of costs cut into equal ranges, one a CTA (lengths are read on the
+// device).  A unit that one CTA finishes is written at once; the others leave
+// fp32 sums that a second kernel joins in CTA order.  More states than a group
+// holds: dq is summed over the groups the same way.
+#include "la_sm100_dit.cuh"
+
+namespace la {
+
+using namespace sm100;
+
+namespace {
+
+// Raised by a bounded wait that gave up; read by la_device_status.
+__device__ unsigned int g_cross_bwd_flag = 0;
+
+constexpr int kT = 128;                     // queries and states a tile
+constexpr int kHalf = 64;                   // queries a step
+constexpr int kThreads = 512;               // 0 TMA, 1 MMA, 4-11 softmax, 12-15 row statistics and dq
+constexpr float kLog2e = 1.4426950408889634f;
+
+template <int D>
+struct BC {
+    static constexpr int G = D == 32 ? 4 : 2;                  // state tiles a group
+    static constexpr int kTile = kT * D * 2;
+    static constexpr int kK = 0, kV = G * kTile;
+    static constexpr int kStage = 3 * kTile, kQ = 2 * G * kTile;   // two stages of q, dout, out
+    static constexpr int kDsBufs = D == 32 ? 2 : 1, kDsBuf = kT * kT * 2;
+    static constexpr int kDs = kQ + 2 * kStage;
+    static constexpr int kStat = kDs + kDsBufs * kDsBuf;       // [2][128] (lse log2 e, D)
+    static constexpr int kBar = kStat + 2 * kT * 8;
+    static constexpr int kBars = 2 + 2 + 2 + 2 + 2 + 2 + 2 + 2 + 2 + 1 + kDsBufs;
+    static constexpr int kSmem = kBar + kBars * 8 + 16 + 64 + 1024;
+    static constexpr uint32_t kLayout = D == 32 ? kLayoutSw64 : kLayoutSw128;
+    static constexpr int kGroup = 8 * D * 2;                   // bytes of 8 rows
+    // TMEM columns
+    static constexpr int kS = 0, kDp = 64, kP = 128, kDsT = 160, kDq = 192, kAcc = 192 + D;   // [tile][dk, dv]
+    static_assert(kAcc + G * 2 * D <= 512, "TMEM");
+    static_assert(kSmem <= 232448, "227 KiB of shared memory");
+};
+
+struct BwdArgs {
+    CrossPlan p;
+    int nq, ng;                      // query tiles, groups of state tiles (of M)
+    __nv_bfloat16 *dq, *dk, *dv;
+    const float *lse;
+    float *part;                     // [CTA][2][G * 128][2 D]: dk, dv of a unit begun earlier (0) or not finished (1)
+    float *dqp;                      // ng > 1: [ng][B][N][H][D]
+};
+
+// One CTA's piece of a unit: query tiles [k0, k1) of (b, h, group g) with kt state tiles.
+struct Seg {
+    int b, h, g, k0, k1, kt, len;
+};
+
+__device__ __forceinline__ int state_tiles(int len) { return (len + kT - 1) / kT; }
+
+// The walk over a CTA's range of the cost line.  A granule (one query tile of
+// a unit) costs its unit's state tiles and belongs to the CTA whose range
+// [ceil(c T / C), ceil((c + 1) T / C)) holds its start.
+template <int G>
+struct Walk {
+    long long o, hi;                 // cost where the next granule starts, the range's end
+    int b, h, g, k, len;
+
+    __device__ __forceinline__ bool next(const BwdArgs &a, Seg &s) {
+        if (o >= hi) return false;
+        const int left = state_tiles(len) - g * G, kt = left < G ? left : G;
+        const long long more = (hi - o + kt - 1) / kt;
+        s = {b, h, g, k, more < a.nq - k ? k + (int)more : a.nq, kt, len};
+        o += (long long)(s.k1 - s.k0) * kt;
+        k = s.k1;
+        if (k == a.nq) unit(a);
+        return true;
+    }
+    // the next unit with states
+    __device__ __forceinline__ void unit(const BwdArgs &a) {
+        k = 0;
+        if (++g * G < state_tiles(len)) return;
+        g = 0;
+        if (++h < a.p.H) return;
+        h = 0;
+        do {
+            if (++b >= a.p.B) {
+                o = hi;
+                return;
+            }
+            len = cross_len(a.p, b);
+        } while (len == 0);
+    }
+};
+
+// Sum of the state tiles of samples [b0, b1), by the whole warp.
+__device__ __forceinline__ long long tiles_of(const CrossPlan &p, int b0, int b1) {
+    long long t = 0;
+    for (int b = b0 + (threadIdx.x & 31); b < b1; b += 32) t += state_tiles(cross_len(p, b));
+#pragma unroll
+    for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    return t;
+}
+
+template <int G>
+__device__ __forceinline__ Walk<G> walk_of(const BwdArgs &a, int c, int C) {
+    const long long per = (long long)a.p.H * a.nq, T = tiles_of(a.p, 0, a.p.B) * per;
+    Walk<G> w{};
+    const long long lo = (c * T + C - 1) / C;
+    w.hi = ((c + 1) * T + C - 1) / C;
+    if (lo >= w.hi) return w.o = w.hi, w;
+    long long base = 0;
+    for (w.b = 0;; ++w.b) {
+        w.len = cross_len(a.p, w.b);
+        const long long n = per * state_tiles(w.len);
+        if (lo < base + n) break;
+        base += n;
+    }
+    const int st = state_tiles(w.len);
+    const long long ph = (long long)a.nq * st;
+    w.h = (int)((lo - base) / ph);
+    base += w.h * ph;
+    w.g = (int)((lo - base) / ((long long)a.nq * G));
+    base += (long long)w.g * a.nq * G;
+    const int left = st - w.g * G, kt = left < G ? left : G;
+    w.k = (int)((lo - base + kt - 1) / kt);
+    w.o = base + (long long)w.k * kt;
+    if (w.k == a.nq) w.unit(a);
+    return w;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+cross_bwd_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
+             const __grid_constant__ CUtensorMap tm_o, const __grid_constant__ CUtensorMap tm_k,
+             const __grid_constant__ CUtensorMap tm_v, const BwdArgs a) {
+    using C = BC<D>;
+    constexpr int G = C::G;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = align1024(smem_raw);
+    uint64_t *q_full = reinterpret_cast<uint64_t *>(smem + C::kBar), *q_empty = q_full + 2, *stat_full = q_empty + 2;
+    uint64_t *sp_full = stat_full + 2, *sp_free = sp_full + 1, *pds_full = sp_free + 1, *pds_free = pds_full + 1;
+    uint64_t *dq_full = pds_free + 1, *dq_free = dq_full + 1, *kv_full = dq_free + 1, *kv_ready = kv_full + 1;
+    uint64_t *kv_empty = kv_ready + 1, *acc_full = kv_empty + 1, *acc_free = acc_full + 1, *fin = acc_free + 1;
+    uint64_t *ds_free = fin + 1;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kBar + C::kBars * 8);
+    volatile int *abort_word = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    const int warp = uniform_warp(), lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 64) {
+        prefetch_tmap(&tm_q);
+        prefetch_tmap(&tm_do);
+        prefetch_tmap(&tm_o);
+        prefetch_tmap(&tm_k);
+        prefetch_tmap(&tm_v);
+    }
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) mbar_init(&q_full[i], 1), mbar_init(&q_empty[i], 1 + 128), mbar_init(&stat_full[i], 128);
+        mbar_init(sp_full, 1), mbar_init(sp_free, 256), mbar_init(pds_full, 256), mbar_init(pds_free, 1);
+        mbar_init(dq_full, 1), mbar_init(dq_free, 128), mbar_init(kv_full, 1), mbar_init(kv_ready, 128);
+        mbar_init(kv_empty, 1), mbar_init(acc_full, 1), mbar_init(acc_free, 256), mbar_init(fin, 1);
+        for (int i = 0; i < C::kDsBufs; ++i) mbar_init(&ds_free[i], 1);
+        *abort_word = 0;
+        fence_barrier_init();
+    }
+    // (before the allocation: a CTA that waited for the previous kernel while it held TMEM could keep that
+    // kernel's own CTAs from theirs)
+    pdl_wait();
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    pdl_trigger();
+    Walk<G> wk = walk_of<G>(a, blockIdx.x, gridDim.x);
+    Seg sg;
+    unsigned *const flag = &g_cross_bwd_flag;
+
+    if (warp == 0) {
+        const bool one = elect_one();
+        int qt = 0, seg = 0;
+        bool ok = true;
+        while (ok && wk.next(a, sg)) {
+            if (!(ok = mbar_poll(kv_empty, (uint32_t)(seg & 1) ^ 1u, abort_word, flag, 1))) break;
+            if (one) {
+                mbar_arrive_expect_tx(kv_full, 2 * sg.kt * C::kTile);
+                for (int j = 0; j < sg.kt; ++j) {
+                    tma_load_3d(smem + C::kK + j * C::kTile, &tm_k, kv_full, sg.h * D, (sg.g * G + j) * kT, sg.b);
+                    tma_load_3d(smem + C::kV + j * C::kTile, &tm_v, kv_full, sg.h * D, (sg.g * G + j) * kT, sg.b);
+                }
+            }
+            ++seg;
+            __syncwarp();
+            for (int k = sg.k0; k < sg.k1; ++k, ++qt) {
+                const int s = qt & 1;
+                if (!(ok = mbar_poll(&q_empty[s], ((uint32_t)(qt >> 1) & 1u) ^ 1u, abort_word, flag, 2))) break;
+                if (one) {
+                    uint8_t *st = smem + C::kQ + s * C::kStage;
+                    mbar_arrive_expect_tx(&q_full[s], C::kStage);
+                    tma_load_3d(st, &tm_q, &q_full[s], sg.h * D, k * kT, sg.b);
+                    tma_load_3d(st + C::kTile, &tm_do, &q_full[s], sg.h * D, k * kT, sg.b);
+                    tma_load_3d(st + 2 * C::kTile, &tm_o, &q_full[s], sg.h * D, k * kT, sg.b);
+                }
+                __syncwarp();
+            }
+        }
+        if (*abort_word && one) {      // let the copies in flight land
+            if (seg > 0) final_wait(kv_full, (uint32_t)(seg - 1) & 1u);
+            for (int k = qt > 2 ? qt - 2 : 0; k < qt; ++k) final_wait(&q_full[k & 1], (uint32_t)(k >> 1) & 1u);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        const bool one = elect_one();
+        const uint32_t id_s = idesc_bf16(kT, kHalf, 0, 0), id_acc = idesc_bf16(kT, D, 0, 1), id_dq = idesc_bf16(kT, D, 1, 1);
+        int qt = 0, seg = 0, steps = 0, tiles = 0;    // steps: halves of (query tile, state tile); tiles: those pairs
+        bool ok = true;
+        // S^T and dP^T of 64 queries (stage s, half hf) against state tile j
+        auto issue_sp = [&](int s, int hf, int j) {
+            const uint32_t st = smem_u32(smem + C::kQ + s * C::kStage) + hf * kHalf * D * 2;
+            const uint64_t dk = smem_desc(smem_u32(smem + C::kK + j * C::kTile), 16, C::kGroup, C::kLayout);
+            const uint64_t dv = smem_desc(smem_u32(smem + C::kV + j * C::kTile), 16, C::kGroup, C::kLayout);
+            const uint64_t dq = smem_desc(st, 16, C::kGroup, C::kLayout), dg = smem_desc(st + C::kTile, 16, C::kGroup, C::kLayout);
+            if (one) {
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) mma_bf16(tmem + C::kS, dk + 2 * kk, dq + 2 * kk, id_s, kk > 0);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) mma_bf16(tmem + C::kDp, dv + 2 * kk, dg + 2 * kk, id_s, kk > 0);
+                mma_commit(sp_full);
+            }
+            __syncwarp();
+        };
+        while (ok && wk.next(a, sg)) {
+            if (!(ok = mbar_poll(kv_ready, (uint32_t)seg & 1u, abort_word, flag, 3))) break;
+            const int n = 2 * sg.kt * (sg.k1 - sg.k0);        // steps of the segment: (query tile, state tile, half)
+            for (int x = 0; x <= n; ++x) {
+                // the next step's scores, as soon as the softmax warps have read the last ones
+                if (x < n) {
+                    const int kq = x / (2 * sg.kt), j = x / 2 % sg.kt, s = (qt + kq) & 1;
+                    if (j == 0 && (x & 1) == 0 &&
+                        !(ok = mbar_poll(&q_full[s], (uint32_t)((qt + kq) >> 1) & 1u, abort_word, flag, 4)))
+                        break;
+                    if (!(ok = mbar_poll(sp_free, (uint32_t)(steps + x) & 1u ^ 1u, abort_word, flag, 5))) break;
+                    tc_fence_after();
+                    issue_sp(s, x & 1, j);
+                }
+                if (x == 0) continue;
+                // the products of the step before
+                const int y = x - 1, kq = y / (2 * sg.kt), j = y / 2 % sg.kt, s = (qt + kq) & 1, hf = y & 1;
+                const bool first = kq == 0;
+                if (y == 0 && !(ok = mbar_poll(acc_free, (uint32_t)seg & 1u ^ 1u, abort_word, flag, 6))) break;
+                if (!(ok = mbar_poll(pds_full, (uint32_t)(steps + y) & 1u, abort_word, flag, 7))) break;
+                tc_fence_after();
+                const uint32_t st = smem_u32(smem + C::kQ + s * C::kStage) + hf * kHalf * D * 2, acc = tmem + C::kAcc + j * 2 * D;
+                const uint64_t dq = smem_desc(st, 8192, C::kGroup, C::kLayout), dg = smem_desc(st + C::kTile, 8192, C::kGroup, C::kLayout);
+                if (one) {
+#pragma unroll
+                    for (int kk = 0; kk < kHalf / 16; ++kk) {
+                        const uint32_t more = !first || hf > 0 || kk > 0;
+                        mma_bf16_ta(acc + D, tmem + C::kP + 8 * kk, dg + kk * (2 * C::kGroup >> 4), id_acc, more);
+                        mma_bf16_ta(acc, tmem + C::kDsT + 8 * kk, dq + kk * (2 * C::kGroup >> 4), id_acc, more);
+                    }
+                    mma_commit(pds_free);
+                }
+                __syncwarp();
+                if (hf == 1) {           // both halves of dS are in shared memory: dQ of the tile
+                    if (j == 0 && !(ok = mbar_poll(dq_free, (uint32_t)(qt + kq) & 1u ^ 1u, abort_word, flag, 8))) break;
+                    tc_fence_after();
+                    const int buf = tiles % C::kDsBufs;
+                    const uint64_t ds = smem_desc(smem_u32(smem + C::kDs + buf * C::kDsBuf), C::kDsBuf / 2, 1024, kLayoutSw128);
+                    const uint64_t dk = smem_desc(smem_u32(smem + C::kK + j * C::kTile), 8192, C::kGroup, C::kLayout);
+                    if (one) {
+#pragma unroll
+                        for (int kk = 0; kk < kT / 16; ++kk)
+                            mma_bf16(tmem + C::kDq, ds + kk * (2048 >> 4), dk + kk * (2 * C::kGroup >> 4), id_dq, j > 0 || kk > 0);
+                        mma_commit(&ds_free[buf]);
+                        if (j + 1 == sg.kt) {
+                            mma_commit(dq_full);
+                            mma_commit(&q_empty[s]);
+                        }
+                    }
+                    ++tiles;
+                    __syncwarp();
+                }
+            }
+            if (ok && one) {
+                mma_commit(acc_full);
+                mma_commit(kv_empty);
+            }
+            __syncwarp();
+            qt += sg.k1 - sg.k0;
+            steps += n;
+            ++seg;
+        }
+        if (*abort_word && one) {
+            mma_commit(fin);
+            final_wait(fin, 0);
+        }
+        __syncwarp();
+    } else if (warp >= 12) {
+        // a thread a query: (lse, D) of the tile for the softmax warps; dq at its end
+        const int r = threadIdx.x - 384, q = warp & 3;
+        int qt = 0, seg = 0;
+        bool ok = true;
+        float2 *stat = reinterpret_cast<float2 *>(smem + C::kStat);
+        while (ok && wk.next(a, sg)) {
+            if (!(ok = mbar_poll(kv_full, (uint32_t)seg & 1u, abort_word, flag, 9))) break;
+            const int lim = sg.len - (sg.g * G + sg.kt - 1) * kT;      // valid rows of the last state tile
+            if (lim < kT) {              // zeros behind the length: ds is 0 there, but 0 * NaN would reach dq
+                uint4 *k = reinterpret_cast<uint4 *>(smem + C::kK + (sg.kt - 1) * C::kTile + lim * D * 2);
+                for (int e = r; e < (kT - lim) * (D / 8); e += 128) k[e] = make_uint4(0, 0, 0, 0);
+                fence_proxy_async_smem();
+            }
+            mbar_arrive(kv_ready);
+            ++seg;
+            const long long bh = ((long long)sg.b * a.p.H + sg.h) * a.p.N;
+            auto stats = [&](int k, int t) {     // of query tile k, the t-th of this CTA
+                const int i = k * kT + r;
+                // a row behind the last query: p = exp2(0 - inf) = 0
+                const float ls = i < a.p.N ? a.lse[bh + i] * kLog2e : INFINITY;
+                if (!mbar_poll(&q_full[t & 1], (uint32_t)(t >> 1) & 1u, abort_word, flag, 10)) return false;
+                const uint8_t *st = smem + C::kQ + (t & 1) * C::kStage;
+                float d = 0.f;
+#pragma unroll
+                for (int ch = 0; ch < D / 8; ++ch) {
+                    const int off = D == 32 ? r * 64 + ((ch ^ ((r >> 1) & 3)) << 4) : r * 128 + ((ch ^ (r & 7)) << 4);
+                    const uint4 x = *reinterpret_cast<const uint4 *>(st + C::kTile + off);
+                    const uint4 y = *reinterpret_cast<const uint4 *>(st + 2 * C::kTile + off);
+                    const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) d += bf_lo(xw[e]) * bf_lo(yw[e]) + bf_hi(xw[e]) * bf_hi(yw[e]);
+                }
+                stat[(t & 1) * kT + r] = make_float2(ls, d);
+                mbar_arrive(&stat_full[t & 1]);
+                mbar_arrive(&q_empty[t & 1]);
+                return true;
+            };
+            if (!(ok = stats(sg.k0, qt))) break;
+            for (int k = sg.k0; k < sg.k1; ++k, ++qt) {
+                if (k + 1 < sg.k1 && !(ok = stats(k + 1, qt + 1))) break;
+                if (!(ok = mbar_poll(dq_full, (uint32_t)qt & 1u, abort_word, flag, 11))) break;
+                tc_fence_after();
+                __syncwarp();
+                const int i = k * kT + r;
+#pragma unroll 1
+                for (int hh = 0; hh < D / 32; ++hh) {
+                    float o[32];
+                    tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + C::kDq + 32 * hh, o);
+                    tmem_wait_ld();
+                    if (hh + 1 == D / 32) {
+                        tc_fence_before();
+                        mbar_arrive(dq_free);
+                    }
+                    if (i < a.p.N) {
+                    const long long at = (((long long)sg.b * a.p.N + i) * a.p.H + sg.h) * D + 32 * hh;
+                    if (a.ng > 1) {
+                        float4 *to = reinterpret_cast<float4 *>(a.dqp + (long long)sg.g * a.p.B * a.p.N * a.p.H * D + at);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) to[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                    } else {
+                        const float sc = a.p.scale;
+                        uint4 *to = reinterpret_cast<uint4 *>(a.dq + at);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            to[e] = make_uint4(pack_bf2(o[8 * e] * sc, o[8 * e + 1] * sc), pack_bf2(o[8 * e + 2] * sc, o[8 * e + 3] * sc),
+                                               pack_bf2(o[8 * e + 4] * sc, o[8 * e + 5] * sc), pack_bf2(o[8 * e + 6] * sc, o[8 * e + 7] * sc));
+                    }
+                    }
+                    __syncwarp();
+                }
+            }
+        }
+    } else if (warp >= 4) {
+        // a thread a state and 32 of the step's 64 queries
+        const int q = warp & 3, wg = (warp - 4) >> 2, r = q * 32 + lane;
+        const uint32_t tl = tmem + ((uint32_t)(q * 32) << 16);
+        const float c = a.p.scale * kLog2e;
+        int qt = 0, seg = 0, steps = 0, tiles = 0;
+        bool ok = true;
+        while (ok && wk.next(a, sg)) {
+            for (int k = sg.k0; ok && k < sg.k1; ++k, ++qt) {
+                if (!(ok = mbar_poll(&stat_full[qt & 1], (uint32_t)(qt >> 1) & 1u, abort_word, flag, 12))) break;
+                for (int j = 0; ok && j < sg.kt; ++j, ++tiles) {
+                    const bool valid = (sg.g * G + j) * kT + r < sg.len;
+                    const int buf = tiles % C::kDsBufs;
+                    if (!(ok = mbar_poll(&ds_free[buf], ((uint32_t)(tiles / C::kDsBufs) & 1u) ^ 1u, abort_word, flag, 13))) break;
+                    for (int hf = 0; hf < 2; ++hf, ++steps) {
+                        if (!(ok = mbar_poll(sp_full, (uint32_t)steps & 1u, abort_word, flag, 14))) break;
+                        tc_fence_after();
+                        __syncwarp();
+                        float s[32], dp[32];
+                        tmem_ld32(tl + C::kS + wg * 32, s);
+                        tmem_ld32(tl + C::kDp + wg * 32, dp);
+                        tmem_wait_ld();
+                        tc_fence_before();
+                        mbar_arrive(sp_free);
+                        const float4 *st = reinterpret_cast<const float4 *>(smem + C::kStat + ((qt & 1) * kT + hf * kHalf + wg * 32) * 8);
+                        uint32_t pk[16], dk[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const float4 t = st[e];                    // (lse, D) of two queries
+                            float p0 = ex2(fmaf(s[2 * e], c, -t.x)), p1 = ex2(fmaf(s[2 * e + 1], c, -t.z));
+                            float d0 = p0 * (dp[2 * e] - t.y), d1 = p1 * (dp[2 * e + 1] - t.w);
+                            pk[e] = valid ? pack_bf2(p0, p1) : 0u;     // a state behind the length may hold NaN
+                            dk[e] = valid ? pack_bf2(d0, d1) : 0u;
+                        }
+                        if (!(ok = mbar_poll(pds_free, (uint32_t)steps & 1u ^ 1u, abort_word, flag, 15))) break;
+                        tc_fence_after();
+                        __syncwarp();
+                        tmem_st16(tl + C::kP + wg * 16, pk);
+                        tmem_st16(tl + C::kDsT + wg * 16, dk);
+                        uint8_t *ds = smem + C::kDs + buf * C::kDsBuf + hf * (C::kDsBuf / 2) + r * 128;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            *reinterpret_cast<uint4 *>(ds + (((wg * 4 + e) ^ (r & 7)) << 4)) =
+                                make_uint4(dk[4 * e], dk[4 * e + 1], dk[4 * e + 2], dk[4 * e + 3]);
+                        fence_proxy_async_smem();
+                        tmem_wait_st();
+                        tc_fence_before();
+                        mbar_arrive(pds_full);
+                    }
+                }
+            }
+            if (!ok) break;
+            // dk (first four warps) and dv of the segment's states
+            if (!(ok = mbar_poll(acc_full, (uint32_t)seg & 1u, abort_word, flag, 16))) break;
+            ++seg;
+            tc_fence_after();
+            __syncwarp();
+            const bool whole = sg.k0 == 0 && sg.k1 == a.nq;
+            const float sc = wg == 0 ? a.p.scale : 1.f;
+            for (int j = 0; j < sg.kt; ++j) {
+                const int m = (sg.g * G + j) * kT + r;
+#pragma unroll 1
+                for (int hh = 0; hh < D / 32; ++hh) {
+                    float o[32];
+                    tmem_ld32(tl + C::kAcc + j * 2 * D + wg * D + 32 * hh, o);
+                    tmem_wait_ld();
+                    if (m < sg.len && whole) {
+                        __nv_bfloat16 *to = wg == 0 ? a.dk + ((long long)sg.b * a.p.M + m) * a.p.lddk : a.dv + ((long long)sg.b * a.p.M + m) * a.p.lddv;
+                        uint4 *t4 = reinterpret_cast<uint4 *>(to + sg.h * D + 32 * hh);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            t4[e] = make_uint4(pack_bf2(o[8 * e] * sc, o[8 * e + 1] * sc), pack_bf2(o[8 * e + 2] * sc, o[8 * e + 3] * sc),
+                                               pack_bf2(o[8 * e + 4] * sc, o[8 * e + 5] * sc), pack_bf2(o[8 * e + 6] * sc, o[8 * e + 7] * sc));
+                    } else if (m < sg.len) {
+                        float *to = a.part + (((long long)blockIdx.x * 2 + (sg.k0 == 0)) * (G * kT) + j * kT + r) * 2 * D + wg * D + 32 * hh;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            reinterpret_cast<float4 *>(to)[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                    }
+                    __syncwarp();
+                }
+            }
+            tc_fence_before();
+            mbar_arrive(acc_free);
+        }
+    }
+    __syncwarp();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// dk, dv of the units that more than one CTA worked on, from their sums in CTA
+// order; zeros behind a sample's length, and zero dq where there are no states.
+// One CTA a (b, h, 128 states).
+template <int D>
+__global__ void __launch_bounds__(256)
+cross_bwd_join(const BwdArgs a, int C) {
+    constexpr int G = BC<D>::G;
+    pdl_wait();
+    const int jt = blockIdx.x, h = blockIdx.y % a.p.H, b = blockIdx.y / a.p.H, g = jt / G;
+    const int len = cross_len(a.p, b), st = state_tiles(len);
+    if (len == 0 && jt == 0)
+        for (long long e = threadIdx.x; e < (long long)a.p.N * (D / 8); e += 256)
+            *reinterpret_cast<uint4 *>(a.dq + (((long long)b * a.p.N + e / (D / 8)) * a.p.H + h) * D + e % (D / 8) * 8) =
+                make_uint4(0, 0, 0, 0);
+    // the CTAs [c0, c1] whose ranges hold the unit's granules
+    long long c0 = 0, c1 = -1, T = 1, base = 0;
+    int kt = 1;
+    if (jt < st) {
+        const long long per = (long long)a.p.H * a.nq;
+        T = tiles_of(a.p, 0, a.p.B) * per;
+        base = tiles_of(a.p, 0, b) * per + ((long long)h * st + g * G) * a.nq;
+        kt = st - g * G < G ? st - g * G : G;
+        c0 = base * C / T;
+        c1 = (base + (long long)(a.nq - 1) * kt) * C / T;
+    }
+    const bool whole = jt < st && c0 == c1;      // written by that CTA, but for the rows behind the length
+    auto granules = [&](long long c) {   // whether CTA c has granules of the unit
+        const long long lo = (c * T + C - 1) / C, hi = ((c + 1) * T + C - 1) / C;
+        const long long k = lo <= base ? 0 : (lo - base + kt - 1) / kt;
+        return k < a.nq && base + k * kt < hi;
+    };
+    for (int e = threadIdx.x; e < kT * (2 * D / 4); e += 256) {
+        const int row = e / (D / 2), f = e % (D / 2) * 4, m = jt * kT + row;
+        if (m >= a.p.M) break;
+        if (whole && m < len) continue;
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (m < len)
+            for (long long c = c0; c <= c1; ++c) {
+                if (c > c0 && !granules(c)) continue;
+                const float4 x = *reinterpret_cast<const float4 *>(
+                    a.part + ((c * 2 + (c == c0)) * (G * kT) + (jt - g * G) * kT + row) * 2 * D + f);
+                s.x += x.x, s.y += x.y, s.z += x.z, s.w += x.w;
+            }
+        const float sc = f < D ? a.p.scale : 1.f;
+        __nv_bfloat16 *to = f < D ? a.dk + ((long long)b * a.p.M + m) * a.p.lddk + h * D + f
+                                  : a.dv + ((long long)b * a.p.M + m) * a.p.lddv + h * D + f - D;
+        *reinterpret_cast<uint2 *>(to) = make_uint2(pack_bf2(s.x * sc, s.y * sc), pack_bf2(s.z * sc, s.w * sc));
+    }
+}
+
+// dq from the groups' sums, in group order.
+template <int D>
+__global__ void __launch_bounds__(256)
+cross_dq_join(const BwdArgs a) {
+    pdl_wait();
+    const long long n = (long long)a.p.B * a.p.N * a.p.H * D, per = n / a.p.B;
+    for (long long e = ((long long)blockIdx.x * 256 + threadIdx.x) * 4; e < n; e += (long long)gridDim.x * 1024) {
+        const int groups = (state_tiles(cross_len(a.p, (int)(e / per))) + BC<D>::G - 1) / BC<D>::G;
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int g = 0; g < groups; ++g) {
+            const float4 x = *reinterpret_cast<const float4 *>(a.dqp + g * n + e);
+            s.x += x.x, s.y += x.y, s.z += x.z, s.w += x.w;
+        }
+        const float sc = a.p.scale;
+        *reinterpret_cast<uint2 *>(a.dq + e) = make_uint2(pack_bf2(s.x * sc, s.y * sc), pack_bf2(s.z * sc, s.w * sc));
+    }
+}
+
+// ---------------------------------------------------------------- host
+
+int groups_of(const CrossPlan &p) { return (p.M + kT * (p.d == 32 ? 4 : 2) - 1) / (kT * (p.d == 32 ? 4 : 2)); }
+
+struct BwdWs {
+    size_t dqp, total;
+};
+BwdWs bwd_ws(const CrossPlan &p) {
+    BwdWs w;
+    const int G = p.d == 32 ? 4 : 2;
+    w.dqp = align256(size_t(kSmCount) * 2 * G * kT * 2 * p.d * sizeof(float));
+    const int ng = groups_of(p);
+    w.total = w.dqp + (ng > 1 ? align256(size_t(ng) * p.B * p.N * p.H * p.d * sizeof(float)) : 0);
+    return w;
+}
+
+bool head_map(CUtensorMap *m, const void *base, const CrossPlan &p, int rows, long long ld) {
+    const cuuint64_t dims[3] = {(cuuint64_t)p.H * p.d, (cuuint64_t)rows, (cuuint64_t)p.B};
+    const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)ld * 2 * rows};
+    const cuuint32_t box[3] = {(cuuint32_t)p.d, (cuuint32_t)kT, 1};
+    return make_dit_map(m, base, 3, dims, strides, box, p.d == 32 ? 64 : 128);
+}
+
+bool g_ready[128] = {};
+bool setup() {
+    return set_smem((const void *)cross_bwd_tc<32>, BC<32>::kSmem) && set_smem((const void *)cross_bwd_tc<64>, BC<64>::kSmem);
+}
+
+template <int D>
+int bwd_t(const void *q, const void *k, const void *v, const void *out, const void *dout, const BwdArgs &a, cudaStream_t s) {
+    if (!once_per_device(&g_ready, setup)) return -1;
+    const long long ld = (long long)a.p.H * D;
+    CUtensorMap mq, mg, mo, mk, mv;
+    if (!head_map(&mq, q, a.p, a.p.N, ld) || !head_map(&mg, dout, a.p, a.p.N, ld) || !head_map(&mo, out, a.p, a.p.N, ld) ||
+        !head_map(&mk, k, a.p, a.p.M, a.p.ldk) || !head_map(&mv, v, a.p, a.p.M, a.p.ldv))
+        return -1;
+    const long long granules = (long long)a.p.B * a.p.H * a.ng * a.nq;
+    const int grid = granules < kSmCount ? (int)granules : kSmCount;
+    if (!launch_pdl(cross_bwd_tc<D>, (unsigned)grid, kThreads, BC<D>::kSmem, s, mq, mg, mo, mk, mv, a)) return -1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((a.p.M + kT - 1) / kT), (unsigned)(a.p.B * a.p.H));
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, cross_bwd_join<D>, a, grid) != cudaSuccess) return -1;
+    if (a.ng == 1) return 2;
+    return launch_pdl(cross_dq_join<D>, 8 * kSmCount, 256, 0, s, a) ? 3 : -1;
+}
+
+}  // namespace
+
+size_t cross_bwd_tc_ws(const CrossPlan &p) { return bwd_ws(p).total; }
+
+int launch_cross_bwd_tc(const void *q, const void *k, const void *v, const void *out, const void *dout, const float *lse,
+                        void *dq, void *dk, void *dv, const CrossPlan &p, void *ws, cudaStream_t s) {
+    BwdArgs a{};
+    a.p = p;
+    a.nq = (p.N + kT - 1) / kT;
+    a.ng = groups_of(p);
+    a.dq = (__nv_bfloat16 *)dq;
+    a.dk = (__nv_bfloat16 *)dk;
+    a.dv = (__nv_bfloat16 *)dv;
+    a.lse = lse;
+    a.part = (float *)ws;
+    a.dqp = (float *)((char *)ws + bwd_ws(p).dqp);
+    return p.d == 32 ? bwd_t<32>(q, k, v, out, dout, a, s) : bwd_t<64>(q, k, v, out, dout, a, s);
+}
+
+int read_and_clear_cross_bwd_flag(unsigned *flag_out) {
+    if (cudaMemcpyFromSymbol(flag_out, g_cross_bwd_flag, sizeof(unsigned)) != cudaSuccess) return -1;
+    const unsigned zero = 0;
+    if (*flag_out && cudaMemcpyToSymbol(g_cross_bwd_flag, &zero, sizeof(zero)) != cudaSuccess) return -1;
+    return 0;
+}
+
+}  // namespace la

@@ -118,6 +118,9 @@ cross_fwd_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         *abort_word = 0;
         fence_barrier_init();
     }
+    // (before the allocation: a CTA that waited for the previous kernel while it held TMEM could keep that
+    // kernel's own CTAs from theirs)
+    pdl_wait();
     if (warp == 1) {
         tmem_alloc(tmem_slot, 256);
         tmem_relinquish();
@@ -126,7 +129,6 @@ cross_fwd_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;     // stream t: S and P at 128 t, O at 128 t + 64
-    pdl_wait();
     pdl_trigger();
     int last_b = -1, last_len = 0;
 

@@ -146,6 +146,9 @@ gemm_tc(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtens
         *abort_word = 0;
         fence_barrier_init();
     }
+    // (before the allocation: a CTA that waited for the previous kernel while it held TMEM could keep that
+    // kernel's own CTAs from theirs)
+    pdl_wait();
     if (warp == 1) {
         if constexpr (CG == 2) {
             tmem_alloc_pair(tmem_slot, C::kTmem);
@@ -159,7 +162,6 @@ gemm_tc(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtens
     if constexpr (CG == 2) cluster_sync();   // the pair's barriers are set up
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    pdl_wait();      // everything above overlaps the previous kernel's end
     pdl_trigger();
     int issued = 0;   // stages filled (warp 0) or read (warp 1)
     int tiles = 0;    // tiles accumulated (warp 1)

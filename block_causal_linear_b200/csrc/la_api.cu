@@ -593,15 +593,15 @@ la_status la_block_apply(const void *q, void *out, la_dtype dt, int B, int N_sli
 }
 
 la_status la_device_status(void *stream) {
-    unsigned flag = 0, fk = 0, fq = 0, fc = 0, fr = 0, fl = 0, fn = 0, fx = 0;
+    unsigned flag = 0, fk = 0, fq = 0, fc = 0, fr = 0, fl = 0, fn = 0, fx = 0, fy = 0;
     // (synchronises the stream first)
     if (la::read_and_clear_device_flag(static_cast<cudaStream_t>(stream), &flag) != 0) return LA_ECUDA;
     if (la::read_and_clear_bwd_k_flag(&fk) != 0 || la::read_and_clear_bwd_q_flag(&fq) != 0 ||
         la::read_and_clear_conv_flag(&fc) != 0 || la::read_and_clear_rope_flag(&fr) != 0 ||
         la::read_and_clear_linear_flag(&fl) != 0 || la::read_and_clear_norm_flag(&fn) != 0 ||
-        la::read_and_clear_cross_flag(&fx) != 0)
+        la::read_and_clear_cross_flag(&fx) != 0 || la::read_and_clear_cross_bwd_flag(&fy) != 0)
         return LA_ECUDA;
-    return (flag | fk | fq | fc | fr | fl | fn | fx) ? LA_ETIMEOUT : LA_OK;
+    return (flag | fk | fq | fc | fr | fl | fn | fx | fy) ? LA_ETIMEOUT : LA_OK;
 }
 
 la_status la_selftest_bounded_wait(void *stream) {

@@ -115,6 +115,10 @@ size_t cross_fwd_tc_ws(const CrossPlan &p);
 int launch_cross_fwd_tc(const void *q, const void *k, const void *v, void *out, float *lse, const CrossPlan &p, void *ws,
                         cudaStream_t s);
 int read_and_clear_cross_flag(unsigned *flag_out);
+size_t cross_bwd_tc_ws(const CrossPlan &p);
+int launch_cross_bwd_tc(const void *q, const void *k, const void *v, const void *out, const void *dout, const float *lse,
+                        void *dq, void *dk, void *dv, const CrossPlan &p, void *ws, cudaStream_t s);
+int read_and_clear_cross_bwd_flag(unsigned *flag_out);
 size_t cross_fwd_ws(int is_bf16, const CrossPlan &p);
 size_t cross_bwd_ws(int is_bf16, const CrossPlan &p);
 int launch_cross_fwd(int is_bf16, const void *q, const void *k, const void *v, void *out, float *lse,

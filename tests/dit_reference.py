@@ -136,6 +136,9 @@ def linear_backward(dy, x, w, pre, name, dtype):
 
 # exponentials: in bf16 calls, whose p is rounded to 2^-8 anyway, an approximation of 2^-12 is allowed
 EXP_REL = {torch.bfloat16: 2.0 ** -12, torch.float32: 2.0 ** -20}
+# what fp32's smallest normal number bounds: a p (or ds) below it may become zero, which is off by less than 2^-126
+# in that term whatever its relative error (p = 1e-38 times dp - D = 10 and q = 4 misses 4e-37 of dk that way)
+FLUSH = 2.0 ** -126
 
 
 def _heads(t):
@@ -165,7 +168,7 @@ def cross_forward(q, k, v, lens, scale, dtype):
         rel = 2 * e + EXP_REL[dtype] * 2 + (n + 8) * U
         outs.append(p @ vv)
         ph = half(torch.bfloat16) if dtype == torch.bfloat16 else 0.0
-        so.append((rel + ph) * (p @ vv.abs()))
+        so.append((rel + ph) * (p @ vv.abs()) + FLUSH * vv.abs().sum(-2, keepdim=True))
         lses.append(torch.logsumexp(s, -1))
         sl.append((e + EXP_REL[dtype] + (n + 8) * U)[..., 0] + 4 * U * lses[-1].abs())
     st = [torch.stack(t) for t in (outs, lses, so, sl)]
@@ -188,12 +191,12 @@ def cross_backward(q, k, v, out, lse, dout, lens, scale, dtype):
         s = scale * (Q @ T(K))
         es = scale * (d + 4) * U * (Q.abs() @ T(K.abs())) + 4 * U * (s.abs() + lse[b].double()[..., None].abs())
         p = torch.exp(s - lse[b].double()[..., None])
-        ep = p * (es + EXP_REL[dtype])
+        ep = p * (es + EXP_REL[dtype]) + FLUSH
         dp, D = G @ T(V), (G * oh[b]).sum(-1, keepdim=True)
         eD = (d + 4) * U * (G * oh[b]).abs().sum(-1, keepdim=True)
         edp = (d + 4) * U * (G.abs() @ T(V.abs()))
         ds = p * (dp - D)
-        eds = ep * (dp - D).abs() + p * (edp + eD + U * (dp.abs() + D.abs())) + (ph + 2 * U) * ds.abs()
+        eds = ep * (dp - D).abs() + p * (edp + eD + U * (dp.abs() + D.abs())) + (ph + 2 * U) * ds.abs() + FLUSH
         epr = ep + ph * p
         res[0][0][b] = scale * (ds @ K)
         res[0][1][b] = scale * (eds @ K.abs() + (n + 8) * U * (ds.abs() @ K.abs()))
