@@ -3,14 +3,16 @@
 //
 //   s_j = scale q . k_j over the valid states j < len;  p = softmax(s);  o = sum p_j v_j
 //
-// One CTA (two a SM) carries two streams, each a tile of 128 queries of one
-// (b, h), through the states in tiles of 64: S = Q K^T into TMEM, the softmax
-// warps (a thread a query) turn it into P = exp2(c s - m) in bf16 over the same
-// columns, O += P V takes P from TMEM.  The maximum m in use moves, and O in
-// TMEM is rescaled, only when a row's maximum outgrows it by 2^8: P is then at
-// most 256, which costs bf16 and the fp32 sum no precision.  Heads are 32 or 64
-// wide, so the exponentials (16 a clock and SM) bound it, not the products or
-// HBM: the streams of a SM overlap so that some warp always has exponentials.
+// One CTA a SM carries 3 (d = 32) or 2 (d = 64) streams, each a tile of 128
+// queries of one (b, h), through the states in steps of 64: S = Q K^T into
+// TMEM, the stream's softmax warps (a thread a query) turn it into P = exp2(c s
+// - m) in bf16 over the same columns, O += P V takes P from TMEM.  S has two
+// buffers a stream, so a stream's next scores are there when it has finished
+// the last.  The maximum m in use moves, and O in TMEM is rescaled, only when a
+// row's maximum outgrows it by 2^8: P is then at most 256, which costs bf16 and
+// the fp32 sum no precision.  Heads are 32 or 64 wide, so the exponentials (16
+// a clock and SM) bound it, not the products or HBM; a quarter of them runs on
+// the FMA pipe instead.
 //
 // Few queries against many states are cut along the states into pieces whose
 // unnormalised sums a second kernel joins.
@@ -26,26 +28,29 @@ namespace {
 __device__ unsigned int g_cross_flag = 0;
 
 constexpr int kQT = 128, kKT = 64;         // queries a stream's tile, states a step
-constexpr int kThreads = 64 + 256;         // TMA warp, MMA warp, 2 x 4 softmax warps
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kGrow = 8.f;               // log2 of the growth that moves the maximum in use
 
 template <int D>
 struct FC {
+    static constexpr int kStreams = D == 32 ? 3 : 2;
+    static constexpr int kThreads = 32 + 160 * kStreams;       // TMA warp, an MMA warp and 4 softmax warps a stream
     static constexpr int kQ = kQT * D * 2, kKV = kKT * D * 2, kStage = 2 * kKV;
-    static constexpr int kStages = D == 32 ? 4 : 2;
-    static constexpr int kRing = 4 * kQ;                       // [stream][buffer] query tiles first
+    static constexpr int kStages = D == 32 ? 8 : 6;
+    static constexpr int kRing = 2 * kStreams * kQ;            // [stream][buffer] query tiles first
     static constexpr int kBar = kRing + kStages * kStage;
-    // q_full[2][2], q_empty[2][2], kv_full, kv_empty, r[2], p[2], fin
-    static constexpr int kBars = 8 + 2 * kStages + 5;
+    static constexpr int kBars = 11 * kStreams + 2 * kStages;
     static constexpr int kSmem = kBar + kBars * 8 + 16 + 1024;
     static constexpr uint32_t kLayout = D == 32 ? kLayoutSw64 : kLayoutSw128;
     static constexpr int kGroup = 8 * D * 2;                   // bytes of 8 rows
+    static constexpr int kCols = 2 * kKT + D;                  // TMEM a stream: S and P twice, O
+    static_assert(kStreams * kCols <= 512, "TMEM");
+    static_assert(kSmem <= 232448, "227 KiB of shared memory");
 };
 
 struct FwdArgs {
     CrossPlan p;
-    int pairs, items;        // query tile pairs a (b, h); items = B * H * pairs * splits
+    int groups, items;       // groups of query tiles (one a stream) of a (b, h); items = B * H * groups * splits
     int splits;              // pieces along the states (in whole steps)
     __nv_bfloat16 *out;
     float *lse;
@@ -53,14 +58,14 @@ struct FwdArgs {
 };
 
 struct Item {
-    int b, h, pair, j0, j1, len;
+    int b, h, group, j0, j1, len;
 };
 
 // Item w, its sample's length kept from the last item where the sample is the same.
 __device__ __forceinline__ Item item_of(const FwdArgs &a, int w, int &last_b, int &last_len) {
     Item i;
-    i.pair = w % a.pairs;
-    int r = w / a.pairs;
+    i.group = w % a.groups;
+    int r = w / a.groups;
     const int sp = r % a.splits;
     r /= a.splits;
     i.h = r % a.p.H;
@@ -85,23 +90,24 @@ __device__ __forceinline__ void exp_half(const float (&s)[32], uint32_t *pk, flo
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
         const float2 x = ffma2(make_float2(s[2 * e], s[2 * e + 1]), make_float2(c, c), make_float2(-m, -m));
-        const float2 p = make_float2(ex2(x.x), ex2(x.y));
-        sum.x += p.x;
-        sum.y += p.y;
+        const float2 p = e % 4 == 3 ? ex2_fma(x) : make_float2(ex2(x.x), ex2(x.y));
+        sum = fadd2(sum, p);
         pk[e] = pack_bf2(p.x, p.y);
     }
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(FC<D>::kThreads, 1)
 cross_fwd_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
              const __grid_constant__ CUtensorMap tm_v, const FwdArgs a) {
     using C = FC<D>;
+    constexpr int NS = C::kStreams;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = align1024(smem_raw);
-    uint64_t *q_full = reinterpret_cast<uint64_t *>(smem + C::kBar), *q_empty = q_full + 4;
-    uint64_t *kv_full = q_empty + 4, *kv_empty = kv_full + C::kStages, *rb = kv_empty + C::kStages, *pb = rb + 2, *fin = pb + 2;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(fin + 1);
+    // per stream: q_full[2], q_empty[2], sb[2] (S is there), pb[2] (P is there), ob[2] (P V is added)
+    uint64_t *q_full = reinterpret_cast<uint64_t *>(smem + C::kBar), *q_empty = q_full + 2 * NS, *sb = q_empty + 2 * NS;
+    uint64_t *pb = sb + 2 * NS, *ob = pb + 2 * NS, *kv_full = ob + 2 * NS, *kv_empty = kv_full + C::kStages, *fin = kv_empty + C::kStages;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(fin + NS);
     volatile int *abort_word = reinterpret_cast<volatile int *>(tmem_slot + 1);
     const int warp = uniform_warp(), lane = threadIdx.x & 31;
 
@@ -111,10 +117,9 @@ cross_fwd_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         prefetch_tmap(&tm_v);
     }
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 4; ++i) mbar_init(&q_full[i], 1), mbar_init(&q_empty[i], 1);
-        for (int i = 0; i < C::kStages; ++i) mbar_init(&kv_full[i], 1), mbar_init(&kv_empty[i], 1);
-        for (int i = 0; i < 2; ++i) mbar_init(&rb[i], 1), mbar_init(&pb[i], 128);
-        mbar_init(fin, 1);
+        for (int i = 0; i < 2 * NS; ++i) mbar_init(&q_full[i], 1), mbar_init(&q_empty[i], 1), mbar_init(&sb[i], 1), mbar_init(&pb[i], 128), mbar_init(&ob[i], 1);
+        for (int i = 0; i < C::kStages; ++i) mbar_init(&kv_full[i], 1), mbar_init(&kv_empty[i], NS);
+        for (int i = 0; i < NS; ++i) mbar_init(&fin[i], 1);
         *abort_word = 0;
         fence_barrier_init();
     }
@@ -122,167 +127,190 @@ cross_fwd_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
     // kernel's own CTAs from theirs)
     pdl_wait();
     if (warp == 1) {
-        tmem_alloc(tmem_slot, 256);
+        tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;     // stream t: S and P at 128 t, O at 128 t + 64
+    const uint32_t tmem = *tmem_slot;     // stream t from column kCols t: S and P at 0 and 64, O at 128
     pdl_trigger();
     int last_b = -1, last_len = 0;
+    unsigned *const flag = &g_cross_flag;
 
     if (warp == 0) {
         const bool one = elect_one();
-        int kv = 0, uses[2] = {0, 0};
+        int kv = 0, uses[NS] = {};
         bool ok = true;
         for (int w = blockIdx.x; ok && w < a.items; w += gridDim.x) {
             const Item i = item_of(a, w, last_b, last_len);
             if (i.j0 == i.j1) continue;
-            for (int t = 0; ok && t < 2; ++t) {
-                const int q0 = (2 * i.pair + t) * kQT;
-                if (q0 >= a.p.N) break;
+            auto load_q = [&](int t) {
+                const int q0 = (NS * i.group + t) * kQT;
+                if (q0 >= a.p.N || !ok) return;
                 const int s = 2 * t + (uses[t] & 1);
-                if (!(ok = mbar_poll(&q_empty[s], ((uint32_t)(uses[t] >> 1) & 1u) ^ 1u, abort_word, &g_cross_flag, 1))) break;
+                if (!(ok = mbar_poll(&q_empty[s], ((uint32_t)(uses[t] >> 1) & 1u) ^ 1u, abort_word, flag, 1))) return;
                 if (one) {
                     mbar_arrive_expect_tx(&q_full[s], C::kQ);
                     tma_load_3d(smem + s * C::kQ, &tm_q, &q_full[s], i.h * D, q0, i.b);
                 }
                 ++uses[t];
                 __syncwarp();
-            }
-            for (int j = i.j0; ok && j < i.j1; ++j, ++kv) {
+            };
+            auto load_kv = [&](int j) {
                 const int s = kv % C::kStages;
-                if (!(ok = mbar_poll(&kv_empty[s], ((uint32_t)(kv / C::kStages) & 1u) ^ 1u, abort_word, &g_cross_flag, 2))) break;
+                if (!ok || !(ok = mbar_poll(&kv_empty[s], ((uint32_t)(kv / C::kStages) & 1u) ^ 1u, abort_word, flag, 2))) return;
                 if (one) {
                     uint8_t *st = smem + C::kRing + s * C::kStage;
                     mbar_arrive_expect_tx(&kv_full[s], C::kStage);
                     tma_load_3d(st, &tm_k, &kv_full[s], i.h * D, j * kKT, i.b);
                     tma_load_3d(st + C::kKV, &tm_v, &kv_full[s], i.h * D, j * kKT, i.b);
                 }
+                ++kv;
                 __syncwarp();
-            }
+            };
+#pragma unroll
+            for (int t = 0; t < NS; ++t) load_q(t);
+            for (int j = i.j0; j < i.j1; ++j) load_kv(j);
         }
         if (*abort_word && one) {          // let the copies in flight land
             for (int k = kv > C::kStages ? kv - C::kStages : 0; k < kv; ++k)
                 final_wait(&kv_full[k % C::kStages], (uint32_t)(k / C::kStages) & 1u);
-            for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int t = 0; t < NS; ++t)
                 for (int k = uses[t] > 2 ? uses[t] - 2 : 0; k < uses[t]; ++k)
                     final_wait(&q_full[2 * t + (k & 1)], (uint32_t)(k >> 1) & 1u);
         }
         __syncwarp();
-    } else if (warp == 1) {
+    } else if (warp <= NS) {
+        // the products of one stream (a warp each: the steps' waits and issues are a serial chain of some hundred
+        // cycles, and one warp for all streams was what bound the kernel)
         const bool one = elect_one();
-        const uint32_t id_s = idesc_bf16(kQT, kKT, 0, 0), id_o = idesc_bf16(kQT, D, 0, 1);
-        int kv = 0, uses[2] = {0, 0};
-        uint32_t pph = 0;                  // bit t: the next phase of pb[t]
+        constexpr uint32_t id_s = idesc_bf16(kQT, kKT, 0, 0), id_o = idesc_bf16(kQT, D, 0, 1);
+        const int t = warp - 1;
+        const uint32_t ts = tmem + C::kCols * t;
+        const uint64_t dq0 = smem_desc(smem_u32(smem + 2 * t * C::kQ), 16, C::kGroup, C::kLayout);
+        const uint64_t dk0 = smem_desc(smem_u32(smem + C::kRing), 16, C::kGroup, C::kLayout);
+        const uint64_t dv0 = smem_desc(smem_u32(smem + C::kRing + C::kKV), 8192, C::kGroup, C::kLayout);
+        int ring = 0, uses = 0;            // ring stage of the item's first step; items begun
+        uint32_t kph = 0;                  // parity of the ring's pass at `ring`
+        uint32_t pph = 0;                  // bit i: the next phase of pb[2 t + i] and ob[2 t + i]
         bool ok = true;
-        // S of stream t from query buffer qs and the states of ring position k; then tell the stream
-        auto issue_s = [&](int t, int qs, int k) {
-            const uint64_t da = smem_desc(smem_u32(smem + qs * C::kQ), 16, C::kGroup, C::kLayout);
-            const uint64_t db = smem_desc(smem_u32(smem + C::kRing + (k % C::kStages) * C::kStage), 16, C::kGroup, C::kLayout);
+        // step j's S, over columns whose P the product of step j - 2 may still read: after that product
+        // (products with other accumulators are not ordered); then tell the stream
+        auto issue_s = [&](int j, int s, uint32_t ph, uint64_t dq) {
+            if (!(ok = ok && mbar_poll(&kv_full[s], ph, abort_word, flag, 3))) return;
+            tc_fence_after();
+            const uint64_t dk = dk0 + (uint64_t)(s * C::kStage >> 4);
             if (one) {
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) mma_bf16(tmem + 128 * t, da + 2 * kk, db + 2 * kk, id_s, kk > 0);
+                for (int kk = 0; kk < D / 16; ++kk) mma_bf16(ts + (j & 1) * kKT, dq + 2 * kk, dk + 2 * kk, id_s, kk > 0);
+                mma_commit(&sb[2 * t + (j & 1)]);
             }
+            __syncwarp();
         };
         for (int w = blockIdx.x; ok && w < a.items; w += gridDim.x) {
             const Item i = item_of(a, w, last_b, last_len);
             const int n = i.j1 - i.j0;
             if (n == 0) continue;
-            const int nt = (2 * i.pair + 1) * kQT < a.p.N ? 2 : 1;
-            if (!(ok = mbar_poll(&kv_full[kv % C::kStages], (uint32_t)(kv / C::kStages) & 1u, abort_word, &g_cross_flag, 3))) break;
-            for (int t = 0; t < nt; ++t) {
-                if (!(ok = mbar_poll(&q_full[2 * t + (uses[t] & 1)], (uint32_t)(uses[t] >> 1) & 1u, abort_word, &g_cross_flag, 4))) break;
-                tc_fence_after();
-                issue_s(t, 2 * t + (uses[t] & 1), kv);
-                if (one) mma_commit(&rb[t]);
-                __syncwarp();
-            }
-            for (int j = 0; ok && j < n; ++j, ++kv) {
-                const uint32_t v = smem_u32(smem + C::kRing + (kv % C::kStages) * C::kStage + C::kKV);
-                for (int t = 0; t < nt; ++t) {
-                    if (!(ok = mbar_poll(&pb[t], (pph >> t) & 1u, abort_word, &g_cross_flag, 5))) break;
-                    pph ^= 1u << t;
-                    tc_fence_after();
-                    // P (16 states = 8 columns a step) times V read along its rows
-                    const uint64_t dv = smem_desc(v, 8192, C::kGroup, C::kLayout);
-                    if (one) {
-#pragma unroll
-                        for (int kk = 0; kk < kKT / 16; ++kk)
-                            mma_bf16_ta(tmem + 128 * t + 64, tmem + 128 * t + 8 * kk, dv + kk * (2 * C::kGroup >> 4), id_o, j > 0 || kk > 0);
-                    }
-                    if (j + 1 < n) {
-                        if (t == 0 && !(ok = mbar_poll(&kv_full[(kv + 1) % C::kStages], (uint32_t)((kv + 1) / C::kStages) & 1u,
-                                                       abort_word, &g_cross_flag, 6)))
-                            break;
-                        tc_fence_after();
-                        issue_s(t, 2 * t + (uses[t] & 1), kv + 1);
-                    }
-                    if (one) {
-                        mma_commit(&rb[t]);        // the next S, or the finished O
-                        if (j + 1 == n) mma_commit(&q_empty[2 * t + (uses[t] & 1)]);
-                    }
-                    __syncwarp();
+            if ((NS * i.group + t) * kQT >= a.p.N) {       // not this stream's: its share of freeing the ring
+                for (int j = 0; ok && j < n; ++j) {
+                    if (!(ok = mbar_poll(&kv_full[ring], kph, abort_word, flag, 4))) break;
+                    if (one) mbar_arrive(&kv_empty[ring]);
+                    if (++ring == C::kStages) ring = 0, kph ^= 1u;
                 }
-                if (ok && one) mma_commit(&kv_empty[kv % C::kStages]);
-                __syncwarp();
+                continue;
             }
-            for (int t = 0; t < nt; ++t) ++uses[t];
+            if (!(ok = mbar_poll(&q_full[2 * t + (uses & 1)], (uint32_t)(uses >> 1) & 1u, abort_word, flag, 5))) break;
+            const uint64_t dq = dq0 + (uint64_t)((uses & 1) * C::kQ >> 4);
+            int r2 = ring;                                 // ring stage and parity of the next S
+            uint32_t k2 = kph;
+            for (int j = 0; j < 2 && j < n; ++j) {
+                issue_s(j, r2, k2, dq);
+                if (++r2 == C::kStages) r2 = 0, k2 ^= 1u;
+            }
+            for (int j = 0; ok && j < n; ++j) {
+                const int b = j & 1, pi = 2 * t + b;
+                if (!(ok = mbar_poll(&pb[pi], (pph >> b) & 1u, abort_word, flag, 6))) break;
+                tc_fence_after();
+                const uint64_t dv = dv0 + (uint64_t)(ring * C::kStage >> 4);
+                if (one) {
+                    // P (16 states = 8 columns a step) times V read along its rows
+#pragma unroll
+                    for (int kk = 0; kk < kKT / 16; ++kk)
+                        mma_bf16_ta(ts + 2 * kKT, ts + b * kKT + 8 * kk, dv + kk * (2 * C::kGroup >> 4), id_o, j > 0 || kk > 0);
+                    mma_commit(&ob[pi]);
+                    mma_commit(&kv_empty[ring]);
+                    if (j + 1 == n) mma_commit(&q_empty[2 * t + (uses & 1)]);
+                }
+                __syncwarp();
+                if (++ring == C::kStages) ring = 0, kph ^= 1u;
+                if (j + 2 < n) {
+                    if (!(ok = mbar_poll(&ob[pi], (pph >> b) & 1u, abort_word, flag, 11))) break;
+                    issue_s(j + 2, r2, k2, dq);
+                    if (++r2 == C::kStages) r2 = 0, k2 ^= 1u;
+                } else if (j + 1 == n && !(ok = mbar_poll(&ob[pi], (pph >> b) & 1u, abort_word, flag, 12))) {
+                    break;                                 // (the next item's S goes over both buffers)
+                }
+                pph ^= 1u << b;
+            }
+            ++uses;
         }
         if (*abort_word && one) {
-            mma_commit(fin);
-            final_wait(fin, 0);
+            mma_commit(&fin[t]);
+            final_wait(&fin[t], 0);
         }
         __syncwarp();
     } else {
-        const int t = (warp - 2) >> 2, q = warp & 3;             // stream, quarter of the TMEM lanes
-        const uint32_t ts = tmem + 128 * t + ((uint32_t)(q * 32) << 16), to = ts + 64;
+        const int t = (warp - 1 - NS) >> 2, q = warp & 3;             // stream, quarter of the TMEM lanes
+        const uint32_t ts = tmem + C::kCols * t + ((uint32_t)(q * 32) << 16), to = ts + 2 * kKT;
         const float c = a.p.scale * kLog2e;
-        uint32_t rph = 0;
+        uint32_t sph = 0, oph = 3;         // bit i: the next phase of sb[2 t + i], the phase of the last product on ob[2 t + i]
         int kv = 0;
         bool ok = true;
         for (int w = blockIdx.x; ok && w < a.items; w += gridDim.x) {
             const Item i = item_of(a, w, last_b, last_len);
             const int n = i.j1 - i.j0;
-            if ((2 * i.pair + t) * kQT >= a.p.N) {
+            if ((NS * i.group + t) * kQT >= a.p.N) {
                 kv += n;
                 continue;
             }
-            const int row = (2 * i.pair + t) * kQT + q * 32 + lane;
+            const int row = (NS * i.group + t) * kQT + q * 32 + lane;
             float m = -INFINITY, l = 0.f;
             for (int j = 0; j < n; ++j) {
-                if (!(ok = mbar_poll(&rb[t], rph & 1u, abort_word, &g_cross_flag, 7))) break;
-                rph ^= 1u;
+                const uint32_t tj = ts + (j & 1) * kKT;
+                if (!(ok = mbar_poll(&sb[2 * t + (j & 1)], (sph >> (j & 1)) & 1u, abort_word, flag, 7))) break;
+                sph ^= 1u << (j & 1);
                 tc_fence_after();
                 __syncwarp();
                 const int lim = i.len - (i.j0 + j) * kKT;
-                float hi[32], mx;
-                {
-                    float lo[32];
-                    tmem_ld32(ts, lo);
-                    tmem_ld32(ts + 32, hi);
-                    tmem_wait_ld();
-                    if (lim < kKT) {
-                        hide(lo, lim);
-                        hide(hi, lim - 32);
-                    }
-                    mx = fmaxf(lo[0], hi[0]);
-#pragma unroll
-                    for (int e = 1; e < 32; ++e) mx = fmaxf(mx, fmaxf(lo[e], hi[e]));
-                }
+                float lo[32], hi[32];
+                tmem_ld32(tj, lo);
+                tmem_ld32(tj + 32, hi);
+                tmem_wait_ld();
                 if (lim < kKT) {
-                    // zeros for V behind the length (0 * NaN would reach every row)
+                    // states behind the length: no score, and zeros for V (0 * NaN would reach every row)
+                    hide(lo, lim);
+                    hide(hi, lim - 32);
                     const int st = (kv + j) % C::kStages;
-                    if (!(ok = mbar_poll(&kv_full[st], (uint32_t)((kv + j) / C::kStages) & 1u, abort_word, &g_cross_flag, 8))) break;
+                    if (!(ok = mbar_poll(&kv_full[st], (uint32_t)((kv + j) / C::kStages) & 1u, abort_word, flag, 8))) break;
                     uint4 *v = reinterpret_cast<uint4 *>(smem + C::kRing + st * C::kStage + C::kKV + lim * D * 2);
                     for (int e = q * 32 + lane; e < (kKT - lim) * (D / 8); e += 128) v[e] = make_uint4(0, 0, 0, 0);
                     fence_proxy_async_smem();
                 }
-                mx = fmaxf(mx * c, -3.0e38f);
+                float mx4[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) mx4[e] = fmaxf(lo[e], hi[e]);
+#pragma unroll
+                for (int e = 4; e < 32; ++e) mx4[e & 3] = fmaxf(mx4[e & 3], fmaxf(lo[e], hi[e]));
+                const float mx = fmaxf(fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * c, -3.0e38f);
                 if (j == 0) {
                     m = mx;
                 } else if (__any_sync(0xffffffffu, mx > m + kGrow)) {
+                    const int pj = (j & 1) ^ 1;                 // the last P V is in O
+                    if (!(ok = mbar_poll(&ob[2 * t + pj], (oph >> pj) & 1u, abort_word, flag, 9))) break;
+                    tc_fence_after();
+                    __syncwarp();
                     const float mn = fmaxf(m, mx), f = ex2(m - mn);
                     m = mn;
                     l *= f;
@@ -297,34 +325,27 @@ cross_fwd_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                         tmem_st32(to + 32 * h, u);
                     }
                 }
-                // P of the upper half first; the lower half of S is read again, which costs less than the
-                // registers to keep it
                 uint32_t pk[32];
                 float2 sum = make_float2(0.f, 0.f);
+                exp_half(lo, pk, sum, c, m);
                 exp_half(hi, pk + 16, sum, c, m);
-                {
-                    float lo[32];
-                    tmem_ld32(ts, lo);
-                    tmem_wait_ld();
-                    if (lim < 32) hide(lo, lim);
-                    exp_half(lo, pk, sum, c, m);
-                }
                 l += sum.x + sum.y;
-                tmem_st32(ts, pk);
+                tmem_st32(tj, pk);
                 tmem_wait_st();
                 tc_fence_before();
-                mbar_arrive(&pb[t]);
+                mbar_arrive(&pb[2 * t + (j & 1)]);
+                oph ^= 1u << (j & 1);
             }
             kv += n;
             if (!ok) break;
             if (n > 0) {
-                if (!(ok = mbar_poll(&rb[t], rph & 1u, abort_word, &g_cross_flag, 9))) break;
-                rph ^= 1u;
+                const int pj = (n - 1) & 1;
+                if (!(ok = mbar_poll(&ob[2 * t + pj], (oph >> pj) & 1u, abort_word, flag, 10))) break;
                 tc_fence_after();
                 __syncwarp();
             }
             const long long bhn = ((long long)i.b * a.p.H + i.h) * a.p.N + row, rows = (long long)a.p.B * a.p.H * a.p.N;
-            const int sp = (w / a.pairs) % a.splits;
+            const int sp = (w / a.groups) % a.splits;
             const bool in = row < a.p.N;
             const float inv = n > 0 ? 1.f / l : 0.f;
 #pragma unroll 1
@@ -348,6 +369,7 @@ cross_fwd_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                         go[e] = make_uint4(pack_bf2(o[8 * e] * inv, o[8 * e + 1] * inv), pack_bf2(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
                                            pack_bf2(o[8 * e + 4] * inv, o[8 * e + 5] * inv), pack_bf2(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
                 }
+                __syncwarp();
             }
             tc_fence_before();
             if (in && a.splits > 1) reinterpret_cast<float2 *>(a.part + a.splits * rows * D)[sp * rows + bhn] = make_float2(m, l);
@@ -358,7 +380,7 @@ cross_fwd_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
     __syncthreads();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, 256);
+        tmem_dealloc(tmem, 512);
     }
 }
 
@@ -495,20 +517,21 @@ constexpr int kFew = 8;          // queries up to which the CUDA-core form runs
 
 struct FwdShape {
     bool few;
-    int nq, pairs, splits;
+    int nq, groups, splits;
     size_t part;
 };
 
 // Queries a CTA of the few-query form, and the pieces along the states: enough
-// items for two CTAs a SM (the few-query form: eight), with at least 4 steps
+// items for every SM (the few-query form: eight a SM), with at least 4 steps
 // (128 states) each.
 FwdShape fwd_shape(const CrossPlan &p) {
     FwdShape f{};
     f.few = p.N <= kFew;
     f.nq = p.N <= 1 ? 1 : (p.N <= 2 ? 2 : 4);
-    f.pairs = (p.N + 2 * kQT - 1) / (2 * kQT);
-    const long long items = (long long)p.B * p.H * (f.few ? (p.N + f.nq - 1) / f.nq : f.pairs);
-    const int want = (f.few ? 8 : 2) * kSmCount, per = f.few ? 128 : 4 * kKT;
+    const int rows = kQT * (p.d == 32 ? FC<32>::kStreams : FC<64>::kStreams);
+    f.groups = (p.N + rows - 1) / rows;
+    const long long items = (long long)p.B * p.H * (f.few ? (p.N + f.nq - 1) / f.nq : f.groups);
+    const int want = (f.few ? 8 : 1) * kSmCount, per = f.few ? 128 : 4 * kKT;
     long long s = want / items;
     if (s > p.M / per) s = p.M / per;
     f.splits = (int)(s < 1 ? 1 : s);
@@ -550,8 +573,8 @@ int fwd_t(const void *q, const void *k, const void *v, const FwdShape &f, FwdArg
         if (!head_map(&mq, q, a.p, a.p.N, (long long)a.p.H * D, kQT) || !head_map(&mk, k, a.p, a.p.M, a.p.ldk, kKT) ||
             !head_map(&mv, v, a.p, a.p.M, a.p.ldv, kKT))
             return -1;
-        const int grid = a.items < 2 * kSmCount ? a.items : 2 * kSmCount;
-        if (!launch_pdl(cross_fwd_tc<D>, (unsigned)grid, kThreads, FC<D>::kSmem, s, mq, mk, mv, a)) return -1;
+        const int grid = a.items < kSmCount ? a.items : kSmCount;
+        if (!launch_pdl(cross_fwd_tc<D>, (unsigned)grid, FC<D>::kThreads, FC<D>::kSmem, s, mq, mk, mv, a)) return -1;
     }
     if (f.splits == 1) return 1;
     const long long x = (long long)a.p.B * a.p.H * a.p.N * (D / 4);
@@ -572,9 +595,9 @@ int launch_cross_fwd_tc(const void *q, const void *k, const void *v, void *out, 
     const FwdShape f = fwd_shape(p);
     FwdArgs a{};
     a.p = p;
-    a.pairs = f.pairs;
+    a.groups = f.groups;
     a.splits = f.splits;
-    a.items = f.few ? 0 : p.B * p.H * f.pairs * f.splits;
+    a.items = f.few ? 0 : p.B * p.H * f.groups * f.splits;
     a.out = (__nv_bfloat16 *)out;
     a.lse = lse;
     a.part = (float *)ws;

@@ -85,6 +85,45 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+        "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+        "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+// 2^x of two values on the FMA pipe, for some of the exponentials of a kernel
+// that the special-function unit (16 a clock and SM) bounds: x = n + f with n
+// the nearest integer (found by adding and taking off 1.5 2^23) and 2^f on
+// [-1/2, 1/2] by a polynomial of degree 4, the minimax one for the relative
+// error (2.6e-6, by the Remez exchange); 2^n is added to the exponent bits.
+// x below -125 counts as -125.
+__device__ __forceinline__ float2 ex2_fma(float2 x) {
+    constexpr float kMagic = 12582912.f;
+    x.x = fmaxf(x.x, -125.f);
+    x.y = fmaxf(x.y, -125.f);
+    const float2 t = fadd2(x, make_float2(kMagic, kMagic));
+    const float2 f = fadd2(x, fmul2(fadd2(t, make_float2(-kMagic, -kMagic)), make_float2(-1.f, -1.f)));
+    float2 p = ffma2(make_float2(0.0095701f, 0.0095701f), f, make_float2(0.05591786f, 0.05591786f));
+    p = ffma2(p, f, make_float2(0.24024745f, 0.24024745f));
+    p = ffma2(p, f, make_float2(0.69312181f, 0.69312181f));
+    p = ffma2(p, f, make_float2(0.99999926f, 0.99999926f));
+    return make_float2(__int_as_float(__float_as_int(p.x) + (__float_as_int(t.x) << 23)),
+                       __int_as_float(__float_as_int(p.y) + (__float_as_int(t.y) << 23)));
+}
+
 // ---- CTA pairs (cta_group::2): two CTAs of a cluster on one MMA, the even
 // one ("leader") issuing.  Shared-memory addresses of the pair differ in bit
 // 24 of the cluster window; clearing it names the leader's.
