@@ -11,7 +11,7 @@
 // the last.  The maximum m in use moves, and O in TMEM is rescaled, only when a
 // row's maximum outgrows it by 2^8: P is then at most 256, which costs bf16 and
 // the fp32 sum no precision.  Heads are 32 or 64 wide, so the exponentials (16
-// a clock and SM) bound it, not the products or HBM; a quarter of them runs on
+// a clock and SM) bound it, not the products or HBM; three in eight run on
 // the FMA pipe instead.
 //
 // Few queries against many states are cut along the states into pieces whose
@@ -38,7 +38,8 @@ struct FC {
     static constexpr int kQ = kQT * D * 2, kKV = kKT * D * 2, kStage = 2 * kKV;
     static constexpr int kStages = D == 32 ? 8 : 6;
     static constexpr int kRing = 2 * kStreams * kQ;            // [stream][buffer] query tiles first
-    static constexpr int kBar = kRing + kStages * kStage;
+    static constexpr int kOut = kRing + kStages * kStage;      // 32 rows of out a softmax warp
+    static constexpr int kBar = kOut + 4 * kStreams * 32 * D * 2;
     static constexpr int kBars = 11 * kStreams + 2 * kStages;
     static constexpr int kSmem = kBar + kBars * 8 + 16 + 1024;
     static constexpr uint32_t kLayout = D == 32 ? kLayoutSw64 : kLayoutSw128;
@@ -52,29 +53,28 @@ struct FwdArgs {
     CrossPlan p;
     int groups, items;       // groups of query tiles (one a stream) of a (b, h); items = B * H * groups * splits
     int splits;              // pieces along the states (in whole steps)
+    Div d_groups, d_splits, d_h;
     __nv_bfloat16 *out;
     float *lse;
     float *part;             // splits > 1: [split][B][H][N][D] sums, then [split][B][H][N][2] (m, l)
 };
 
 struct Item {
-    int b, h, group, j0, j1, len;
+    int b, h, group, sp, j0, j1, len;
 };
 
 // Item w, its sample's length kept from the last item where the sample is the same.
 __device__ __forceinline__ Item item_of(const FwdArgs &a, int w, int &last_b, int &last_len) {
     Item i;
-    i.group = w % a.groups;
-    int r = w / a.groups;
-    const int sp = r % a.splits;
-    r /= a.splits;
-    i.h = r % a.p.H;
-    i.b = r / a.p.H;
+    int r = a.d_groups.divmod(w, i.group);
+    r = a.d_splits.divmod(r, i.sp);
+    i.b = a.d_h.divmod(r, i.h);
     if (i.b != last_b) last_b = i.b, last_len = cross_len(a.p, i.b);
     i.len = last_len;
     const int steps = (i.len + kKT - 1) / kKT;
-    i.j0 = (int)((long long)steps * sp / a.splits);
-    i.j1 = (int)((long long)steps * (sp + 1) / a.splits);
+    if (a.splits == 1) return i.j0 = 0, i.j1 = steps, i;
+    i.j0 = (int)((long long)steps * i.sp / a.splits);
+    i.j1 = (int)((long long)steps * (i.sp + 1) / a.splits);
     return i;
 }
 
@@ -90,7 +90,7 @@ __device__ __forceinline__ void exp_half(const float (&s)[32], uint32_t *pk, flo
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
         const float2 x = ffma2(make_float2(s[2 * e], s[2 * e + 1]), make_float2(c, c), make_float2(-m, -m));
-        const float2 p = e % 4 == 3 ? ex2_fma(x) : make_float2(ex2(x.x), ex2(x.y));
+        const float2 p = e % 8 % 3 == 2 || e % 8 == 7 ? ex2_fma(x) : make_float2(ex2(x.x), ex2(x.y));
         sum = fadd2(sum, p);
         pk[e] = pack_bf2(p.x, p.y);
     }
@@ -99,7 +99,7 @@ __device__ __forceinline__ void exp_half(const float (&s)[32], uint32_t *pk, flo
 template <int D>
 __global__ void __launch_bounds__(FC<D>::kThreads, 1)
 cross_fwd_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-             const __grid_constant__ CUtensorMap tm_v, const FwdArgs a) {
+             const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_out, const FwdArgs a) {
     using C = FC<D>;
     constexpr int NS = C::kStreams;
     extern __shared__ uint8_t smem_raw[];
@@ -115,6 +115,7 @@ cross_fwd_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         prefetch_tmap(&tm_q);
         prefetch_tmap(&tm_k);
         prefetch_tmap(&tm_v);
+        prefetch_tmap(&tm_out);
     }
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2 * NS; ++i) mbar_init(&q_full[i], 1), mbar_init(&q_empty[i], 1), mbar_init(&sb[i], 1), mbar_init(&pb[i], 128), mbar_init(&ob[i], 1);
@@ -265,6 +266,7 @@ cross_fwd_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         const int t = (warp - 1 - NS) >> 2, q = warp & 3;             // stream, quarter of the TMEM lanes
         const uint32_t ts = tmem + C::kCols * t + ((uint32_t)(q * 32) << 16), to = ts + 2 * kKT;
         const float c = a.p.scale * kLog2e;
+        uint8_t *ob_out = smem + C::kOut + (warp - 1 - NS) * 32 * D * 2;
         uint32_t sph = 0, oph = 3;         // bit i: the next phase of sb[2 t + i], the phase of the last product on ob[2 t + i]
         int kv = 0;
         bool ok = true;
@@ -302,8 +304,8 @@ cross_fwd_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
 #pragma unroll
                 for (int e = 0; e < 4; ++e) mx4[e] = fmaxf(lo[e], hi[e]);
 #pragma unroll
-                for (int e = 4; e < 32; ++e) mx4[e & 3] = fmaxf(mx4[e & 3], fmaxf(lo[e], hi[e]));
-                const float mx = fmaxf(fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * c, -3.0e38f);
+                for (int e = 4; e < 32; ++e) mx4[e & 3] = fmax3(mx4[e & 3], lo[e], hi[e]);
+                const float mx = fmaxf(fmaxf(fmax3(mx4[0], mx4[1], mx4[2]), mx4[3]) * c, -3.0e38f);
                 if (j == 0) {
                     m = mx;
                 } else if (__any_sync(0xffffffffu, mx > m + kGrow)) {
@@ -345,7 +347,6 @@ cross_fwd_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 __syncwarp();
             }
             const long long bhn = ((long long)i.b * a.p.H + i.h) * a.p.N + row, rows = (long long)a.p.B * a.p.H * a.p.N;
-            const int sp = (w / a.groups) % a.splits;
             const bool in = row < a.p.N;
             const float inv = n > 0 ? 1.f / l : 0.f;
 #pragma unroll 1
@@ -359,22 +360,38 @@ cross_fwd_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                     for (int e = 0; e < 32; ++e) o[e] = 0.f;
                 }
                 if (in && a.splits > 1) {
-                    float4 *po = reinterpret_cast<float4 *>(a.part + (sp * rows + bhn) * D + 32 * h);
+                    float4 *po = reinterpret_cast<float4 *>(a.part + (i.sp * rows + bhn) * D + 32 * h);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) po[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-                } else if (in) {
-                    uint4 *go = reinterpret_cast<uint4 *>(a.out + (((long long)i.b * a.p.N + row) * a.p.H + i.h) * D + 32 * h);
+                } else if (a.splits == 1) {
+                    if (h == 0) {
+                        if (lane == 0) bulk_wait_read<0>();     // the last tile's rows have been read out
+                        __syncwarp();
+                    }
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        go[e] = make_uint4(pack_bf2(o[8 * e] * inv, o[8 * e + 1] * inv), pack_bf2(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
-                                           pack_bf2(o[8 * e + 4] * inv, o[8 * e + 5] * inv), pack_bf2(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+                    for (int e = 0; e < 4; ++e) {
+                        const int ch = 4 * h + e;
+                        const int off = D == 32 ? lane * 64 + ((ch ^ ((lane >> 1) & 3)) << 4) : lane * 128 + ((ch ^ (lane & 7)) << 4);
+                        *reinterpret_cast<uint4 *>(ob_out + off) =
+                            make_uint4(pack_bf2(o[8 * e] * inv, o[8 * e + 1] * inv), pack_bf2(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
+                                       pack_bf2(o[8 * e + 4] * inv, o[8 * e + 5] * inv), pack_bf2(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+                    }
                 }
                 __syncwarp();
             }
+            if (a.splits == 1 && row - lane < a.p.N) {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    tma_store_3d(&tm_out, ob_out, i.h * D, row - lane, i.b);
+                    bulk_commit();
+                }
+            }
             tc_fence_before();
-            if (in && a.splits > 1) reinterpret_cast<float2 *>(a.part + a.splits * rows * D)[sp * rows + bhn] = make_float2(m, l);
+            if (in && a.splits > 1) reinterpret_cast<float2 *>(a.part + a.splits * rows * D)[i.sp * rows + bhn] = make_float2(m, l);
             else if (in && a.lse) a.lse[bhn] = n > 0 ? (m + __log2f(l)) * kLn2 : -INFINITY;
         }
+        if (lane == 0) bulk_wait_read<0>();
     }
     __syncwarp();
     __syncthreads();
@@ -569,12 +586,12 @@ int fwd_t(const void *q, const void *k, const void *v, const FwdShape &f, FwdArg
         if (cudaLaunchKernelEx(&cfg, fn, (const bf *)q, (const bf *)k, (const bf *)v, a) != cudaSuccess) return -1;
     } else {
         if (!once_per_device(&g_ready, setup)) return -1;
-        CUtensorMap mq, mk, mv;
+        CUtensorMap mq, mk, mv, mo;
         if (!head_map(&mq, q, a.p, a.p.N, (long long)a.p.H * D, kQT) || !head_map(&mk, k, a.p, a.p.M, a.p.ldk, kKT) ||
-            !head_map(&mv, v, a.p, a.p.M, a.p.ldv, kKT))
+            !head_map(&mv, v, a.p, a.p.M, a.p.ldv, kKT) || !head_map(&mo, a.out, a.p, a.p.N, (long long)a.p.H * D, 32))
             return -1;
         const int grid = a.items < kSmCount ? a.items : kSmCount;
-        if (!launch_pdl(cross_fwd_tc<D>, (unsigned)grid, FC<D>::kThreads, FC<D>::kSmem, s, mq, mk, mv, a)) return -1;
+        if (!launch_pdl(cross_fwd_tc<D>, (unsigned)grid, FC<D>::kThreads, FC<D>::kSmem, s, mq, mk, mv, mo, a)) return -1;
     }
     if (f.splits == 1) return 1;
     const long long x = (long long)a.p.B * a.p.H * a.p.N * (D / 4);
@@ -598,6 +615,9 @@ int launch_cross_fwd_tc(const void *q, const void *k, const void *v, void *out, 
     a.groups = f.groups;
     a.splits = f.splits;
     a.items = f.few ? 0 : p.B * p.H * f.groups * f.splits;
+    a.d_groups = Div((unsigned)f.groups);
+    a.d_splits = Div((unsigned)f.splits);
+    a.d_h = Div((unsigned)p.H);
     a.out = (__nv_bfloat16 *)out;
     a.lse = lse;
     a.part = (float *)ws;

@@ -85,6 +85,12 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 __device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
     float2 d;
     asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
@@ -115,7 +121,7 @@ __device__ __forceinline__ float2 ex2_fma(float2 x) {
     x.x = fmaxf(x.x, -125.f);
     x.y = fmaxf(x.y, -125.f);
     const float2 t = fadd2(x, make_float2(kMagic, kMagic));
-    const float2 f = fadd2(x, fmul2(fadd2(t, make_float2(-kMagic, -kMagic)), make_float2(-1.f, -1.f)));
+    const float2 f = ffma2(fadd2(t, make_float2(-kMagic, -kMagic)), make_float2(-1.f, -1.f), x);
     float2 p = ffma2(make_float2(0.0095701f, 0.0095701f), f, make_float2(0.05591786f, 0.05591786f));
     p = ffma2(p, f, make_float2(0.24024745f, 0.24024745f));
     p = ffma2(p, f, make_float2(0.69312181f, 0.69312181f));
@@ -177,6 +183,23 @@ __device__ __forceinline__ void mbar_arrive_leader(uint64_t *bar) {
 }
 
 }  // namespace sm100
+
+// Division of 0 <= n < 2^31 by a divisor that the host knows.
+struct Div {
+    unsigned d;
+    int s;
+    unsigned long long m;
+    Div() = default;
+    explicit Div(unsigned x) : d(x) { magic_div(x, m, s); }
+#ifdef __CUDACC__
+    __device__ __forceinline__ int div(int n) const { return fast_div(n, m, s); }
+    __device__ __forceinline__ int divmod(int n, int &rem) const {
+        const int q = fast_div(n, m, s);
+        rem = n - q * (int)d;
+        return q;
+    }
+#endif
+};
 
 // A bf16 tensor map: dims innermost first (elements), byte strides of dims
 // 1.., box extents, swizzle of 64 or 128 bytes (or 0), zero fill out of range.
