@@ -11,8 +11,9 @@
 // the last.  The maximum m in use moves, and O in TMEM is rescaled, only when a
 // row's maximum outgrows it by 2^8: P is then at most 256, which costs bf16 and
 // the fp32 sum no precision.  Heads are 32 or 64 wide, so the exponentials (16
-// a clock and SM) bound it, not the products or HBM; three in eight run on
-// the FMA pipe instead.
+// a clock and SM) bound it, not the products or HBM (moving three in eight
+// of them to a polynomial on the FMA pipe measured 1% slower: the steps'
+// latencies, not the unit alone, are what is left).
 //
 // Few queries against many states are cut along the states into pieces whose
 // unnormalised sums a second kernel joins.
@@ -90,7 +91,7 @@ __device__ __forceinline__ void exp_half(const float (&s)[32], uint32_t *pk, flo
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
         const float2 x = ffma2(make_float2(s[2 * e], s[2 * e + 1]), make_float2(c, c), make_float2(-m, -m));
-        const float2 p = e % 8 % 3 == 2 || e % 8 == 7 ? ex2_fma(x) : make_float2(ex2(x.x), ex2(x.y));
+        const float2 p = make_float2(ex2(x.x), ex2(x.y));
         sum = fadd2(sum, p);
         pk[e] = pack_bf2(p.x, p.y);
     }
@@ -291,14 +292,17 @@ cross_fwd_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 tmem_ld32(tj + 32, hi);
                 tmem_wait_ld();
                 if (lim < kKT) {
-                    // states behind the length: no score, and zeros for V (0 * NaN would reach every row)
-                    hide(lo, lim);
+                    // states behind the length: no score, and zeros for V (0 * NaN would reach every row; behind
+                    // the tensor's end the copy has put zeros itself)
+                    if (lim < 32) hide(lo, lim);
                     hide(hi, lim - 32);
-                    const int st = (kv + j) % C::kStages;
-                    if (!(ok = mbar_poll(&kv_full[st], (uint32_t)((kv + j) / C::kStages) & 1u, abort_word, flag, 8))) break;
-                    uint4 *v = reinterpret_cast<uint4 *>(smem + C::kRing + st * C::kStage + C::kKV + lim * D * 2);
-                    for (int e = q * 32 + lane; e < (kKT - lim) * (D / 8); e += 128) v[e] = make_uint4(0, 0, 0, 0);
-                    fence_proxy_async_smem();
+                    if (i.len < a.p.M) {
+                        const int st = (kv + j) % C::kStages;
+                        if (!(ok = mbar_poll(&kv_full[st], (uint32_t)((kv + j) / C::kStages) & 1u, abort_word, flag, 8))) break;
+                        uint4 *v = reinterpret_cast<uint4 *>(smem + C::kRing + st * C::kStage + C::kKV + lim * D * 2);
+                        for (int e = q * 32 + lane; e < (kKT - lim) * (D / 8); e += 128) v[e] = make_uint4(0, 0, 0, 0);
+                        fence_proxy_async_smem();
+                    }
                 }
                 float mx4[4];
 #pragma unroll
