@@ -9,9 +9,12 @@
 // memory and their dk, dv in TMEM, and walks the queries in tiles of 128: each
 // score and its exponential is computed once, and dq of a query tile is whole
 // when its pass over the states ends.  The scores are held transposed, S^T = K
-// Q^T with a state a TMEM lane, 64 queries at a time: P^T and dS^T then are the
-// TMEM operands of dV += P^T dO and dK += dS^T Q as the softmax warps leave
-// them, and only dS goes through shared memory, for dQ += dS K.
+// Q^T with a state a TMEM lane: P^T and dS^T then are the TMEM operands of dV
+// += P^T dO and dK += dS^T Q as the softmax warps leave them, and only dS goes
+// through shared memory, for dQ += dS K.  Two groups of four softmax warps take
+// 32 queries at a time each and do not wait for one another; the scores, the
+// dV and dK products (in one fixed order) and the dQ products have an issuing
+// warp each, as their waits are chains of some hundred cycles.
 //
 // The call's work, (b, h, group of state tiles) units of all query tiles, is
 // one line of costs cut into equal ranges, one a CTA (lengths are read on the
@@ -30,8 +33,8 @@ namespace {
 __device__ unsigned int g_cross_bwd_flag = 0;
 
 constexpr int kT = 128;                     // queries and states a tile
-constexpr int kHalf = 64;                   // queries a step
-constexpr int kThreads = 512;               // 0 TMA, 1 MMA, 4-11 softmax, 12-15 row statistics and dq
+constexpr int kStep = 32;                   // queries a step of one softmax group
+constexpr int kThreads = 512;               // 0 TMA, 1-3 products, 4-11 softmax, 12-15 row statistics and dq
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <int D>
@@ -42,9 +45,9 @@ struct BC {
     static constexpr int kStage = 3 * kTile, kQ = 2 * G * kTile;   // two stages of q, dout, out
     static constexpr int kDsBufs = D == 32 ? 2 : 1, kDsBuf = kT * kT * 2;
     static constexpr int kDs = kQ + 2 * kStage;
-    static constexpr int kStat = kDs + kDsBufs * kDsBuf;       // [2][128] (lse log2 e, D)
+    static constexpr int kStat = kDs + kDsBufs * kDsBuf;       // [2][128] -lse log2 e, then [2][128] -D
     static constexpr int kBar = kStat + 2 * kT * 8;
-    static constexpr int kBars = 2 + 2 + 2 + 2 + 2 + 2 + 2 + 2 + 2 + 1 + kDsBufs;
+    static constexpr int kBars = 26 + kDsBufs;
     static constexpr int kSmem = kBar + kBars * 8 + 16 + 64 + 1024;
     static constexpr uint32_t kLayout = D == 32 ? kLayoutSw64 : kLayoutSw128;
     static constexpr int kGroup = 8 * D * 2;                   // bytes of 8 rows
@@ -151,10 +154,10 @@ cross_bwd_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = align1024(smem_raw);
     uint64_t *q_full = reinterpret_cast<uint64_t *>(smem + C::kBar), *q_empty = q_full + 2, *stat_full = q_empty + 2;
-    uint64_t *sp_full = stat_full + 2, *sp_free = sp_full + 1, *pds_full = sp_free + 1, *pds_free = pds_full + 1;
-    uint64_t *dq_full = pds_free + 1, *dq_free = dq_full + 1, *kv_full = dq_free + 1, *kv_ready = kv_full + 1;
+    uint64_t *sp_full = stat_full + 2, *sp_free = sp_full + 2, *pds_full = sp_free + 2, *pds_free = pds_full + 2;
+    uint64_t *ds_full = pds_free + 2, *dq_full = ds_full + 2, *dq_free = dq_full + 1, *kv_full = dq_free + 1, *kv_ready = kv_full + 1;
     uint64_t *kv_empty = kv_ready + 1, *acc_full = kv_empty + 1, *acc_free = acc_full + 1, *fin = acc_free + 1;
-    uint64_t *ds_free = fin + 1;
+    uint64_t *ds_free = fin + 3;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kBar + C::kBars * 8);
     volatile int *abort_word = reinterpret_cast<volatile int *>(tmem_slot + 1);
     const int warp = uniform_warp(), lane = threadIdx.x & 31;
@@ -168,10 +171,12 @@ cross_bwd_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
     }
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) mbar_init(&q_full[i], 1), mbar_init(&q_empty[i], 1 + 128), mbar_init(&stat_full[i], 128);
-        mbar_init(sp_full, 1), mbar_init(sp_free, 256), mbar_init(pds_full, 256), mbar_init(pds_free, 1);
+        for (int i = 0; i < 2; ++i)
+            mbar_init(&sp_full[i], 1), mbar_init(&sp_free[i], 128), mbar_init(&pds_full[i], 128), mbar_init(&pds_free[i], 1);
         mbar_init(dq_full, 1), mbar_init(dq_free, 128), mbar_init(kv_full, 1), mbar_init(kv_ready, 128);
-        mbar_init(kv_empty, 1), mbar_init(acc_full, 1), mbar_init(acc_free, 256), mbar_init(fin, 1);
-        for (int i = 0; i < C::kDsBufs; ++i) mbar_init(&ds_free[i], 1);
+        mbar_init(kv_empty, 1), mbar_init(acc_full, 1), mbar_init(acc_free, 256);
+        for (int i = 0; i < 3; ++i) mbar_init(&fin[i], 1);
+        for (int i = 0; i < C::kDsBufs; ++i) mbar_init(&ds_free[i], 1), mbar_init(&ds_full[i], 256);
         *abort_word = 0;
         fence_barrier_init();
     }
@@ -225,90 +230,127 @@ cross_bwd_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         }
         __syncwarp();
     } else if (warp == 1) {
+        // S^T = K Q^T and dP^T = V dO^T of 32 queries for one softmax group, then for the other
         const bool one = elect_one();
-        const uint32_t id_s = idesc_bf16(kT, kHalf, 0, 0), id_acc = idesc_bf16(kT, D, 0, 1), id_dq = idesc_bf16(kT, D, 1, 1);
-        int qt = 0, seg = 0, steps = 0, tiles = 0;    // steps: halves of (query tile, state tile); tiles: those pairs
+        constexpr uint32_t id_s = idesc_bf16(kT, kStep, 0, 0);
+        const uint64_t dk0 = smem_desc(smem_u32(smem + C::kK), 16, C::kGroup, C::kLayout);
+        const uint64_t dq0 = smem_desc(smem_u32(smem + C::kQ), 16, C::kGroup, C::kLayout);
+        constexpr uint64_t tile = C::kTile >> 4, stage = C::kStage >> 4, sub = kStep * D * 2 >> 4;
+        int qt = 0, seg = 0;
+        uint32_t steps = 0;                // of each group
         bool ok = true;
-        // S^T and dP^T of 64 queries (stage s, half hf) against state tile j
-        auto issue_sp = [&](int s, int hf, int j) {
-            const uint32_t st = smem_u32(smem + C::kQ + s * C::kStage) + hf * kHalf * D * 2;
-            const uint64_t dk = smem_desc(smem_u32(smem + C::kK + j * C::kTile), 16, C::kGroup, C::kLayout);
-            const uint64_t dv = smem_desc(smem_u32(smem + C::kV + j * C::kTile), 16, C::kGroup, C::kLayout);
-            const uint64_t dq = smem_desc(st, 16, C::kGroup, C::kLayout), dg = smem_desc(st + C::kTile, 16, C::kGroup, C::kLayout);
-            if (one) {
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) mma_bf16(tmem + C::kS, dk + 2 * kk, dq + 2 * kk, id_s, kk > 0);
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) mma_bf16(tmem + C::kDp, dv + 2 * kk, dg + 2 * kk, id_s, kk > 0);
-                mma_commit(sp_full);
-            }
-            __syncwarp();
-        };
         while (ok && wk.next(a, sg)) {
             if (!(ok = mbar_poll(kv_ready, (uint32_t)seg & 1u, abort_word, flag, 3))) break;
-            const int n = 2 * sg.kt * (sg.k1 - sg.k0);        // steps of the segment: (query tile, state tile, half)
-            for (int x = 0; x <= n; ++x) {
-                // the next step's scores, as soon as the softmax warps have read the last ones
-                if (x < n) {
-                    const int kq = x / (2 * sg.kt), j = x / 2 % sg.kt, s = (qt + kq) & 1;
-                    if (j == 0 && (x & 1) == 0 &&
-                        !(ok = mbar_poll(&q_full[s], (uint32_t)((qt + kq) >> 1) & 1u, abort_word, flag, 4)))
-                        break;
-                    if (!(ok = mbar_poll(sp_free, (uint32_t)(steps + x) & 1u ^ 1u, abort_word, flag, 5))) break;
-                    tc_fence_after();
-                    issue_sp(s, x & 1, j);
-                }
-                if (x == 0) continue;
-                // the products of the step before
-                const int y = x - 1, kq = y / (2 * sg.kt), j = y / 2 % sg.kt, s = (qt + kq) & 1, hf = y & 1;
-                const bool first = kq == 0;
-                if (y == 0 && !(ok = mbar_poll(acc_free, (uint32_t)seg & 1u ^ 1u, abort_word, flag, 6))) break;
-                if (!(ok = mbar_poll(pds_full, (uint32_t)(steps + y) & 1u, abort_word, flag, 7))) break;
-                tc_fence_after();
-                const uint32_t st = smem_u32(smem + C::kQ + s * C::kStage) + hf * kHalf * D * 2, acc = tmem + C::kAcc + j * 2 * D;
-                const uint64_t dq = smem_desc(st, 8192, C::kGroup, C::kLayout), dg = smem_desc(st + C::kTile, 8192, C::kGroup, C::kLayout);
-                if (one) {
+            ++seg;
+            for (int k = sg.k0; ok && k < sg.k1; ++k, ++qt) {
+                if (!(ok = mbar_poll(&q_full[qt & 1], (uint32_t)(qt >> 1) & 1u, abort_word, flag, 4))) break;
+                const uint64_t dq = dq0 + (qt & 1) * stage;
+                for (int j = 0; ok && j < sg.kt; ++j) {
+                    const uint64_t dk = dk0 + j * tile, dv = dk + G * tile;
 #pragma unroll
-                    for (int kk = 0; kk < kHalf / 16; ++kk) {
-                        const uint32_t more = !first || hf > 0 || kk > 0;
-                        mma_bf16_ta(acc + D, tmem + C::kP + 8 * kk, dg + kk * (2 * C::kGroup >> 4), id_acc, more);
-                        mma_bf16_ta(acc, tmem + C::kDsT + 8 * kk, dq + kk * (2 * C::kGroup >> 4), id_acc, more);
+                    for (int x = 0; x < 4; ++x) {          // 32 queries x; group x & 1
+                        const int g = x & 1;
+                        if (!(ok = ok && mbar_poll(&sp_free[g], (steps + (x >> 1)) & 1u ^ 1u, abort_word, flag, 5))) break;
+                        tc_fence_after();
+                        if (one) {
+#pragma unroll
+                            for (int kk = 0; kk < D / 16; ++kk)
+                                mma_bf16(tmem + C::kS + g * kStep, dk + 2 * kk, dq + x * sub + 2 * kk, id_s, kk > 0);
+#pragma unroll
+                            for (int kk = 0; kk < D / 16; ++kk)
+                                mma_bf16(tmem + C::kDp + g * kStep, dv + 2 * kk, dq + tile + x * sub + 2 * kk, id_s, kk > 0);
+                            mma_commit(&sp_full[g]);
+                        }
+                        __syncwarp();
                     }
-                    mma_commit(pds_free);
+                    steps += 2;
                 }
+            }
+        }
+        if (*abort_word && one) {
+            mma_commit(&fin[0]);
+            final_wait(&fin[0], 0);
+        }
+        __syncwarp();
+    } else if (warp == 2) {
+        // dV += P^T dO, dK += dS^T Q, the groups' steps in turn: one order of sums
+        const bool one = elect_one();
+        constexpr uint32_t id_acc = idesc_bf16(kT, D, 0, 1);
+        const uint64_t dq0 = smem_desc(smem_u32(smem + C::kQ), 8192, C::kGroup, C::kLayout);
+        constexpr uint64_t tile = C::kTile >> 4, stage = C::kStage >> 4, sub = kStep * D * 2 >> 4, k16 = 2 * C::kGroup >> 4;
+        int qt = 0, seg = 0;
+        uint32_t steps = 0;
+        bool ok = true;
+        while (ok && wk.next(a, sg)) {
+            if (!(ok = mbar_poll(acc_free, (uint32_t)seg & 1u ^ 1u, abort_word, flag, 6))) break;
+            tc_fence_after();
+            ++seg;
+            for (int k = sg.k0; ok && k < sg.k1; ++k, ++qt) {
+                const uint64_t dq = dq0 + (qt & 1) * stage, dg = dq + tile;
+                for (int j = 0; ok && j < sg.kt; ++j) {
+                    const uint32_t acc = tmem + C::kAcc + j * 2 * D;
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const int g = x & 1;
+                        if (!(ok = ok && mbar_poll(&pds_full[g], (steps + (x >> 1)) & 1u, abort_word, flag, 7))) break;
+                        tc_fence_after();
+                        if (one) {
+#pragma unroll
+                            for (int kk = 0; kk < kStep / 16; ++kk) {
+                                const uint32_t more = k > sg.k0 || x > 0 || kk > 0;
+                                mma_bf16_ta(acc + D, tmem + C::kP + 16 * g + 8 * kk, dg + x * sub + kk * k16, id_acc, more);
+                                mma_bf16_ta(acc, tmem + C::kDsT + 16 * g + 8 * kk, dq + x * sub + kk * k16, id_acc, more);
+                            }
+                            mma_commit(&pds_free[g]);
+                        }
+                        __syncwarp();
+                    }
+                    steps += 2;
+                }
+                if (ok && one) mma_commit(&q_empty[qt & 1]);
                 __syncwarp();
-                if (hf == 1) {           // both halves of dS are in shared memory: dQ of the tile
-                    if (j == 0 && !(ok = mbar_poll(dq_free, (uint32_t)(qt + kq) & 1u ^ 1u, abort_word, flag, 8))) break;
-                    tc_fence_after();
+            }
+            if (ok && one) mma_commit(acc_full);
+            __syncwarp();
+        }
+        if (*abort_word && one) {
+            mma_commit(&fin[1]);
+            final_wait(&fin[1], 0);
+        }
+        __syncwarp();
+    } else if (warp == 3) {
+        // dQ += dS K, when both groups have left their dS of a state tile
+        const bool one = elect_one();
+        constexpr uint32_t id_dq = idesc_bf16(kT, D, 1, 1);
+        const uint64_t ds0 = smem_desc(smem_u32(smem + C::kDs), C::kDsBuf / 2, 1024, kLayoutSw128);
+        const uint64_t dk0 = smem_desc(smem_u32(smem + C::kK), 8192, C::kGroup, C::kLayout);
+        int qt = 0;
+        uint32_t tiles = 0;
+        bool ok = true;
+        while (ok && wk.next(a, sg)) {
+            for (int k = sg.k0; ok && k < sg.k1; ++k, ++qt) {
+                if (!(ok = mbar_poll(dq_free, (uint32_t)qt & 1u ^ 1u, abort_word, flag, 8))) break;
+                for (int j = 0; j < sg.kt; ++j, ++tiles) {
                     const int buf = tiles % C::kDsBufs;
-                    const uint64_t ds = smem_desc(smem_u32(smem + C::kDs + buf * C::kDsBuf), C::kDsBuf / 2, 1024, kLayoutSw128);
-                    const uint64_t dk = smem_desc(smem_u32(smem + C::kK + j * C::kTile), 8192, C::kGroup, C::kLayout);
+                    if (!(ok = mbar_poll(&ds_full[buf], (tiles / C::kDsBufs) & 1u, abort_word, flag, 17))) break;
+                    tc_fence_after();
+                    const uint64_t ds = ds0 + buf * (uint64_t)(C::kDsBuf >> 4), dk = dk0 + j * (uint64_t)(C::kTile >> 4);
                     if (one) {
 #pragma unroll
                         for (int kk = 0; kk < kT / 16; ++kk)
                             mma_bf16(tmem + C::kDq, ds + kk * (2048 >> 4), dk + kk * (2 * C::kGroup >> 4), id_dq, j > 0 || kk > 0);
                         mma_commit(&ds_free[buf]);
-                        if (j + 1 == sg.kt) {
-                            mma_commit(dq_full);
-                            mma_commit(&q_empty[s]);
-                        }
+                        if (j + 1 == sg.kt) mma_commit(dq_full);
                     }
-                    ++tiles;
                     __syncwarp();
                 }
             }
-            if (ok && one) {
-                mma_commit(acc_full);
-                mma_commit(kv_empty);
-            }
+            if (ok && one) mma_commit(kv_empty);
             __syncwarp();
-            qt += sg.k1 - sg.k0;
-            steps += n;
-            ++seg;
         }
         if (*abort_word && one) {
-            mma_commit(fin);
-            final_wait(fin, 0);
+            mma_commit(&fin[2]);
+            final_wait(&fin[2], 0);
         }
         __syncwarp();
     } else if (warp >= 12) {
@@ -316,7 +358,7 @@ cross_bwd_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         const int r = threadIdx.x - 384, q = warp & 3;
         int qt = 0, seg = 0;
         bool ok = true;
-        float2 *stat = reinterpret_cast<float2 *>(smem + C::kStat);
+        float *stat = reinterpret_cast<float *>(smem + C::kStat);
         while (ok && wk.next(a, sg)) {
             if (!(ok = mbar_poll(kv_full, (uint32_t)seg & 1u, abort_word, flag, 9))) break;
             const int lim = sg.len - (sg.g * G + sg.kt - 1) * kT;      // valid rows of the last state tile
@@ -331,7 +373,7 @@ cross_bwd_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             auto stats = [&](int k, int t) {     // of query tile k, the t-th of this CTA
                 const int i = k * kT + r;
                 // a row behind the last query: p = exp2(0 - inf) = 0
-                const float ls = i < a.p.N ? a.lse[bh + i] * kLog2e : INFINITY;
+                const float ls = i < a.p.N ? -a.lse[bh + i] * kLog2e : -INFINITY;
                 if (!mbar_poll(&q_full[t & 1], (uint32_t)(t >> 1) & 1u, abort_word, flag, 10)) return false;
                 const uint8_t *st = smem + C::kQ + (t & 1) * C::kStage;
                 float d = 0.f;
@@ -344,7 +386,8 @@ cross_bwd_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
 #pragma unroll
                     for (int e = 0; e < 4; ++e) d += bf_lo(xw[e]) * bf_lo(yw[e]) + bf_hi(xw[e]) * bf_hi(yw[e]);
                 }
-                stat[(t & 1) * kT + r] = make_float2(ls, d);
+                stat[(t & 1) * kT + r] = ls;
+                stat[(2 + (t & 1)) * kT + r] = -d;
                 mbar_arrive(&stat_full[t & 1]);
                 mbar_arrive(&q_empty[t & 1]);
                 return true;
@@ -389,49 +432,62 @@ cross_bwd_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         const int q = warp & 3, wg = (warp - 4) >> 2, r = q * 32 + lane;
         const uint32_t tl = tmem + ((uint32_t)(q * 32) << 16);
         const float c = a.p.scale * kLog2e;
-        int qt = 0, seg = 0, steps = 0, tiles = 0;
+        int qt = 0, seg = 0;
+        uint32_t steps = 0, tiles = 0;
         bool ok = true;
         while (ok && wk.next(a, sg)) {
             for (int k = sg.k0; ok && k < sg.k1; ++k, ++qt) {
                 if (!(ok = mbar_poll(&stat_full[qt & 1], (uint32_t)(qt >> 1) & 1u, abort_word, flag, 12))) break;
                 for (int j = 0; ok && j < sg.kt; ++j, ++tiles) {
-                    const bool valid = (sg.g * G + j) * kT + r < sg.len;
+                    const bool valid = (sg.g * G + j) * kT + r < sg.len, whole = __all_sync(0xffffffffu, valid);
                     const int buf = tiles % C::kDsBufs;
-                    if (!(ok = mbar_poll(&ds_free[buf], ((uint32_t)(tiles / C::kDsBufs) & 1u) ^ 1u, abort_word, flag, 13))) break;
-                    for (int hf = 0; hf < 2; ++hf, ++steps) {
-                        if (!(ok = mbar_poll(sp_full, (uint32_t)steps & 1u, abort_word, flag, 14))) break;
+                    if (!(ok = mbar_poll(&ds_free[buf], (tiles / C::kDsBufs) & 1u ^ 1u, abort_word, flag, 13))) break;
+#pragma unroll 1
+                    for (int u = 0; u < 2; ++u, ++steps) {
+                        if (!(ok = mbar_poll(&sp_full[wg], steps & 1u, abort_word, flag, 14))) break;
                         tc_fence_after();
                         __syncwarp();
                         float s[32], dp[32];
-                        tmem_ld32(tl + C::kS + wg * 32, s);
-                        tmem_ld32(tl + C::kDp + wg * 32, dp);
+                        tmem_ld32(tl + C::kS + wg * kStep, s);
+                        tmem_ld32(tl + C::kDp + wg * kStep, dp);
                         tmem_wait_ld();
                         tc_fence_before();
-                        mbar_arrive(sp_free);
-                        const float4 *st = reinterpret_cast<const float4 *>(smem + C::kStat + ((qt & 1) * kT + hf * kHalf + wg * 32) * 8);
+                        mbar_arrive(&sp_free[wg]);
+                        const float4 *ls = reinterpret_cast<const float4 *>(smem + C::kStat + ((qt & 1) * kT + (2 * u + wg) * kStep) * 4);
+                        const float4 *ld = ls + 2 * kT / 4;
                         uint32_t pk[16], dk[16];
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const float4 t = st[e];                    // (lse, D) of two queries
-                            float p0 = ex2(fmaf(s[2 * e], c, -t.x)), p1 = ex2(fmaf(s[2 * e + 1], c, -t.z));
-                            float d0 = p0 * (dp[2 * e] - t.y), d1 = p1 * (dp[2 * e + 1] - t.w);
-                            pk[e] = valid ? pack_bf2(p0, p1) : 0u;     // a state behind the length may hold NaN
-                            dk[e] = valid ? pack_bf2(d0, d1) : 0u;
+                        for (int e = 0; e < 8; ++e) {
+                            const float4 l4 = ls[e], d4 = ld[e];       // -lse, -D of four queries
+                            const float2 x0 = ffma2(make_float2(s[4 * e], s[4 * e + 1]), make_float2(c, c), make_float2(l4.x, l4.y));
+                            const float2 x1 = ffma2(make_float2(s[4 * e + 2], s[4 * e + 3]), make_float2(c, c), make_float2(l4.z, l4.w));
+                            const float2 p0 = make_float2(ex2(x0.x), ex2(x0.y)), p1 = make_float2(ex2(x1.x), ex2(x1.y));
+                            const float2 d0 = fmul2(p0, fadd2(make_float2(dp[4 * e], dp[4 * e + 1]), make_float2(d4.x, d4.y)));
+                            const float2 d1 = fmul2(p1, fadd2(make_float2(dp[4 * e + 2], dp[4 * e + 3]), make_float2(d4.z, d4.w)));
+                            pk[2 * e] = pack_bf2(p0.x, p0.y), pk[2 * e + 1] = pack_bf2(p1.x, p1.y);
+                            dk[2 * e] = pack_bf2(d0.x, d0.y), dk[2 * e + 1] = pack_bf2(d1.x, d1.y);
                         }
-                        if (!(ok = mbar_poll(pds_free, (uint32_t)steps & 1u ^ 1u, abort_word, flag, 15))) break;
+                        if (!whole) {                                  // a state behind the length may hold NaN
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) pk[e] = valid ? pk[e] : 0u, dk[e] = valid ? dk[e] : 0u;
+                        }
+                        if (!(ok = mbar_poll(&pds_free[wg], steps & 1u ^ 1u, abort_word, flag, 15))) break;
                         tc_fence_after();
                         __syncwarp();
                         tmem_st16(tl + C::kP + wg * 16, pk);
                         tmem_st16(tl + C::kDsT + wg * 16, dk);
-                        uint8_t *ds = smem + C::kDs + buf * C::kDsBuf + hf * (C::kDsBuf / 2) + r * 128;
+                        uint8_t *ds = smem + C::kDs + buf * C::kDsBuf + u * (C::kDsBuf / 2) + r * 128;
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
                             *reinterpret_cast<uint4 *>(ds + (((wg * 4 + e) ^ (r & 7)) << 4)) =
                                 make_uint4(dk[4 * e], dk[4 * e + 1], dk[4 * e + 2], dk[4 * e + 3]);
-                        fence_proxy_async_smem();
                         tmem_wait_st();
                         tc_fence_before();
-                        mbar_arrive(pds_full);
+                        mbar_arrive(&pds_full[wg]);
+                        if (u == 1) {
+                            fence_proxy_async_smem();
+                            mbar_arrive(&ds_full[buf]);
+                        }
                     }
                 }
             }
