@@ -11,10 +11,13 @@
 // when its pass over the states ends.  The scores are held transposed, S^T = K
 // Q^T with a state a TMEM lane: P^T and dS^T then are the TMEM operands of dV
 // += P^T dO and dK += dS^T Q as the softmax warps leave them, and only dS goes
-// through shared memory, for dQ += dS K.  Two groups of four softmax warps take
-// 32 queries at a time each and do not wait for one another; the scores, the
-// dV and dK products (in one fixed order) and the dQ products have an issuing
-// warp each, as their waits are chains of some hundred cycles.
+// through shared memory, for dQ += dS K.  -lse / scale and -D of a query enter
+// as a further step of the products' inner dimension (three bf16 parts, 24
+// bits, against ones): read per element from shared memory they took more of
+// its bandwidth than everything else.  Two groups of four softmax warps take 32
+// queries at a time each; the scores, the dV and dK products (in one fixed
+// order) and the dQ products have an issuing warp each, as their waits are
+// chains of some hundred cycles.
 //
 // The call's work, (b, h, group of state tiles) units of all query tiles, is
 // one line of costs cut into equal ranges, one a CTA (lengths are read on the
@@ -34,6 +37,7 @@ __device__ unsigned int g_cross_bwd_flag = 0;
 
 constexpr int kT = 128;                     // queries and states a tile
 constexpr int kStep = 32;                   // queries a step of one softmax group
+constexpr int kHalf = 2 * kStep;            // of both
 constexpr int kThreads = 512;               // 0 TMA, 1-3 products, 4-11 softmax, 12-15 row statistics and dq
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -45,9 +49,10 @@ struct BC {
     static constexpr int kStage = 3 * kTile, kQ = 2 * G * kTile;   // two stages of q, dout, out
     static constexpr int kDsBufs = D == 32 ? 2 : 1, kDsBuf = kT * kT * 2;
     static constexpr int kDs = kQ + 2 * kStage;
-    static constexpr int kStat = kDs + kDsBufs * kDsBuf;       // [2][128] -lse log2 e, then [2][128] -D
-    static constexpr int kBar = kStat + 2 * kT * 8;
-    static constexpr int kBars = 26 + kDsBufs;
+    // [stage][-lse / scale, -D] parts of a query, K-major [128][16] without swizzle; then the ones against them
+    static constexpr int kExtTile = kT * 32, kExt = kDs + kDsBufs * kDsBuf, kOnes = kExt + 4 * kExtTile;
+    static constexpr int kBar = kOnes + kExtTile;
+    static constexpr int kBars = 24 + 2 * kDsBufs;
     static constexpr int kSmem = kBar + kBars * 8 + 16 + 64 + 1024;
     static constexpr uint32_t kLayout = D == 32 ? kLayoutSw64 : kLayoutSw128;
     static constexpr int kGroup = 8 * D * 2;                   // bytes of 8 rows
@@ -154,7 +159,7 @@ cross_bwd_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = align1024(smem_raw);
     uint64_t *q_full = reinterpret_cast<uint64_t *>(smem + C::kBar), *q_empty = q_full + 2, *stat_full = q_empty + 2;
-    uint64_t *sp_full = stat_full + 2, *sp_free = sp_full + 2, *pds_full = sp_free + 2, *pds_free = pds_full + 2;
+    uint64_t *sp_full = stat_full + 2, *sp_free = sp_full + 1, *pds_full = sp_free + 1, *pds_free = pds_full + 2;
     uint64_t *ds_full = pds_free + 2, *dq_full = ds_full + 2, *dq_free = dq_full + 1, *kv_full = dq_free + 1, *kv_ready = kv_full + 1;
     uint64_t *kv_empty = kv_ready + 1, *acc_full = kv_empty + 1, *acc_free = acc_full + 1, *fin = acc_free + 1;
     uint64_t *ds_free = fin + 3;
@@ -172,7 +177,8 @@ cross_bwd_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) mbar_init(&q_full[i], 1), mbar_init(&q_empty[i], 1 + 128), mbar_init(&stat_full[i], 128);
         for (int i = 0; i < 2; ++i)
-            mbar_init(&sp_full[i], 1), mbar_init(&sp_free[i], 128), mbar_init(&pds_full[i], 128), mbar_init(&pds_free[i], 1);
+            mbar_init(&pds_full[i], 128), mbar_init(&pds_free[i], 1);
+        mbar_init(sp_full, 1), mbar_init(sp_free, 256);
         mbar_init(dq_full, 1), mbar_init(dq_free, 128), mbar_init(kv_full, 1), mbar_init(kv_ready, 128);
         mbar_init(kv_empty, 1), mbar_init(acc_full, 1), mbar_init(acc_free, 256);
         for (int i = 0; i < 3; ++i) mbar_init(&fin[i], 1);
@@ -180,6 +186,12 @@ cross_bwd_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         *abort_word = 0;
         fence_barrier_init();
     }
+    for (int e = threadIdx.x; e < 5 * C::kExtTile / 16; e += kThreads) {
+        // the parts' upper eight columns stay zero, the lower ones are written a tile at a time
+        const uint32_t x = e < 4 * C::kExtTile / 16 ? 0u : 0x3F803F80u;
+        reinterpret_cast<uint4 *>(smem + C::kExt)[e] = make_uint4(x, x, x, x);
+    }
+    fence_proxy_async_smem();
     // (before the allocation: a CTA that waited for the previous kernel while it held TMEM could keep that
     // kernel's own CTAs from theirs)
     pdl_wait();
@@ -230,40 +242,41 @@ cross_bwd_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         }
         __syncwarp();
     } else if (warp == 1) {
-        // S^T = K Q^T and dP^T = V dO^T of 32 queries for one softmax group, then for the other
+        // S^T = K Q^T - lse / scale and dP^T = V dO^T - D of 64 queries, once both groups have read the last ones
         const bool one = elect_one();
-        constexpr uint32_t id_s = idesc_bf16(kT, kStep, 0, 0);
+        constexpr uint32_t id_s = idesc_bf16(kT, kHalf, 0, 0);
         const uint64_t dk0 = smem_desc(smem_u32(smem + C::kK), 16, C::kGroup, C::kLayout);
         const uint64_t dq0 = smem_desc(smem_u32(smem + C::kQ), 16, C::kGroup, C::kLayout);
-        constexpr uint64_t tile = C::kTile >> 4, stage = C::kStage >> 4, sub = kStep * D * 2 >> 4;
+        const uint64_t de0 = smem_desc(smem_u32(smem + C::kExt), 128, 256, kLayoutNone);
+        const uint64_t d1 = smem_desc(smem_u32(smem + C::kOnes), 128, 256, kLayoutNone);
+        constexpr uint64_t tile = C::kTile >> 4, stage = C::kStage >> 4, ext = C::kExtTile >> 4;
         int qt = 0, seg = 0;
-        uint32_t steps = 0;                // of each group
+        uint32_t steps = 0;
         bool ok = true;
         while (ok && wk.next(a, sg)) {
             if (!(ok = mbar_poll(kv_ready, (uint32_t)seg & 1u, abort_word, flag, 3))) break;
             ++seg;
             for (int k = sg.k0; ok && k < sg.k1; ++k, ++qt) {
-                if (!(ok = mbar_poll(&q_full[qt & 1], (uint32_t)(qt >> 1) & 1u, abort_word, flag, 4))) break;
-                const uint64_t dq = dq0 + (qt & 1) * stage;
+                if (!(ok = mbar_poll(&stat_full[qt & 1], (uint32_t)(qt >> 1) & 1u, abort_word, flag, 4))) break;
+                const uint64_t dq = dq0 + (qt & 1) * stage, de = de0 + (qt & 1) * 2 * ext;
                 for (int j = 0; ok && j < sg.kt; ++j) {
                     const uint64_t dk = dk0 + j * tile, dv = dk + G * tile;
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {          // 32 queries x; group x & 1
-                        const int g = x & 1;
-                        if (!(ok = ok && mbar_poll(&sp_free[g], (steps + (x >> 1)) & 1u ^ 1u, abort_word, flag, 5))) break;
+                    for (int u = 0; u < 2; ++u, ++steps) {
+                        if (!(ok = ok && mbar_poll(sp_free, steps & 1u ^ 1u, abort_word, flag, 5))) break;
                         tc_fence_after();
+                        const uint64_t du = dq + u * (kHalf * D * 2 >> 4), eu = de + u * (ext / 2);
                         if (one) {
 #pragma unroll
-                            for (int kk = 0; kk < D / 16; ++kk)
-                                mma_bf16(tmem + C::kS + g * kStep, dk + 2 * kk, dq + x * sub + 2 * kk, id_s, kk > 0);
+                            for (int kk = 0; kk < D / 16; ++kk) mma_bf16(tmem + C::kS, dk + 2 * kk, du + 2 * kk, id_s, kk > 0);
+                            mma_bf16(tmem + C::kS, d1, eu, id_s, 1);
 #pragma unroll
-                            for (int kk = 0; kk < D / 16; ++kk)
-                                mma_bf16(tmem + C::kDp + g * kStep, dv + 2 * kk, dq + tile + x * sub + 2 * kk, id_s, kk > 0);
-                            mma_commit(&sp_full[g]);
+                            for (int kk = 0; kk < D / 16; ++kk) mma_bf16(tmem + C::kDp, dv + 2 * kk, du + tile + 2 * kk, id_s, kk > 0);
+                            mma_bf16(tmem + C::kDp, d1, eu + ext, id_s, 1);
+                            mma_commit(sp_full);
                         }
                         __syncwarp();
                     }
-                    steps += 2;
                 }
             }
         }
@@ -358,7 +371,13 @@ cross_bwd_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         const int r = threadIdx.x - 384, q = warp & 3;
         int qt = 0, seg = 0;
         bool ok = true;
-        float *stat = reinterpret_cast<float *>(smem + C::kStat);
+        const float per = 1.f / a.p.scale;
+        // x as the sum of three bf16
+        auto parts = [](float x) {
+            const float hi = __bfloat162float(__float2bfloat16_rn(x)), y = x - hi;
+            const float mid = __bfloat162float(__float2bfloat16_rn(y));
+            return make_uint4(pack_bf2(hi, mid), pack_bf2(y - mid, 0.f), 0u, 0u);
+        };
         while (ok && wk.next(a, sg)) {
             if (!(ok = mbar_poll(kv_full, (uint32_t)seg & 1u, abort_word, flag, 9))) break;
             const int lim = sg.len - (sg.g * G + sg.kt - 1) * kT;      // valid rows of the last state tile
@@ -372,8 +391,8 @@ cross_bwd_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             const long long bh = ((long long)sg.b * a.p.H + sg.h) * a.p.N;
             auto stats = [&](int k, int t) {     // of query tile k, the t-th of this CTA
                 const int i = k * kT + r;
-                // a row behind the last query: p = exp2(0 - inf) = 0
-                const float ls = i < a.p.N ? -a.lse[bh + i] * kLog2e : -INFINITY;
+                // (a row behind the last query: p = exp2 of far less than -126, which is 0, for any scale the entry points take)
+                const float ls = i < a.p.N ? -a.lse[bh + i] * per : -1e30f;
                 if (!mbar_poll(&q_full[t & 1], (uint32_t)(t >> 1) & 1u, abort_word, flag, 10)) return false;
                 const uint8_t *st = smem + C::kQ + (t & 1) * C::kStage;
                 float d = 0.f;
@@ -386,8 +405,10 @@ cross_bwd_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
 #pragma unroll
                     for (int e = 0; e < 4; ++e) d += bf_lo(xw[e]) * bf_lo(yw[e]) + bf_hi(xw[e]) * bf_hi(yw[e]);
                 }
-                stat[(t & 1) * kT + r] = ls;
-                stat[(2 + (t & 1)) * kT + r] = -d;
+                uint8_t *ext = smem + C::kExt + (t & 1) * 2 * C::kExtTile + (r >> 3) * 256 + (r & 7) * 16;
+                *reinterpret_cast<uint4 *>(ext) = parts(ls);
+                *reinterpret_cast<uint4 *>(ext + C::kExtTile) = parts(-d);
+                fence_proxy_async_smem();
                 mbar_arrive(&stat_full[t & 1]);
                 mbar_arrive(&q_empty[t & 1]);
                 return true;
@@ -437,14 +458,13 @@ cross_bwd_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         bool ok = true;
         while (ok && wk.next(a, sg)) {
             for (int k = sg.k0; ok && k < sg.k1; ++k, ++qt) {
-                if (!(ok = mbar_poll(&stat_full[qt & 1], (uint32_t)(qt >> 1) & 1u, abort_word, flag, 12))) break;
                 for (int j = 0; ok && j < sg.kt; ++j, ++tiles) {
                     const bool valid = (sg.g * G + j) * kT + r < sg.len, whole = __all_sync(0xffffffffu, valid);
                     const int buf = tiles % C::kDsBufs;
                     if (!(ok = mbar_poll(&ds_free[buf], (tiles / C::kDsBufs) & 1u ^ 1u, abort_word, flag, 13))) break;
 #pragma unroll 1
                     for (int u = 0; u < 2; ++u, ++steps) {
-                        if (!(ok = mbar_poll(&sp_full[wg], steps & 1u, abort_word, flag, 14))) break;
+                        if (!(ok = mbar_poll(sp_full, steps & 1u, abort_word, flag, 14))) break;
                         tc_fence_after();
                         __syncwarp();
                         float s[32], dp[32];
@@ -452,20 +472,15 @@ cross_bwd_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                         tmem_ld32(tl + C::kDp + wg * kStep, dp);
                         tmem_wait_ld();
                         tc_fence_before();
-                        mbar_arrive(&sp_free[wg]);
-                        const float4 *ls = reinterpret_cast<const float4 *>(smem + C::kStat + ((qt & 1) * kT + (2 * u + wg) * kStep) * 4);
-                        const float4 *ld = ls + 2 * kT / 4;
+                        mbar_arrive(sp_free);
                         uint32_t pk[16], dk[16];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const float4 l4 = ls[e], d4 = ld[e];       // -lse, -D of four queries
-                            const float2 x0 = ffma2(make_float2(s[4 * e], s[4 * e + 1]), make_float2(c, c), make_float2(l4.x, l4.y));
-                            const float2 x1 = ffma2(make_float2(s[4 * e + 2], s[4 * e + 3]), make_float2(c, c), make_float2(l4.z, l4.w));
-                            const float2 p0 = make_float2(ex2(x0.x), ex2(x0.y)), p1 = make_float2(ex2(x1.x), ex2(x1.y));
-                            const float2 d0 = fmul2(p0, fadd2(make_float2(dp[4 * e], dp[4 * e + 1]), make_float2(d4.x, d4.y)));
-                            const float2 d1 = fmul2(p1, fadd2(make_float2(dp[4 * e + 2], dp[4 * e + 3]), make_float2(d4.z, d4.w)));
-                            pk[2 * e] = pack_bf2(p0.x, p0.y), pk[2 * e + 1] = pack_bf2(p1.x, p1.y);
-                            dk[2 * e] = pack_bf2(d0.x, d0.y), dk[2 * e + 1] = pack_bf2(d1.x, d1.y);
+                        for (int e = 0; e < 16; ++e) {
+                            const float2 x = fmul2(make_float2(s[2 * e], s[2 * e + 1]), make_float2(c, c));
+                            const float2 p = make_float2(ex2(x.x), ex2(x.y));
+                            const float2 d = fmul2(p, make_float2(dp[2 * e], dp[2 * e + 1]));
+                            pk[e] = pack_bf2(p.x, p.y);
+                            dk[e] = pack_bf2(d.x, d.y);
                         }
                         if (!whole) {                                  // a state behind the length may hold NaN
 #pragma unroll

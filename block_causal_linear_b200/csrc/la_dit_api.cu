@@ -40,7 +40,7 @@ la_status cross_plan(la::CrossPlan &p, la_dtype dt, int B, int N, int M, int H, 
     const long long e = dt == LA_BF16 ? 2 : 4;
     if (ldk < (long long)H * d || ldv < (long long)H * d || (ldk * e) % 16 || (ldv * e) % 16) return LA_EINVAL;
     if (!count_ok(B, M, ldk) || !count_ok(B, M, ldv)) return LA_EINVAL;
-    if (!(scale > 0.0f) || !std::isfinite(scale)) return LA_EINVAL;
+    if (!(scale >= 1e-20f) || !std::isfinite(scale)) return LA_EINVAL;
     if (reinterpret_cast<uintptr_t>(kv_len) & 3u) return LA_EINVAL;
     p.B = B; p.N = N; p.M = M; p.H = H; p.d = d;
     p.ldk = ldk; p.ldv = ldv;

@@ -407,7 +407,7 @@ LA_API la_status la_linear_backward(const void *dy, const void *x, const void *w
  * kv_len[b] states only (a value outside [0, M] is held to it); whatever k
  * and v hold behind them, NaN included, has no effect.
  *   s_ij = scale q_i . k_j,  p_i = softmax(s_i),  out_i = sum_j p_ij v_j
- * scale finite and > 0.  lse: fp32 [B][H][N], log sum_j exp(s_ij), written
+ * scale finite and at least 1e-20.  lse: fp32 [B][H][N], log sum_j exp(s_ij), written
  * for the backward pass, or NULL.  An element with no states has out = 0,
  * lse = -inf.
  * Backward, given dout:  D_i = dout_i . out_i,
