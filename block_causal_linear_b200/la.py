@@ -13,6 +13,7 @@ raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -564,13 +565,18 @@ def full_backward(q, k, v, dout, tokens_per_block=0, rope: Optional[la_rope] = N
 LA_ACT = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
 
 
-def _launch(name, device, stream, call):
-    """call(lib, stream pointer) with `device` current; raises LAError on a non-zero status."""
-    if stream is None and device.index == torch.cuda.current_device():
-        rc = call(lib(), torch.cuda.current_stream().cuda_stream)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _launch(name, fn, device, stream, *args):
+    """fn(*args, stream pointer) with `device` current; raises LAError on a non-zero status."""
+    index = device.index
+    if stream is None and index == torch.cuda.current_device():
+        rc = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(device):
-            rc = call(lib(), (stream if stream is not None else torch.cuda.current_stream()).cuda_stream)
+            rc = fn(*args, _raw_stream(index) if stream is None else stream.cuda_stream)
     if rc != LA_OK:
         raise LAError(rc, name)
 
@@ -585,6 +591,12 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+@functools.lru_cache(maxsize=4096)
+def _ws_bytes(name, *sizes):
+    """Workspace bytes of these sizes (a host function of them alone)."""
+    return int(getattr(lib(), name)(*sizes))
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -593,7 +605,7 @@ def _check_like(name, t, shape, dtype, device):
     """t is None, or a contiguous CUDA tensor of this shape, dtype and device."""
     if t is None:
         return
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
@@ -614,7 +626,8 @@ def _check_stream(device, stream):
         raise ValueError(f"the stream belongs to {stream.device}, the tensors to {device}")
 
 
-def _workspace(n, name, ws, device, stream):
+def _workspace(name, sizes, ws, device, stream):
+    n = _ws_bytes(name, *sizes)
     if n == 0:
         raise LAError(LA_EINVAL, name)
     if ws is None:
@@ -653,8 +666,8 @@ def layer_norm_forward(x, weight=None, bias=None, eps=1e-6, return_stats=False, 
         mean, rstd = (_empty(x.shape[:-1], torch.float32, x.device, stream) for _ in range(2))
     for name, t in (("mean", mean), ("rstd", rstd)):
         _check_like(name, t, x.shape[:-1], torch.float32, x.device)
-    _launch("la_layer_norm_forward", x.device, stream, lambda L, s: L.la_layer_norm_forward(
-        x.data_ptr(), _ptr(weight), _ptr(bias), y.data_ptr(), _ptr(mean), _ptr(rstd), dt, B, N, C, pb, float(eps), s))
+    _launch("la_layer_norm_forward", lib().la_layer_norm_forward, x.device, stream, x.data_ptr(), _ptr(weight),
+            _ptr(bias), y.data_ptr(), _ptr(mean), _ptr(rstd), dt, B, N, C, pb, float(eps))
     return (y, mean, rstd) if return_stats else y
 
 
@@ -688,11 +701,10 @@ def layer_norm_backward(dy, x, weight, mean, rstd, per_batch=None, weight_grad=T
     if dx is None:
         raise ValueError("dx is missing")
     if dw is not None or db is not None:
-        n = lib().la_layer_norm_backward_workspace_size(B, N, C, pb)
-        ws = _workspace(n, "la_layer_norm_backward_workspace_size", ws, x.device, stream)
-    _launch("la_layer_norm_backward", x.device, stream, lambda L, s: L.la_layer_norm_backward(
-        dy.data_ptr(), x.data_ptr(), _ptr(weight), mean.data_ptr(), rstd.data_ptr(), dx.data_ptr(), _ptr(dw), _ptr(db),
-        dt, B, N, C, pb, _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), s))
+        ws = _workspace("la_layer_norm_backward_workspace_size", (B, N, C, pb), ws, x.device, stream)
+    _launch("la_layer_norm_backward", lib().la_layer_norm_backward, x.device, stream, dy.data_ptr(), x.data_ptr(),
+            _ptr(weight), mean.data_ptr(), rstd.data_ptr(), dx.data_ptr(), _ptr(dw), _ptr(db), dt, B, N, C, pb,
+            _ptr(ws), 0 if ws is None else ws.nbytes)
     return dx, dw, db
 
 
@@ -731,10 +743,9 @@ def linear_forward(x, weight, bias=None, act="none", residual=None, return_pre=F
     y = _empty(shape, x.dtype, x.device, stream) if out is None else out
     if return_pre and pre is None and code:
         pre = _empty(shape, x.dtype, x.device, stream)
-    ws = _workspace(lib().la_linear_workspace_size(R, K, N, dt), "la_linear_workspace_size", ws, x.device, stream)
-    _launch("la_linear_forward", x.device, stream, lambda L, s: L.la_linear_forward(
-        x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(residual), y.data_ptr(), _ptr(pre), dt, code, R, K, N,
-        ws.data_ptr(), ws.numel() * ws.element_size(), s))
+    ws = _workspace("la_linear_workspace_size", (R, K, N, dt), ws, x.device, stream)
+    _launch("la_linear_forward", lib().la_linear_forward, x.device, stream, x.data_ptr(), weight.data_ptr(), _ptr(bias),
+            _ptr(residual), y.data_ptr(), _ptr(pre), dt, code, R, K, N, ws.data_ptr(), ws.nbytes)
     return (y, pre) if return_pre else y
 
 
@@ -758,11 +769,9 @@ def linear_backward(dy, x, weight, pre=None, act="none", input_grad=True, weight
     dx, dw, db = grads
     for name, t, sh in (("dx", dx, x.shape), ("dweight", dw, (N, K)), ("dbias", db, (N,))):
         _check_like(name, t, sh, x.dtype, x.device)
-    n = lib().la_linear_backward_workspace_size(R, K, N, dt, code)
-    ws = _workspace(n, "la_linear_backward_workspace_size", ws, x.device, stream)
-    _launch("la_linear_backward", x.device, stream, lambda L, s: L.la_linear_backward(
-        dy.data_ptr(), x.data_ptr(), weight.data_ptr(), _ptr(pre), _ptr(dx), _ptr(dw), _ptr(db), dt, code, R, K, N,
-        ws.data_ptr(), ws.numel() * ws.element_size(), s))
+    ws = _workspace("la_linear_backward_workspace_size", (R, K, N, dt, code), ws, x.device, stream)
+    _launch("la_linear_backward", lib().la_linear_backward, x.device, stream, dy.data_ptr(), x.data_ptr(),
+            weight.data_ptr(), _ptr(pre), _ptr(dx), _ptr(dw), _ptr(db), dt, code, R, K, N, ws.data_ptr(), ws.nbytes)
     return dx, dw, db
 
 
@@ -810,13 +819,12 @@ def cross_attention_forward(q, k, v, kv_len=None, scale=None, return_lse=False, 
     o = _empty(q.shape, q.dtype, q.device, stream) if out is None else out
     if return_lse and lse is None:
         lse = _empty((B, H, N), torch.float32, q.device, stream)
-    n = lib().la_cross_attention_workspace_size(dt, B, N, M, H, d)
-    if n == 0:
-        raise LAError(LA_EUNSUPPORTED if d not in (32, 64) else LA_EINVAL, "la_cross_attention_forward")
-    ws = _workspace(n, "la_cross_attention_workspace_size", ws, q.device, stream)
-    _launch("la_cross_attention_forward", q.device, stream, lambda L, s: L.la_cross_attention_forward(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(kv_len), o.data_ptr(), _ptr(lse), dt, B, N, M, H, d, ldk, ldv,
-        sc, ws.data_ptr(), ws.numel() * ws.element_size(), s))
+    if d not in (32, 64):
+        raise LAError(LA_EUNSUPPORTED, "la_cross_attention_forward")
+    ws = _workspace("la_cross_attention_workspace_size", (dt, B, N, M, H, d), ws, q.device, stream)
+    _launch("la_cross_attention_forward", lib().la_cross_attention_forward, q.device, stream, q.data_ptr(), k.data_ptr(),
+            v.data_ptr(), _ptr(kv_len), o.data_ptr(), _ptr(lse), dt, B, N, M, H, d, ldk, ldv, sc, ws.data_ptr(),
+            ws.nbytes)
     return (o, lse) if return_lse else o
 
 
@@ -835,14 +843,12 @@ def cross_attention_backward(q, k, v, out, lse, dout, kv_len=None, scale=None, w
     dq, dk, dv = grads
     _check_like("dq", dq, q.shape, q.dtype, q.device)
     lddk, lddv = _check_states("dk", dk, q, M), _check_states("dv", dv, q, M)
-    n = lib().la_cross_attention_backward_workspace_size(dt, B, N, M, H, d)
-    if n == 0:
-        raise LAError(LA_EUNSUPPORTED if d not in (32, 64) else LA_EINVAL, "la_cross_attention_backward")
-    ws = _workspace(n, "la_cross_attention_backward_workspace_size", ws, q.device, stream)
-    _launch("la_cross_attention_backward", q.device, stream, lambda L, s: L.la_cross_attention_backward(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(kv_len), out.data_ptr(), lse.data_ptr(), dout.data_ptr(),
-        dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dt, B, N, M, H, d, ldk, ldv, lddk, lddv, sc, ws.data_ptr(),
-        ws.numel() * ws.element_size(), s))
+    if d not in (32, 64):
+        raise LAError(LA_EUNSUPPORTED, "la_cross_attention_backward")
+    ws = _workspace("la_cross_attention_backward_workspace_size", (dt, B, N, M, H, d), ws, q.device, stream)
+    _launch("la_cross_attention_backward", lib().la_cross_attention_backward, q.device, stream, q.data_ptr(),
+            k.data_ptr(), v.data_ptr(), _ptr(kv_len), out.data_ptr(), lse.data_ptr(), dout.data_ptr(), dq.data_ptr(),
+            dk.data_ptr(), dv.data_ptr(), dt, B, N, M, H, d, ldk, ldv, lddk, lddv, sc, ws.data_ptr(), ws.nbytes)
     return dq, dk, dv
 
 
