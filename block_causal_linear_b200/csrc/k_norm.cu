@@ -3,9 +3,11 @@
 //   xh = (x - mean) rstd, mean and variance over C, rstd = 1 / sqrt(var + eps);  y = w xh + b
 //   g = w dy;  dx = rstd (g - mean(g) - xh mean(g xh));  dw = sum dy xh, db = sum dy over the rows
 //
-// Bound by HBM: each element is read once (x; x and dy) and written once.  The
-// row stays in registers between the statistics and the result; the vectors
-// come from L1.
+// Bound by HBM: each element is read once (x; x and dy) and written once.  Many
+// rows of up to 2048 channels in whole 16 bytes run a warp a row, the rows
+// arriving by bulk copies in rings of a warp's own, so that what is in flight
+// does not depend on registers or on other warps; few rows, wider ones and ones
+// at odd addresses have forms of their own below.
 #include "la_sm100_dit.cuh"
 
 namespace la {
@@ -28,6 +30,275 @@ struct alignas(sizeof(T) * VEC) Pack {
 
 template <typename T, int VEC>
 __device__ __forceinline__ Pack<T, VEC> load_pack(const T *p) { return *reinterpret_cast<const Pack<T, VEC> *>(p); }
+
+// A warp's rows r0, r0 + step, ... in a ring of slots of `pieces` rows (x, or x
+// and dy) each.
+template <typename T, int PIECES>
+struct RowRing {
+    uint8_t *slots;
+    uint64_t *full;
+    const T *src[PIECES];
+    long long r0, step, rows;
+    uint32_t rowb;
+    int C, S;
+
+    // lane 0: the copies of the i-th row
+    __device__ __forceinline__ void issue(int i) const {
+        const long long r = r0 + i * step;
+        if (r >= rows) return;
+        const int s = i % S;
+        mbar_arrive_expect_tx(&full[s], PIECES * rowb);
+#pragma unroll
+        for (int p = 0; p < PIECES; ++p) bulk_load(slots + (size_t)(s * PIECES + p) * rowb, src[p] + r * C, rowb, &full[s]);
+    }
+    __device__ __forceinline__ const T *row(int i, int p) const {
+        return reinterpret_cast<const T *>(slots + (size_t)(i % S * PIECES + p) * rowb);
+    }
+    // after an abort: copies in flight land before the shared memory goes
+    __device__ __forceinline__ void drain(int i) const {
+        for (int k = i; k < i + S; ++k)
+            if (r0 + k * step < rows) final_wait(&full[k % S], (uint32_t)(k / S) & 1u);
+    }
+};
+
+// The batch element of a row, for rows that advance by a fixed step.
+struct RowGroup {
+    int b;
+    unsigned n;
+    __device__ __forceinline__ RowGroup(long long r, int N) : b((int)(r / N)), n((unsigned)(r % N)) {}
+    __device__ __forceinline__ void advance(unsigned step, unsigned N) {
+        n += step;
+        if (n >= N) b += n / N, n %= N;
+    }
+};
+
+// Forward, a warp a row of up to 32 EPT channels.  The row is read from its
+// slot three times (mean, deviations, result); the vectors stay in registers
+// in bf16, fp32 ones would not fit and come from L1.
+template <typename T, int EPT>
+__global__ void __launch_bounds__(kThreads, EPT == 64 ? 2 : 3)
+norm_fwd_ring(const T *__restrict__ x, const T *__restrict__ w, const T *__restrict__ b, T *__restrict__ y,
+              float *__restrict__ mean_out, float *__restrict__ rstd_out, const NormPlan p, int slots) {
+    constexpr int VEC = 16 / sizeof(T), NV = EPT / VEC;
+    constexpr bool kHold = sizeof(T) == 2;
+    using P = Pack<T, VEC>;
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ uint64_t full[kThreads / 32][kRing];
+    __shared__ int abort_word;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const long long step = (long long)gridDim.x * (kThreads / 32);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kThreads / 32; ++i)
+            for (int s = 0; s < slots; ++s) mbar_init(&full[i][s], 1);
+        abort_word = 0;
+        fence_barrier_init();
+    }
+    __syncthreads();
+    RowRing<T, 1> rr;
+    rr.rowb = (uint32_t)p.C * sizeof(T);
+    rr.slots = ring + (size_t)warp * slots * rr.rowb;
+    rr.full = full[warp];
+    rr.src[0] = x;
+    rr.r0 = (long long)blockIdx.x * (kThreads / 32) + warp;
+    rr.step = step, rr.rows = p.rows, rr.C = p.C, rr.S = slots;
+    if (lane == 0)
+        for (int i = 0; i < slots; ++i) rr.issue(i);
+    const float inv = 1.f / (float)p.C;
+    RowGroup gr(rr.r0, p.N);
+    int held = -1;
+    P wk[kHold ? NV : 1], bk[kHold ? NV : 1];
+    int i = 0;
+    for (long long r = rr.r0; r < p.rows; r += step, ++i) {
+        const long long vo = p.per_batch ? (long long)gr.b * p.C : 0;
+        if (kHold && held != (p.per_batch ? gr.b : 0)) {
+            held = p.per_batch ? gr.b : 0;
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                const int c = (k * 32 + lane) * VEC;
+                if (c < p.C) {
+                    if (w) wk[k] = load_pack<T, VEC>(w + vo + c);
+                    if (b) bk[k] = load_pack<T, VEC>(b + vo + c);
+                }
+            }
+        }
+        if (!mbar_poll(&rr.full[i % slots], (uint32_t)(i / slots) & 1u, &abort_word, &g_norm_flag, 2)) {
+            if (lane == 0) rr.drain(i);
+            return;
+        }
+        const T *xs = rr.row(i, 0);
+        float2 s2 = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int c = (k * 32 + lane) * VEC;
+            if (c < p.C) {
+                const P v = load_pack<T, VEC>(xs + c);
+#pragma unroll
+                for (int j = 0; j < VEC; j += 2) s2 = fadd2(s2, make_float2(to_f(v.v[j]), to_f(v.v[j + 1])));
+            }
+        }
+        const float mean = warp_sum(s2.x + s2.y) * inv;
+        s2 = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int c = (k * 32 + lane) * VEC;
+            if (c < p.C) {
+                const P v = load_pack<T, VEC>(xs + c);
+#pragma unroll
+                for (int j = 0; j < VEC; j += 2) {
+                    const float2 d = fadd2(make_float2(to_f(v.v[j]), to_f(v.v[j + 1])), make_float2(-mean, -mean));
+                    s2 = ffma2(d, d, s2);
+                }
+            }
+        }
+        const float rstd = rsqrtf(warp_sum(s2.x + s2.y) * inv + p.eps);
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int c = (k * 32 + lane) * VEC;
+            if (c < p.C) {
+                const P v = load_pack<T, VEC>(xs + c);
+                P wv, bv, o;
+                if (w) wv = kHold ? wk[k] : load_pack<T, VEC>(w + vo + c);
+                if (b) bv = kHold ? bk[k] : load_pack<T, VEC>(b + vo + c);
+#pragma unroll
+                for (int j = 0; j < VEC; j += 2) {
+                    float2 f = fmul2(fadd2(make_float2(to_f(v.v[j]), to_f(v.v[j + 1])), make_float2(-mean, -mean)), make_float2(rstd, rstd));
+                    if (w) f = fmul2(f, make_float2(to_f(wv.v[j]), to_f(wv.v[j + 1])));
+                    if (b) f = fadd2(f, make_float2(to_f(bv.v[j]), to_f(bv.v[j + 1])));
+                    o.v[j] = from_f<T>(f.x);
+                    o.v[j + 1] = from_f<T>(f.y);
+                }
+                *reinterpret_cast<P *>(y + r * p.C + c) = o;
+            }
+        }
+        __syncwarp();
+        if (lane == 0) rr.issue(i + slots);
+        if (lane == 0) {
+            if (mean_out) mean_out[r] = mean;
+            if (rstd_out) rstd_out[r] = rstd;
+        }
+        gr.advance((unsigned)step, (unsigned)p.N);
+    }
+}
+
+// Backward, a warp a row of up to 32 EPT channels, one CTA a SM.  A lane keeps
+// its channels' sums of dy xh and dy; the row is read from its slot twice (for
+// the row's sums, then for dx), which costs less than the registers to hold
+// it.  CTA c of a group (a batch element with per_batch, else all rows) takes
+// the rows c * warps + warp, + splits * warps, ...; its warps' sums are added
+// in warp order into part[group][split][2][C].
+template <typename T, int EPT>
+__global__ void __launch_bounds__(kThreads, 1)
+norm_bwd_warp(const T *__restrict__ dy, const T *__restrict__ x, const T *__restrict__ w,
+              const float *__restrict__ mean, const float *__restrict__ rstd, T *__restrict__ dx,
+              float *__restrict__ part, const NormPlan p, int splits, int slots) {
+    constexpr int VEC = 16 / sizeof(T), NV = EPT / VEC;
+    using P = Pack<T, VEC>;
+    extern __shared__ __align__(128) uint8_t ring[];     // the rings; at the end [2][C] floats
+    __shared__ uint64_t full[kThreads / 32][kRing];
+    __shared__ int abort_word;
+    const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = blockIdx.x / splits, sp = blockIdx.x % splits;
+    const long long n = p.per_batch ? p.N : p.rows, first = g * n;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < warps; ++i)
+            for (int s = 0; s < slots; ++s) mbar_init(&full[i][s], 1);
+        abort_word = 0;
+        fence_barrier_init();
+    }
+    __syncthreads();
+    RowRing<T, 2> rr;
+    rr.rowb = (uint32_t)p.C * sizeof(T);
+    rr.slots = ring + (size_t)warp * slots * 2 * rr.rowb;
+    rr.full = full[warp];
+    rr.src[0] = x, rr.src[1] = dy;
+    rr.r0 = first + (long long)sp * warps + warp;
+    rr.step = (long long)splits * warps, rr.rows = first + n, rr.C = p.C, rr.S = slots;
+    if (lane == 0)
+        for (int i = 0; i < slots; ++i) rr.issue(i);
+    const float inv = 1.f / (float)p.C;
+    P wk[NV];
+    float2 aw[EPT / 2], ab[EPT / 2];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int c = (k * 32 + lane) * VEC;
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) wk[k].v[j] = from_f<T>(1.f);
+        if (w && c < p.C) wk[k] = load_pack<T, VEC>(w + (p.per_batch ? (long long)g * p.C : 0) + c);
+    }
+#pragma unroll
+    for (int e = 0; e < EPT / 2; ++e) aw[e] = ab[e] = make_float2(0.f, 0.f);
+    float m1 = rr.r0 < rr.rows ? mean[rr.r0] : 0.f, rs1 = rr.r0 < rr.rows ? rstd[rr.r0] : 0.f;
+    int i = 0;
+    for (long long r = rr.r0; r < rr.rows; r += rr.step, ++i) {
+        const float m = m1, rs = rs1;
+        if (r + rr.step < rr.rows) m1 = mean[r + rr.step], rs1 = rstd[r + rr.step];
+        if (!mbar_poll(&rr.full[i % slots], (uint32_t)(i / slots) & 1u, &abort_word, &g_norm_flag, 3)) break;
+        const T *xs = rr.row(i, 0), *ds = rr.row(i, 1);
+        float2 s1 = make_float2(0.f, 0.f), s2 = s1;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int c = (k * 32 + lane) * VEC;
+            if (c < p.C) {
+                const P xp = load_pack<T, VEC>(xs + c), dp = load_pack<T, VEC>(ds + c);
+#pragma unroll
+                for (int j = 0; j < VEC; j += 2) {
+                    const int e = (k * VEC + j) / 2;
+                    const float2 xh = fmul2(fadd2(make_float2(to_f(xp.v[j]), to_f(xp.v[j + 1])), make_float2(-m, -m)), make_float2(rs, rs));
+                    const float2 d = make_float2(to_f(dp.v[j]), to_f(dp.v[j + 1]));
+                    const float2 gi = fmul2(d, make_float2(to_f(wk[k].v[j]), to_f(wk[k].v[j + 1])));
+                    s1 = fadd2(s1, gi);
+                    s2 = ffma2(gi, xh, s2);
+                    aw[e] = ffma2(d, xh, aw[e]);
+                    ab[e] = fadd2(ab[e], d);
+                }
+            }
+        }
+        const float t1 = warp_sum(s1.x + s1.y) * inv, t2 = warp_sum(s2.x + s2.y) * inv;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int c = (k * 32 + lane) * VEC;
+            if (c < p.C) {
+                const P xp = load_pack<T, VEC>(xs + c), dp = load_pack<T, VEC>(ds + c);
+                P o;
+#pragma unroll
+                for (int j = 0; j < VEC; j += 2) {
+                    const float2 xh = fmul2(fadd2(make_float2(to_f(xp.v[j]), to_f(xp.v[j + 1])), make_float2(-m, -m)), make_float2(rs, rs));
+                    const float2 gi = ffma2(make_float2(to_f(dp.v[j]), to_f(dp.v[j + 1])), make_float2(to_f(wk[k].v[j]), to_f(wk[k].v[j + 1])), make_float2(-t1, -t1));
+                    const float2 f = fmul2(ffma2(xh, make_float2(-t2, -t2), gi), make_float2(rs, rs));
+                    o.v[j] = from_f<T>(f.x);
+                    o.v[j + 1] = from_f<T>(f.y);
+                }
+                *reinterpret_cast<P *>(dx + r * p.C + c) = o;
+            }
+        }
+        __syncwarp();
+        if (lane == 0) rr.issue(i + slots);
+    }
+    if (abort_word && lane == 0) rr.drain(i);
+    __syncthreads();
+    if (abort_word || !part) return;
+    float *sum = reinterpret_cast<float *>(ring);
+    for (int q = 0; q < warps; ++q) {
+        if (warp == q) {
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                const int c = (k * 32 + lane) * VEC;
+                if (c < p.C) {
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) {
+                        const float2 va = aw[(k * VEC + j) / 2], vb = ab[(k * VEC + j) / 2];
+                        float *s0 = sum + c + j, *s1p = s0 + p.C;
+                        *s0 = (q ? *s0 : 0.f) + (j & 1 ? va.y : va.x);
+                        *s1p = (q ? *s1p : 0.f) + (j & 1 ? vb.y : vb.x);
+                    }
+                }
+            }
+        }
+        __syncthreads();
+    }
+    float *o = part + ((long long)g * splits + sp) * 2 * p.C;
+    for (int e = threadIdx.x; e < 2 * p.C; e += blockDim.x) o[e] = sum[e];
+}
 
 // Forward, one row on WPR warps, EPT elements a thread.  The variance is the
 // mean square of the deviations (a second pass over the registers).
@@ -460,6 +731,9 @@ split_sum(const float *__restrict__ part, T *__restrict__ out0, T *__restrict__ 
 
 // ---------------------------------------------------------------- host
 
+constexpr int kWarpRow = 2048;           // widest row of the forms with a warp a row
+constexpr int kWarpBytes = 200 << 10;    // their shared memory a SM
+
 constexpr int kWideBwd = 512 * 16;       // widest row of norm_bwd
 constexpr int kWideFwd = 256 * 64;       // widest row of norm_fwd
 
@@ -467,9 +741,27 @@ constexpr int kWideFwd = 256 * 64;       // widest row of norm_fwd
 // element with per_batch, else all rows): as many CTAs as stay resident.
 struct BwdShape {
     int ept, tpr, threads, splits;
+    int slots;         // > 0: norm_bwd_warp with so many slots a warp
 };
-BwdShape bwd_shape(const NormPlan &p) {
+BwdShape bwd_shape(const NormPlan &p, int esize) {
     BwdShape b;
+    b.slots = 0;
+    if (p.C * esize % 16 == 0 && p.C <= kWarpRow) {
+        const long long rows = p.per_batch ? p.N : p.rows, groups = p.per_batch ? p.B : 1;
+        const int pair = 2 * p.C * esize;
+        b.threads = pair * 8 * 3 <= kWarpBytes ? 256 : 128;
+        b.slots = kWarpBytes / (pair * (b.threads / 32));
+        b.slots = b.slots < 2 ? 2 : (b.slots > kRing ? kRing : b.slots);
+        b.ept = p.C <= 256 ? 8 : (p.C <= 512 ? 16 : (p.C <= 1024 ? 32 : 64));
+        b.tpr = 32;
+        // narrow rows leave room for more CTAs a SM
+        const int per_sm = b.ept <= 16 ? 4 : (b.ept == 32 ? 2 : 1);
+        if (per_sm > 1) b.slots = b.slots / per_sm < 2 ? 2 : b.slots / per_sm;
+        long long s = (long long)kSmCount * per_sm / groups;
+        if (s > (rows + 31) / 32) s = (rows + 31) / 32;
+        b.splits = (int)(s < 1 ? 1 : s);
+        return b;
+    }
     b.ept = p.C <= 4096 ? 8 : 16;
     b.tpr = ((p.C + b.ept - 1) / b.ept + 31) / 32 * 32;
     if (b.tpr > 512) b.tpr = 256;
@@ -486,7 +778,10 @@ constexpr int kRingBytes = 48 << 10;
 constexpr int kRingMost = 2 * 2 * kWideBwd * 4;   // two stages of the widest fp32 row
 template <typename T> bool g_norm_ready[128] = {};
 template <typename T> bool norm_setup() {
-    return set_smem((const void *)norm_bwd_ring<T, 16, 512>, kRingMost) &&
+    return set_smem((const void *)norm_bwd_warp<T, 8>, kWarpBytes) && set_smem((const void *)norm_bwd_warp<T, 16>, kWarpBytes) &&
+           set_smem((const void *)norm_bwd_warp<T, 32>, kWarpBytes) && set_smem((const void *)norm_bwd_warp<T, 64>, kWarpBytes) &&
+           set_smem((const void *)norm_fwd_ring<T, 32>, kWarpBytes / 2) && set_smem((const void *)norm_fwd_ring<T, 64>, kWarpBytes / 2) &&
+           set_smem((const void *)norm_bwd_ring<T, 16, 512>, kRingMost) &&
            set_smem((const void *)norm_bwd_ring<T, 8, 512>, kRingMost) &&
            set_smem((const void *)norm_bwd_ring<T, 8, 256>, kRingMost);
 }
@@ -514,6 +809,15 @@ int fwd_pick(const T *x, const T *w, const T *b, T *y, float *mean, float *rstd,
 template <typename T>
 int norm_fwd_t(const T *x, const T *w, const T *b, T *y, float *mean, float *rstd, const NormPlan &p, cudaStream_t s) {
     constexpr int V = 16 / sizeof(T);
+    if (p.C % V == 0 && p.C > 512 && p.C <= kWarpRow && p.rows >= 8 * 8 * kSmCount) {
+        const int per_sm = p.C <= 1024 ? 3 : 2, row = p.C * (int)sizeof(T);
+        int slots = kWarpBytes / per_sm / (8 * row);
+        slots = slots < 1 ? 1 : (slots > kRing ? kRing : slots);
+        if (!once_per_device(&g_norm_ready<T>, norm_setup<T>)) return -1;
+        auto f = p.C <= 1024 ? norm_fwd_ring<T, 32> : norm_fwd_ring<T, 64>;
+        f<<<per_sm * kSmCount, kThreads, 8 * slots * row, s>>>(x, w, b, y, mean, rstd, p, slots);
+        return cudaGetLastError() == cudaSuccess ? 1 : -1;
+    }
     if (p.C <= kWideFwd)
         return p.C % V == 0 ? fwd_pick<T, V>(x, w, b, y, mean, rstd, p, s) : fwd_pick<T, 1>(x, w, b, y, mean, rstd, p, s);
     const long long grid = p.rows < (1 << 30) ? p.rows : (1 << 30);
@@ -525,10 +829,15 @@ template <typename T>
 int norm_bwd_t(const T *dy, const T *x, const T *w, const float *mean, const float *rstd, T *dx, T *dw, T *db,
                float *part, const NormPlan &p, cudaStream_t s) {
     constexpr int V = 16 / sizeof(T);
-    const BwdShape b = bwd_shape(p);
+    const BwdShape b = bwd_shape(p, sizeof(T));
     const int groups = p.per_batch ? p.B : 1;
     if (!dw && !db) part = nullptr;
-    if (p.C <= kWideBwd) {
+    if (b.slots) {
+        const int rings = b.slots * (b.threads / 32) * 2 * p.C * (int)sizeof(T), sums = 2 * p.C * 4;
+        if (!once_per_device(&g_norm_ready<T>, norm_setup<T>)) return -1;
+        auto f = b.ept == 8 ? norm_bwd_warp<T, 8> : (b.ept == 16 ? norm_bwd_warp<T, 16> : (b.ept == 32 ? norm_bwd_warp<T, 32> : norm_bwd_warp<T, 64>));
+        f<<<(unsigned)(groups * b.splits), b.threads, rings > sums ? rings : sums, s>>>(dy, x, w, mean, rstd, dx, part, p, b.splits, b.slots);
+    } else if (p.C <= kWideBwd) {
         // the CTA's pieces at the end, or two rounds of two sums a warp
         const int smem = b.threads > b.tpr ? b.threads * 2 * b.ept * 4 : b.threads / 32 * 16;
         const unsigned grid = (unsigned)(groups * b.splits);
@@ -564,7 +873,8 @@ int norm_bwd_t(const T *dy, const T *x, const T *w, const float *mean, const flo
 }  // namespace
 
 size_t norm_bwd_ws(const NormPlan &p) {
-    return align256(size_t(p.per_batch ? p.B : 1) * bwd_shape(p).splits * 2 * p.C * sizeof(float));
+    const int a = bwd_shape(p, 2).splits, b = bwd_shape(p, 4).splits;      // whichever type the call has
+    return align256(size_t(p.per_batch ? p.B : 1) * (a > b ? a : b) * 2 * p.C * sizeof(float));
 }
 
 int launch_norm_fwd(int is_bf16, const void *x, const void *w, const void *b, void *y, float *mean, float *rstd,
