@@ -4,10 +4,11 @@
 //   g = w dy;  dx = rstd (g - mean(g) - xh mean(g xh));  dw = sum dy xh, db = sum dy over the rows
 //
 // Bound by HBM: each element is read once (x; x and dy) and written once.  Many
-// rows of up to 2048 channels in whole 16 bytes run a warp a row, the rows
-// arriving by bulk copies in rings of a warp's own, so that what is in flight
-// does not depend on registers or on other warps; few rows, wider ones and ones
-// at odd addresses have forms of their own below.
+// rows of whole 16 bytes run a warp a row (forward, up to 2048 channels) or a
+// few (backward, up to 8192), the rows arriving by bulk copies in rings of
+// those warps' own, so that what is in flight does not depend on registers or
+// on other warps; few rows, wider ones and ones at odd addresses have forms of
+// their own below.
 #include "la_sm100_dit.cuh"
 
 namespace la {
@@ -72,23 +73,25 @@ struct RowGroup {
     }
 };
 
-// Forward, a warp a row of up to 32 EPT channels.  The row is read from its
-// slot three times (mean, deviations, result); the vectors stay in registers
-// in bf16, fp32 ones would not fit and come from L1.
+// Forward, a warp a row of up to 32 EPT channels, one CTA a SM.  The row is held
+// in fp32 from its one conversion on (reading it three times from its slot
+// took 1336 instructions a row of 2048, which bound the kernel at 4.4 TB/s);
+// the vectors stay in registers in bf16, fp32 ones would not fit and come from L1.
+constexpr int kFwdThreads = 384;
 template <typename T, int EPT>
-__global__ void __launch_bounds__(kThreads, EPT == 64 ? 2 : 3)
+__global__ void __launch_bounds__(kFwdThreads, 1)
 norm_fwd_ring(const T *__restrict__ x, const T *__restrict__ w, const T *__restrict__ b, T *__restrict__ y,
               float *__restrict__ mean_out, float *__restrict__ rstd_out, const NormPlan p, int slots) {
     constexpr int VEC = 16 / sizeof(T), NV = EPT / VEC;
     constexpr bool kHold = sizeof(T) == 2;
     using P = Pack<T, VEC>;
     extern __shared__ __align__(128) uint8_t ring[];
-    __shared__ uint64_t full[kThreads / 32][kRing];
+    __shared__ uint64_t full[kFwdThreads / 32][kRing];
     __shared__ int abort_word;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const long long step = (long long)gridDim.x * (kThreads / 32);
+    const long long step = (long long)gridDim.x * (kFwdThreads / 32);
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kThreads / 32; ++i)
+        for (int i = 0; i < kFwdThreads / 32; ++i)
             for (int s = 0; s < slots; ++s) mbar_init(&full[i][s], 1);
         abort_word = 0;
         fence_barrier_init();
@@ -99,7 +102,7 @@ norm_fwd_ring(const T *__restrict__ x, const T *__restrict__ w, const T *__restr
     rr.slots = ring + (size_t)warp * slots * rr.rowb;
     rr.full = full[warp];
     rr.src[0] = x;
-    rr.r0 = (long long)blockIdx.x * (kThreads / 32) + warp;
+    rr.r0 = (long long)blockIdx.x * (kFwdThreads / 32) + warp;
     rr.step = step, rr.rows = p.rows, rr.C = p.C, rr.S = slots;
     if (lane == 0)
         for (int i = 0; i < slots; ++i) rr.issue(i);
@@ -126,42 +129,43 @@ norm_fwd_ring(const T *__restrict__ x, const T *__restrict__ w, const T *__restr
             return;
         }
         const T *xs = rr.row(i, 0);
-        float2 s2 = make_float2(0.f, 0.f);
+        float2 v[EPT / 2], s2 = make_float2(0.f, 0.f);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int c = (k * 32 + lane) * VEC;
-            if (c < p.C) {
-                const P v = load_pack<T, VEC>(xs + c);
+            P u;
+            if (c < p.C) u = load_pack<T, VEC>(xs + c);
 #pragma unroll
-                for (int j = 0; j < VEC; j += 2) s2 = fadd2(s2, make_float2(to_f(v.v[j]), to_f(v.v[j + 1])));
+            for (int j = 0; j < VEC; j += 2) {
+                v[(k * VEC + j) / 2] = c < p.C ? make_float2(to_f(u.v[j]), to_f(u.v[j + 1])) : make_float2(0.f, 0.f);
+                s2 = fadd2(s2, v[(k * VEC + j) / 2]);
             }
         }
+        __syncwarp();
+        if (lane == 0) rr.issue(i + slots);
         const float mean = warp_sum(s2.x + s2.y) * inv;
         s2 = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int c = (k * 32 + lane) * VEC;
-            if (c < p.C) {
-                const P v = load_pack<T, VEC>(xs + c);
+        for (int k = 0; k < NV; ++k)
+            if ((k * 32 + lane) * VEC < p.C) {
 #pragma unroll
                 for (int j = 0; j < VEC; j += 2) {
-                    const float2 d = fadd2(make_float2(to_f(v.v[j]), to_f(v.v[j + 1])), make_float2(-mean, -mean));
+                    float2 &d = v[(k * VEC + j) / 2];
+                    d = fadd2(d, make_float2(-mean, -mean));
                     s2 = ffma2(d, d, s2);
                 }
             }
-        }
         const float rstd = rsqrtf(warp_sum(s2.x + s2.y) * inv + p.eps);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int c = (k * 32 + lane) * VEC;
             if (c < p.C) {
-                const P v = load_pack<T, VEC>(xs + c);
                 P wv, bv, o;
                 if (w) wv = kHold ? wk[k] : load_pack<T, VEC>(w + vo + c);
                 if (b) bv = kHold ? bk[k] : load_pack<T, VEC>(b + vo + c);
 #pragma unroll
                 for (int j = 0; j < VEC; j += 2) {
-                    float2 f = fmul2(fadd2(make_float2(to_f(v.v[j]), to_f(v.v[j + 1])), make_float2(-mean, -mean)), make_float2(rstd, rstd));
+                    float2 f = fmul2(v[(k * VEC + j) / 2], make_float2(rstd, rstd));
                     if (w) f = fmul2(f, make_float2(to_f(wv.v[j]), to_f(wv.v[j + 1])));
                     if (b) f = fadd2(f, make_float2(to_f(bv.v[j]), to_f(bv.v[j + 1])));
                     o.v[j] = from_f<T>(f.x);
@@ -170,8 +174,6 @@ norm_fwd_ring(const T *__restrict__ x, const T *__restrict__ w, const T *__restr
                 *reinterpret_cast<P *>(y + r * p.C + c) = o;
             }
         }
-        __syncwarp();
-        if (lane == 0) rr.issue(i + slots);
         if (lane == 0) {
             if (mean_out) mean_out[r] = mean;
             if (rstd_out) rstd_out[r] = rstd;
@@ -180,27 +182,29 @@ norm_fwd_ring(const T *__restrict__ x, const T *__restrict__ w, const T *__restr
     }
 }
 
-// Backward, a warp a row of up to 32 EPT channels, one CTA a SM.  A lane keeps
-// its channels' sums of dy xh and dy; the row is read from its slot twice (for
-// the row's sums, then for dx), which costs less than the registers to hold
-// it.  CTA c of a group (a batch element with per_batch, else all rows) takes
-// the rows c * warps + warp, + splits * warps, ...; its warps' sums are added
-// in warp order into part[group][split][2][C].
-template <typename T, int EPT>
-__global__ void __launch_bounds__(kThreads, 1)
-norm_bwd_warp(const T *__restrict__ dy, const T *__restrict__ x, const T *__restrict__ w,
+// Backward, a team of WPR warps a row, 32 channels a lane, one CTA of 16 warps a
+// SM.  A lane keeps its channels' sums of dy xh and dy; the row is read from
+// its slot twice (for the row's sums, then for dx), which costs less than the
+// registers to hold it.  CTA c of a group (a batch element with per_batch,
+// else all rows) takes the rows c * teams + team, + splits * teams, ...; its
+// teams' sums are added in team order into part[group][split][2][C].
+constexpr int kBwdThreads = 512, kLane = 32;
+template <typename T, int WPR>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+norm_bwd_team(const T *__restrict__ dy, const T *__restrict__ x, const T *__restrict__ w,
               const float *__restrict__ mean, const float *__restrict__ rstd, T *__restrict__ dx,
               float *__restrict__ part, const NormPlan p, int splits, int slots) {
-    constexpr int VEC = 16 / sizeof(T), NV = EPT / VEC;
+    constexpr int VEC = 16 / sizeof(T), NV = kLane / VEC, kTeams = kBwdThreads / 32 / WPR;
     using P = Pack<T, VEC>;
     extern __shared__ __align__(128) uint8_t ring[];     // the rings; at the end [2][C] floats
-    __shared__ uint64_t full[kThreads / 32][kRing];
+    __shared__ uint64_t full[kTeams][kRing];
+    __shared__ float2 red[2][kBwdThreads / 32];
     __shared__ int abort_word;
-    const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, team = warp / WPR, t = threadIdx.x % (32 * WPR);
     const int g = blockIdx.x / splits, sp = blockIdx.x % splits;
     const long long n = p.per_batch ? p.N : p.rows, first = g * n;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < warps; ++i)
+        for (int i = 0; i < kTeams; ++i)
             for (int s = 0; s < slots; ++s) mbar_init(&full[i][s], 1);
         abort_word = 0;
         fence_barrier_init();
@@ -208,42 +212,43 @@ norm_bwd_warp(const T *__restrict__ dy, const T *__restrict__ x, const T *__rest
     __syncthreads();
     RowRing<T, 2> rr;
     rr.rowb = (uint32_t)p.C * sizeof(T);
-    rr.slots = ring + (size_t)warp * slots * 2 * rr.rowb;
-    rr.full = full[warp];
+    rr.slots = ring + (size_t)team * slots * 2 * rr.rowb;
+    rr.full = full[team];
     rr.src[0] = x, rr.src[1] = dy;
-    rr.r0 = first + (long long)sp * warps + warp;
-    rr.step = (long long)splits * warps, rr.rows = first + n, rr.C = p.C, rr.S = slots;
-    if (lane == 0)
+    rr.r0 = first + (long long)sp * kTeams + team;
+    rr.step = (long long)splits * kTeams, rr.rows = first + n, rr.C = p.C, rr.S = slots;
+    if (t == 0)
         for (int i = 0; i < slots; ++i) rr.issue(i);
     const float inv = 1.f / (float)p.C;
     P wk[NV];
-    float2 aw[EPT / 2], ab[EPT / 2];
+    float2 aw[kLane / 2], ab[kLane / 2];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-        const int c = (k * 32 + lane) * VEC;
+        const int c = (k * 32 * WPR + t) * VEC;
 #pragma unroll
         for (int j = 0; j < VEC; ++j) wk[k].v[j] = from_f<T>(1.f);
         if (w && c < p.C) wk[k] = load_pack<T, VEC>(w + (p.per_batch ? (long long)g * p.C : 0) + c);
     }
 #pragma unroll
-    for (int e = 0; e < EPT / 2; ++e) aw[e] = ab[e] = make_float2(0.f, 0.f);
+    for (int e = 0; e < kLane / 2; ++e) aw[e] = ab[e] = make_float2(0.f, 0.f);
     float m1 = rr.r0 < rr.rows ? mean[rr.r0] : 0.f, rs1 = rr.r0 < rr.rows ? rstd[rr.r0] : 0.f;
     int i = 0;
+    // (after a wait that gave up the rows go on, without meaning: the team's barriers stay in step)
     for (long long r = rr.r0; r < rr.rows; r += rr.step, ++i) {
-        const float m = m1, rs = rs1;
+        const float rs = rs1, nm = -m1 * rs1;
         if (r + rr.step < rr.rows) m1 = mean[r + rr.step], rs1 = rstd[r + rr.step];
-        if (!mbar_poll(&rr.full[i % slots], (uint32_t)(i / slots) & 1u, &abort_word, &g_norm_flag, 3)) break;
+        mbar_poll(&rr.full[i % slots], (uint32_t)(i / slots) & 1u, &abort_word, &g_norm_flag, 3);
         const T *xs = rr.row(i, 0), *ds = rr.row(i, 1);
         float2 s1 = make_float2(0.f, 0.f), s2 = s1;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int c = (k * 32 + lane) * VEC;
+            const int c = (k * 32 * WPR + t) * VEC;
             if (c < p.C) {
                 const P xp = load_pack<T, VEC>(xs + c), dp = load_pack<T, VEC>(ds + c);
 #pragma unroll
                 for (int j = 0; j < VEC; j += 2) {
                     const int e = (k * VEC + j) / 2;
-                    const float2 xh = fmul2(fadd2(make_float2(to_f(xp.v[j]), to_f(xp.v[j + 1])), make_float2(-m, -m)), make_float2(rs, rs));
+                    const float2 xh = ffma2(make_float2(to_f(xp.v[j]), to_f(xp.v[j + 1])), make_float2(rs, rs), make_float2(nm, nm));
                     const float2 d = make_float2(to_f(dp.v[j]), to_f(dp.v[j + 1]));
                     const float2 gi = fmul2(d, make_float2(to_f(wk[k].v[j]), to_f(wk[k].v[j + 1])));
                     s1 = fadd2(s1, gi);
@@ -253,16 +258,32 @@ norm_bwd_warp(const T *__restrict__ dy, const T *__restrict__ x, const T *__rest
                 }
             }
         }
-        const float t1 = warp_sum(s1.x + s1.y) * inv, t2 = warp_sum(s2.x + s2.y) * inv;
+        float t1 = warp_sum(s1.x + s1.y), t2 = warp_sum(s2.x + s2.y);
+        if constexpr (WPR > 1) {
+            if (lane == 0) red[i & 1][warp] = make_float2(t1, t2);
+            named_bar_sync(1 + team, 32 * WPR);
+            t1 = t2 = 0.f;
+#pragma unroll
+            for (int q = 0; q < WPR; ++q) {
+                const float2 f = red[i & 1][team * WPR + q];
+                t1 += f.x, t2 += f.y;
+            }
+        } else {
+            __syncwarp();
+        }
+        // every warp of the team is past the last row: its slot takes a new one
+        if (t == 0 && i > 0 && !abort_word) rr.issue(i - 1 + slots);
+        t1 *= inv;
+        t2 *= inv;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int c = (k * 32 + lane) * VEC;
+            const int c = (k * 32 * WPR + t) * VEC;
             if (c < p.C) {
                 const P xp = load_pack<T, VEC>(xs + c), dp = load_pack<T, VEC>(ds + c);
                 P o;
 #pragma unroll
                 for (int j = 0; j < VEC; j += 2) {
-                    const float2 xh = fmul2(fadd2(make_float2(to_f(xp.v[j]), to_f(xp.v[j + 1])), make_float2(-m, -m)), make_float2(rs, rs));
+                    const float2 xh = ffma2(make_float2(to_f(xp.v[j]), to_f(xp.v[j + 1])), make_float2(rs, rs), make_float2(nm, nm));
                     const float2 gi = ffma2(make_float2(to_f(dp.v[j]), to_f(dp.v[j + 1])), make_float2(to_f(wk[k].v[j]), to_f(wk[k].v[j + 1])), make_float2(-t1, -t1));
                     const float2 f = fmul2(ffma2(xh, make_float2(-t2, -t2), gi), make_float2(rs, rs));
                     o.v[j] = from_f<T>(f.x);
@@ -271,25 +292,30 @@ norm_bwd_warp(const T *__restrict__ dy, const T *__restrict__ x, const T *__rest
                 *reinterpret_cast<P *>(dx + r * p.C + c) = o;
             }
         }
-        __syncwarp();
-        if (lane == 0) rr.issue(i + slots);
     }
-    if (abort_word && lane == 0) rr.drain(i);
+    if (abort_word && t == 0)
+        for (int k = 0; k < slots; ++k) final_wait(&rr.full[k], 0), final_wait(&rr.full[k], 1);
     __syncthreads();
     if (abort_word || !part) return;
     float *sum = reinterpret_cast<float *>(ring);
-    for (int q = 0; q < warps; ++q) {
-        if (warp == q) {
+    for (int q = 0; q < kTeams; ++q) {
+        if (team == q) {
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
-                const int c = (k * 32 + lane) * VEC;
+                const int c = (k * 32 * WPR + t) * VEC;
                 if (c < p.C) {
 #pragma unroll
-                    for (int j = 0; j < VEC; ++j) {
-                        const float2 va = aw[(k * VEC + j) / 2], vb = ab[(k * VEC + j) / 2];
-                        float *s0 = sum + c + j, *s1p = s0 + p.C;
-                        *s0 = (q ? *s0 : 0.f) + (j & 1 ? va.y : va.x);
-                        *s1p = (q ? *s1p : 0.f) + (j & 1 ? vb.y : vb.x);
+                    for (int j = 0; j < VEC; j += 4) {
+                        const int e = (k * VEC + j) / 2;
+                        float4 *sw = reinterpret_cast<float4 *>(sum + c + j), *sb = reinterpret_cast<float4 *>(sum + p.C + c + j);
+                        float4 u = make_float4(aw[e].x, aw[e].y, aw[e + 1].x, aw[e + 1].y), v = make_float4(ab[e].x, ab[e].y, ab[e + 1].x, ab[e + 1].y);
+                        if (q) {
+                            const float4 a = *sw, b = *sb;
+                            u.x += a.x, u.y += a.y, u.z += a.z, u.w += a.w;
+                            v.x += b.x, v.y += b.y, v.z += b.z, v.w += b.w;
+                        }
+                        *sw = u;
+                        *sb = v;
                     }
                 }
             }
@@ -297,7 +323,7 @@ norm_bwd_warp(const T *__restrict__ dy, const T *__restrict__ x, const T *__rest
         __syncthreads();
     }
     float *o = part + ((long long)g * splits + sp) * 2 * p.C;
-    for (int e = threadIdx.x; e < 2 * p.C; e += blockDim.x) o[e] = sum[e];
+    for (int e = threadIdx.x; e < 2 * p.C; e += kBwdThreads) o[e] = sum[e];
 }
 
 // Forward, one row on WPR warps, EPT elements a thread.  The variance is the
@@ -415,141 +441,10 @@ norm_fwd_wide(const T *__restrict__ x, const T *__restrict__ w, const T *__restr
     }
 }
 
-// Backward in one pass over x and dy.  A CTA of TPR x TY threads walks the
-// rows of its range, TY at a time, kEpt channels a thread; the channels' sums
-// of dy xh and dy stay in registers until the range ends and leave as one
-// piece, part[group][split][2][C].  Rows arrive by bulk copies in a ring of
-// `stages` stages of TY rows (each a contiguous piece of x and of dy): the
-// loads in flight do not depend on registers or on the one barrier an
-// iteration, which joins the row sums and frees the stage.
-template <typename T, int kEpt, int MAXT>
-__global__ void __launch_bounds__(MAXT)
-norm_bwd_ring(const T *__restrict__ dy, const T *__restrict__ x, const T *__restrict__ w,
-              const float *__restrict__ mean, const float *__restrict__ rstd, T *__restrict__ dx,
-              float *__restrict__ part, const NormPlan p, int tpr, int splits, int stages) {
-    constexpr int VEC = 16 / sizeof(T), NV = kEpt / VEC;
-    extern __shared__ __align__(128) uint8_t ring[];     // [stages][2][TY][C]; at the end [2 kEpt][threads] floats
-    __shared__ uint64_t full[kRing];
-    __shared__ float red[2][2][MAXT / 32];
-    __shared__ int abort_word;
-    const int warps = blockDim.x >> 5, wpr = tpr >> 5, ty = blockDim.x / tpr;
-    const int t = threadIdx.x % tpr, yy = threadIdx.x / tpr, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int g = blockIdx.x / splits, sp = blockIdx.x % splits;
-    const long long rows = p.per_batch ? p.N : p.rows;
-    const long long r0 = g * rows + rows * sp / splits, r1 = g * rows + rows * (sp + 1) / splits;
-    const uint32_t rowb = (uint32_t)p.C * sizeof(T), half = rowb * ty;
-    const int iters = (int)((r1 - r0 + ty - 1) / ty);
-    const float inv = 1.f / (float)p.C;
-    auto issue = [&](int i) {      // one thread: the copies of iteration i
-        const long long r = r0 + (long long)i * ty;
-        const uint32_t bytes = rowb * (uint32_t)(r1 - r < ty ? r1 - r : ty);
-        uint8_t *st = ring + (size_t)(i % stages) * 2 * half;
-        mbar_arrive_expect_tx(&full[i % stages], 2 * bytes);
-        bulk_load(st, x + r * p.C, bytes, &full[i % stages]);
-        bulk_load(st + half, dy + r * p.C, bytes, &full[i % stages]);
-    };
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1);
-        abort_word = 0;
-        fence_barrier_init();
-    }
-    __syncthreads();
-    if (threadIdx.x == 0)
-        for (int i = 0; i < stages && i < iters; ++i) issue(i);
-    float wv[kEpt], aw[kEpt] = {}, ab[kEpt] = {};
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = (i * tpr + t) * VEC;
-        Pack<T, VEC> k;
-        if (w && c < p.C) k = load_pack<T, VEC>(w + (p.per_batch ? (long long)g * p.C : 0) + c);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) wv[i * VEC + j] = c < p.C ? (w ? to_f(k.v[j]) : 1.f) : 0.f;
-    }
-    int i = 0;
-    float m1 = r0 + yy < r1 ? mean[r0 + yy] : 0.f, rs1 = r0 + yy < r1 ? rstd[r0 + yy] : 0.f;
-    for (; i < iters; ++i) {
-        const long long r = r0 + (long long)i * ty + yy;
-        const bool ok = r < r1;
-        const float m = m1, rs = rs1;
-        if (r + ty < r1) m1 = mean[r + ty], rs1 = rstd[r + ty];      // the next row's, a latency ahead
-        mbar_poll(&full[i % stages], (uint32_t)(i / stages) & 1u, &abort_word, &g_norm_flag, 1);
-        const T *xs = reinterpret_cast<const T *>(ring + (size_t)(i % stages) * 2 * half + (size_t)yy * rowb);
-        const T *ds = reinterpret_cast<const T *>(reinterpret_cast<const uint8_t *>(xs) + half);
-        float xh[kEpt], d[kEpt], s1 = 0.f, s2 = 0.f;
-#pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int c = (k * tpr + t) * VEC;
-            const bool in = ok && c < p.C;
-            Pack<T, VEC> xp, dp;
-            if (in) xp = load_pack<T, VEC>(xs + c), dp = load_pack<T, VEC>(ds + c);
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                const int e = k * VEC + j;
-                xh[e] = in ? (to_f(xp.v[j]) - m) * rs : 0.f;
-                d[e] = in ? to_f(dp.v[j]) : 0.f;
-                const float gi = d[e] * wv[e];
-                s1 += gi;
-                s2 += gi * xh[e];
-                aw[e] += d[e] * xh[e];
-                ab[e] += d[e];
-            }
-        }
-        s1 = warp_sum(s1);
-        s2 = warp_sum(s2);
-        if (lane == 0) red[i & 1][0][warp] = s1, red[i & 1][1][warp] = s2;
-        __syncthreads();           // the sums are there, and the stage has been read
-        if (abort_word) break;
-        if (threadIdx.x == 0 && i + stages < iters) issue(i + stages);
-        if (wpr > 1) {
-            s1 = s2 = 0.f;
-            for (int k = 0; k < wpr; ++k) s1 += red[i & 1][0][yy * wpr + k], s2 += red[i & 1][1][yy * wpr + k];
-        }
-        s1 *= inv;
-        s2 *= inv;
-#pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int c = (k * tpr + t) * VEC;
-            Pack<T, VEC> o;
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                const int e = k * VEC + j;
-                o.v[j] = from_f<T>(rs * (d[e] * wv[e] - s1 - xh[e] * s2));
-            }
-            if (ok && c < p.C) *reinterpret_cast<Pack<T, VEC> *>(dx + r * p.C + c) = o;
-        }
-    }
-    if (i < iters) {               // gave up: let the copies in flight land before the shared memory goes
-        if (threadIdx.x == 0)
-            for (int k = i; k < i + stages && k < iters; ++k) final_wait(&full[k % stages], (uint32_t)(k / stages) & 1u);
-        __syncthreads();
-        return;
-    }
-    if (!part) return;
-    float *o = part + ((long long)g * splits + sp) * 2 * p.C;
-    float *sh = reinterpret_cast<float *>(ring);
-    if (ty > 1) {                  // the TY rows' sums, added in row order
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < kEpt; ++k)
-            sh[k * blockDim.x + threadIdx.x] = aw[k], sh[(kEpt + k) * blockDim.x + threadIdx.x] = ab[k];
-        __syncthreads();
-        if (yy) return;
-#pragma unroll
-        for (int k = 0; k < kEpt; ++k) {
-            aw[k] = ab[k] = 0.f;
-            for (int y = 0; y < ty; ++y)
-                aw[k] += sh[k * blockDim.x + y * tpr + t], ab[k] += sh[(kEpt + k) * blockDim.x + y * tpr + t];
-        }
-    }
-#pragma unroll
-    for (int k = 0; k < kEpt; ++k) {
-        const int c = (k / VEC * tpr + t) * VEC + k % VEC;
-        if (c < p.C) o[c] = aw[k], o[p.C + c] = ab[k];
-    }
-}
-
-// The same for rows that are not whole 16 bytes: element loads, the next rows
-// loaded before the current ones are reduced.
+// Backward of rows that are not whole 16 bytes, in one pass: a CTA of TPR x TY
+// threads walks the rows of its range, TY at a time, kEpt channels a thread,
+// the next rows loaded before the current ones are reduced; the channels' sums
+// stay in registers and leave as one piece, part[group][split][2][C].
 template <typename T, int kEpt, int MAXT>
 __global__ void __launch_bounds__(MAXT)
 norm_bwd(const T *__restrict__ dy, const T *__restrict__ x, const T *__restrict__ w, const float *__restrict__ mean,
@@ -731,34 +626,31 @@ split_sum(const float *__restrict__ part, T *__restrict__ out0, T *__restrict__ 
 
 // ---------------------------------------------------------------- host
 
-constexpr int kWarpRow = 2048;           // widest row of the forms with a warp a row
-constexpr int kWarpBytes = 200 << 10;    // their shared memory a SM
+constexpr int kWarpRow = 2048;           // widest row of norm_fwd_ring
+constexpr int kRingBytes = 200 << 10;    // the rings of a SM
 
 constexpr int kWideBwd = 512 * 16;       // widest row of norm_bwd
 constexpr int kWideFwd = 256 * 64;       // widest row of norm_fwd
 
-// Threads a row and a CTA of norm_bwd, and the row ranges of a group (a batch
-// element with per_batch, else all rows): as many CTAs as stay resident.
+// How the backward pass runs, and the row ranges of a group (a batch element
+// with per_batch, else all rows): as many CTAs as stay resident.
 struct BwdShape {
-    int ept, tpr, threads, splits;
-    int slots;         // > 0: norm_bwd_warp with so many slots a warp
+    int wpr, slots;              // norm_bwd_team: warps a row (0: another form), slots a team
+    int ept, tpr, threads;       // norm_bwd
+    int splits;
 };
 BwdShape bwd_shape(const NormPlan &p, int esize) {
-    BwdShape b;
-    b.slots = 0;
-    if (p.C * esize % 16 == 0 && p.C <= kWarpRow) {
-        const long long rows = p.per_batch ? p.N : p.rows, groups = p.per_batch ? p.B : 1;
-        const int pair = 2 * p.C * esize;
-        b.threads = pair * 8 * 3 <= kWarpBytes ? 256 : 128;
-        b.slots = kWarpBytes / (pair * (b.threads / 32));
-        b.slots = b.slots < 2 ? 2 : (b.slots > kRing ? kRing : b.slots);
-        b.ept = p.C <= 256 ? 8 : (p.C <= 512 ? 16 : (p.C <= 1024 ? 32 : 64));
-        b.tpr = 32;
-        // narrow rows leave room for more CTAs a SM
-        const int per_sm = b.ept <= 16 ? 4 : (b.ept == 32 ? 2 : 1);
-        if (per_sm > 1) b.slots = b.slots / per_sm < 2 ? 2 : b.slots / per_sm;
-        long long s = (long long)kSmCount * per_sm / groups;
-        if (s > (rows + 31) / 32) s = (rows + 31) / 32;
+    BwdShape b{};
+    const long long rows = p.per_batch ? p.N : p.rows, groups = p.per_batch ? p.B : 1;
+    if (p.C * (long long)esize % 16 == 0 && p.C <= kWideBwd) {
+        // warps for 32 channels a lane, and two slots a team at least
+        const int pair = 2 * p.C * esize, warps = kBwdThreads / 32;
+        for (b.wpr = 1; 32 * kLane * b.wpr < p.C || warps / b.wpr * 2 * pair > kRingBytes; b.wpr *= 2) {}
+        b.slots = kRingBytes / (warps / b.wpr * pair);
+        if (b.slots > kRing) b.slots = kRing;
+        long long s = kSmCount / groups;
+        const int teams = warps / b.wpr;
+        if (s > (rows + 2 * teams - 1) / (2 * teams)) s = (rows + 2 * teams - 1) / (2 * teams);
         b.splits = (int)(s < 1 ? 1 : s);
         return b;
     }
@@ -766,7 +658,6 @@ BwdShape bwd_shape(const NormPlan &p, int esize) {
     b.tpr = ((p.C + b.ept - 1) / b.ept + 31) / 32 * 32;
     if (b.tpr > 512) b.tpr = 256;
     b.threads = b.tpr >= 256 ? b.tpr : 256 / b.tpr * b.tpr;
-    const long long rows = p.per_batch ? p.N : p.rows, groups = p.per_batch ? p.B : 1;
     const int resident = b.threads <= 256 ? 4 : 2;
     long long s = (long long)resident * kSmCount / groups;
     if (s > (rows + 7) / 8) s = (rows + 7) / 8;
@@ -774,16 +665,12 @@ BwdShape bwd_shape(const NormPlan &p, int esize) {
     return b;
 }
 
-constexpr int kRingBytes = 48 << 10;
-constexpr int kRingMost = 2 * 2 * kWideBwd * 4;   // two stages of the widest fp32 row
 template <typename T> bool g_norm_ready[128] = {};
 template <typename T> bool norm_setup() {
-    return set_smem((const void *)norm_bwd_warp<T, 8>, kWarpBytes) && set_smem((const void *)norm_bwd_warp<T, 16>, kWarpBytes) &&
-           set_smem((const void *)norm_bwd_warp<T, 32>, kWarpBytes) && set_smem((const void *)norm_bwd_warp<T, 64>, kWarpBytes) &&
-           set_smem((const void *)norm_fwd_ring<T, 32>, kWarpBytes / 2) && set_smem((const void *)norm_fwd_ring<T, 64>, kWarpBytes / 2) &&
-           set_smem((const void *)norm_bwd_ring<T, 16, 512>, kRingMost) &&
-           set_smem((const void *)norm_bwd_ring<T, 8, 512>, kRingMost) &&
-           set_smem((const void *)norm_bwd_ring<T, 8, 256>, kRingMost);
+    return set_smem((const void *)norm_bwd_team<T, 1>, kRingBytes) && set_smem((const void *)norm_bwd_team<T, 2>, kRingBytes) &&
+           set_smem((const void *)norm_bwd_team<T, 4>, kRingBytes) && set_smem((const void *)norm_bwd_team<T, 8>, kRingBytes) &&
+           set_smem((const void *)norm_bwd_team<T, 16>, kRingBytes) && set_smem((const void *)norm_fwd_ring<T, 32>, kRingBytes) &&
+           set_smem((const void *)norm_fwd_ring<T, 64>, kRingBytes);
 }
 
 template <typename T, int VEC, int EPT, int WPR>
@@ -809,13 +696,15 @@ int fwd_pick(const T *x, const T *w, const T *b, T *y, float *mean, float *rstd,
 template <typename T>
 int norm_fwd_t(const T *x, const T *w, const T *b, T *y, float *mean, float *rstd, const NormPlan &p, cudaStream_t s) {
     constexpr int V = 16 / sizeof(T);
-    if (p.C % V == 0 && p.C > 512 && p.C <= kWarpRow && p.rows >= 8 * 8 * kSmCount) {
-        const int per_sm = p.C <= 1024 ? 3 : 2, row = p.C * (int)sizeof(T);
-        int slots = kWarpBytes / per_sm / (8 * row);
-        slots = slots < 1 ? 1 : (slots > kRing ? kRing : slots);
+    // (from 4 rows a warp on; fewer, or narrower ones, are as fast without a ring)
+    constexpr int kWarps = kFwdThreads / 32;
+    if (p.C % V == 0 && p.C > 512 && p.C <= kWarpRow && p.rows >= 4LL * kWarps * kSmCount) {
+        const int row = p.C * (int)sizeof(T);
+        int slots = kRingBytes / (kWarps * row);
+        if (slots > kRing) slots = kRing;
         if (!once_per_device(&g_norm_ready<T>, norm_setup<T>)) return -1;
         auto f = p.C <= 1024 ? norm_fwd_ring<T, 32> : norm_fwd_ring<T, 64>;
-        f<<<per_sm * kSmCount, kThreads, 8 * slots * row, s>>>(x, w, b, y, mean, rstd, p, slots);
+        f<<<kSmCount, kFwdThreads, kWarps * slots * row, s>>>(x, w, b, y, mean, rstd, p, slots);
         return cudaGetLastError() == cudaSuccess ? 1 : -1;
     }
     if (p.C <= kWideFwd)
@@ -832,29 +721,21 @@ int norm_bwd_t(const T *dy, const T *x, const T *w, const float *mean, const flo
     const BwdShape b = bwd_shape(p, sizeof(T));
     const int groups = p.per_batch ? p.B : 1;
     if (!dw && !db) part = nullptr;
-    if (b.slots) {
-        const int rings = b.slots * (b.threads / 32) * 2 * p.C * (int)sizeof(T), sums = 2 * p.C * 4;
+    const unsigned grid = (unsigned)(groups * b.splits);
+    if (b.wpr) {
+        const int rings = b.slots * (kBwdThreads / 32 / b.wpr) * 2 * p.C * (int)sizeof(T), sums = 2 * p.C * 4;
         if (!once_per_device(&g_norm_ready<T>, norm_setup<T>)) return -1;
-        auto f = b.ept == 8 ? norm_bwd_warp<T, 8> : (b.ept == 16 ? norm_bwd_warp<T, 16> : (b.ept == 32 ? norm_bwd_warp<T, 32> : norm_bwd_warp<T, 64>));
-        f<<<(unsigned)(groups * b.splits), b.threads, rings > sums ? rings : sums, s>>>(dy, x, w, mean, rstd, dx, part, p, b.splits, b.slots);
+        auto f = b.wpr == 1   ? norm_bwd_team<T, 1>
+                 : b.wpr == 2 ? norm_bwd_team<T, 2>
+                 : b.wpr == 4 ? norm_bwd_team<T, 4>
+                 : b.wpr == 8 ? norm_bwd_team<T, 8>
+                              : norm_bwd_team<T, 16>;
+        f<<<grid, kBwdThreads, rings > sums ? rings : sums, s>>>(dy, x, w, mean, rstd, dx, part, p, b.splits, b.slots);
     } else if (p.C <= kWideBwd) {
         // the CTA's pieces at the end, or two rounds of two sums a warp
         const int smem = b.threads > b.tpr ? b.threads * 2 * b.ept * 4 : b.threads / 32 * 16;
-        const unsigned grid = (unsigned)(groups * b.splits);
-        if (p.C % V == 0) {
-            // a stage is two pieces of TY rows; about 48 KiB of them, so that every resident CTA has its own
-            const int stage = 2 * (b.threads / b.tpr) * p.C * (int)sizeof(T);
-            int stages = kRingBytes / stage;
-            stages = stages < 2 ? 2 : (stages > kRing ? kRing : stages);
-            const int sums = b.threads > b.tpr ? b.threads * 2 * b.ept * 4 : 0;
-            const int bytes = stages * stage > sums ? stages * stage : sums;
-            if (!once_per_device(&g_norm_ready<T>, norm_setup<T>)) return -1;
-            auto f = b.ept == 16 ? norm_bwd_ring<T, 16, 512> : (b.threads > 256 ? norm_bwd_ring<T, 8, 512> : norm_bwd_ring<T, 8, 256>);
-            f<<<grid, b.threads, bytes, s>>>(dy, x, w, mean, rstd, dx, part, p, b.tpr, b.splits, stages);
-        } else {
-            auto f = b.ept == 16 ? norm_bwd<T, 16, 512> : (b.threads > 256 ? norm_bwd<T, 8, 512> : norm_bwd<T, 8, 256>);
-            f<<<grid, b.threads, smem, s>>>(dy, x, w, mean, rstd, dx, part, p, b.tpr, b.splits);
-        }
+        auto f = b.ept == 16 ? norm_bwd<T, 16, 512> : (b.threads > 256 ? norm_bwd<T, 8, 512> : norm_bwd<T, 8, 256>);
+        f<<<grid, b.threads, smem, s>>>(dy, x, w, mean, rstd, dx, part, p, b.tpr, b.splits);
     } else {
         const long long grid = p.rows < (1 << 30) ? p.rows : (1 << 30);
         norm_dx_wide<T><<<(unsigned)grid, kThreads, 0, s>>>(dy, x, w, mean, rstd, dx, p);
