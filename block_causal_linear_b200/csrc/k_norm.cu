@@ -29,6 +29,28 @@ struct alignas(sizeof(T) * VEC) Pack {
     T v[VEC];
 };
 
+// Elements j and j + 1 (j even) as floats, and back: a bf16 pair is one word, so
+// that reading it is two instructions and writing it one (element by element
+// it was six).
+template <typename T, int VEC>
+__device__ __forceinline__ float2 get2(const Pack<T, VEC> &p, int j) {
+    if constexpr (sizeof(T) == 2) {
+        const uint32_t w = reinterpret_cast<const uint32_t *>(&p)[j / 2];
+        return make_float2(bf_lo(w), bf_hi(w));
+    } else {
+        return make_float2(p.v[j], p.v[j + 1]);
+    }
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void set2(Pack<T, VEC> &p, int j, float2 f) {
+    if constexpr (sizeof(T) == 2) {
+        reinterpret_cast<uint32_t *>(&p)[j / 2] = pack_bf2(f.x, f.y);
+    } else {
+        p.v[j] = f.x;
+        p.v[j + 1] = f.y;
+    }
+}
+
 template <typename T, int VEC>
 __device__ __forceinline__ Pack<T, VEC> load_pack(const T *p) { return *reinterpret_cast<const Pack<T, VEC> *>(p); }
 
@@ -133,12 +155,13 @@ norm_fwd_ring(const T *__restrict__ x, const T *__restrict__ w, const T *__restr
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int c = (k * 32 + lane) * VEC;
-            P u;
-            if (c < p.C) u = load_pack<T, VEC>(xs + c);
+            if (c < p.C) {
+                const P u = load_pack<T, VEC>(xs + c);
 #pragma unroll
-            for (int j = 0; j < VEC; j += 2) {
-                v[(k * VEC + j) / 2] = c < p.C ? make_float2(to_f(u.v[j]), to_f(u.v[j + 1])) : make_float2(0.f, 0.f);
-                s2 = fadd2(s2, v[(k * VEC + j) / 2]);
+                for (int j = 0; j < VEC; j += 2) {
+                    v[(k * VEC + j) / 2] = get2(u, j);
+                    s2 = fadd2(s2, v[(k * VEC + j) / 2]);
+                }
             }
         }
         __syncwarp();
@@ -166,10 +189,9 @@ norm_fwd_ring(const T *__restrict__ x, const T *__restrict__ w, const T *__restr
 #pragma unroll
                 for (int j = 0; j < VEC; j += 2) {
                     float2 f = fmul2(v[(k * VEC + j) / 2], make_float2(rstd, rstd));
-                    if (w) f = fmul2(f, make_float2(to_f(wv.v[j]), to_f(wv.v[j + 1])));
-                    if (b) f = fadd2(f, make_float2(to_f(bv.v[j]), to_f(bv.v[j + 1])));
-                    o.v[j] = from_f<T>(f.x);
-                    o.v[j + 1] = from_f<T>(f.y);
+                    if (w) f = fmul2(f, get2(wv, j));
+                    if (b) f = fadd2(f, get2(bv, j));
+                    set2(o, j, f);
                 }
                 *reinterpret_cast<P *>(y + r * p.C + c) = o;
             }
@@ -248,9 +270,9 @@ norm_bwd_team(const T *__restrict__ dy, const T *__restrict__ x, const T *__rest
 #pragma unroll
                 for (int j = 0; j < VEC; j += 2) {
                     const int e = (k * VEC + j) / 2;
-                    const float2 xh = ffma2(make_float2(to_f(xp.v[j]), to_f(xp.v[j + 1])), make_float2(rs, rs), make_float2(nm, nm));
-                    const float2 d = make_float2(to_f(dp.v[j]), to_f(dp.v[j + 1]));
-                    const float2 gi = fmul2(d, make_float2(to_f(wk[k].v[j]), to_f(wk[k].v[j + 1])));
+                    const float2 xh = ffma2(get2(xp, j), make_float2(rs, rs), make_float2(nm, nm));
+                    const float2 d = get2(dp, j);
+                    const float2 gi = fmul2(d, get2(wk[k], j));
                     s1 = fadd2(s1, gi);
                     s2 = ffma2(gi, xh, s2);
                     aw[e] = ffma2(d, xh, aw[e]);
@@ -283,11 +305,10 @@ norm_bwd_team(const T *__restrict__ dy, const T *__restrict__ x, const T *__rest
                 P o;
 #pragma unroll
                 for (int j = 0; j < VEC; j += 2) {
-                    const float2 xh = ffma2(make_float2(to_f(xp.v[j]), to_f(xp.v[j + 1])), make_float2(rs, rs), make_float2(nm, nm));
-                    const float2 gi = ffma2(make_float2(to_f(dp.v[j]), to_f(dp.v[j + 1])), make_float2(to_f(wk[k].v[j]), to_f(wk[k].v[j + 1])), make_float2(-t1, -t1));
+                    const float2 xh = ffma2(get2(xp, j), make_float2(rs, rs), make_float2(nm, nm));
+                    const float2 gi = ffma2(get2(dp, j), get2(wk[k], j), make_float2(-t1, -t1));
                     const float2 f = fmul2(ffma2(xh, make_float2(-t2, -t2), gi), make_float2(rs, rs));
-                    o.v[j] = from_f<T>(f.x);
-                    o.v[j + 1] = from_f<T>(f.y);
+                    set2(o, j, f);
                 }
                 *reinterpret_cast<P *>(dx + r * p.C + c) = o;
             }
