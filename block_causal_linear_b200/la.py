@@ -581,14 +581,22 @@ def _launch(name, fn, device, stream, *args):
         raise LAError(rc, name)
 
 
-def _empty(shape, dtype, device, stream):
-    """torch.empty whose memory belongs to the stream that will use it (a
-    buffer freed by the caller is then not handed out while that stream's
-    kernels still use it)."""
+def _like(t, stream):
+    """An uninitialised tensor like the contiguous t, whose memory belongs to the
+    stream that will use it (a buffer freed by the caller is then not handed
+    out while that stream's kernels still use it)."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty_like(t)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty_like(t)
+
+
+def _new(t, shape, stream, dtype=None):
+    """The same of another shape, of t's dtype or another, on t's device."""
+    if stream is None:
+        return t.new_empty(shape, dtype=dtype)
+    with torch.cuda.stream(stream):
+        return t.new_empty(shape, dtype=dtype)
 
 
 @functools.lru_cache(maxsize=4096)
@@ -602,15 +610,14 @@ def _ptr(t):
 
 
 def _check_like(name, t, shape, dtype, device):
-    """t is None, or a contiguous CUDA tensor of this shape, dtype and device."""
-    if t is None:
+    """t is a contiguous CUDA tensor of this shape, dtype and device (or None)."""
+    if t is None or (t.shape == shape and t.dtype == dtype and t.device == device and t.is_contiguous()):
         return
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous tensor on {device}")
+    raise ValueError(f"{name} must be a contiguous tensor on {device}")
 
 
 def _check_main(name, t, dims):
@@ -626,26 +633,28 @@ def _check_stream(device, stream):
         raise ValueError(f"the stream belongs to {stream.device}, the tensors to {device}")
 
 
-def _workspace(name, sizes, ws, device, stream):
+def _workspace(name, sizes, ws, like, stream):
     n = _ws_bytes(name, *sizes)
     if n == 0:
         raise LAError(LA_EINVAL, name)
     if ws is None:
-        return _empty(n, torch.uint8, device, stream)
-    if ws.device != device or not ws.is_contiguous():
-        raise ValueError(f"ws must be a contiguous tensor on {device}")
+        return _new(like, n, stream, torch.uint8)
+    if ws.device != like.device or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous tensor on {like.device}")
     return ws
 
 
 def _norm_sizes(x, weight, bias):
     """(B, N, C, per_batch) of x [..., C]; a [B, C] weight or bias has one vector per x[b]."""
     C = x.shape[-1]
-    vecs = [t for t in (weight, bias) if t is not None]
-    per_batch = bool(vecs) and vecs[0].dim() == 2
+    vec = weight if weight is not None else bias
+    per_batch = vec is not None and vec.dim() == 2
     B = x.shape[0] if per_batch or x.dim() == 3 else 1
     N = x.numel() // (B * C)
-    for name, t in (("weight", weight), ("bias", bias)):
-        _check_like(name, t, (B, C) if per_batch else (C,), x.dtype, x.device)
+    if vec is not None:
+        shape, dtype, device = (B, C) if per_batch else (C,), x.dtype, x.device
+        _check_like("weight", weight, shape, dtype, device)
+        _check_like("bias", bias, shape, dtype, device)
     return B, N, C, int(per_batch)
 
 
@@ -657,15 +666,19 @@ def layer_norm_forward(x, weight=None, bias=None, eps=1e-6, return_stats=False, 
     dt = _check_main("x", x, (2, 3))
     B, N, C, pb = _norm_sizes(x, weight, bias)
     _check_stream(x.device, stream)
-    _check_like("out", out, x.shape, x.dtype, x.device)
-    y = _empty(x.shape, x.dtype, x.device, stream) if out is None else out
+    if out is None:
+        y = _like(x, stream)
+    else:
+        _check_like("out", out, x.shape, x.dtype, x.device)
+        y = out
     mean = rstd = None
     if stats is not None:
         mean, rstd = stats
+        _check_like("mean", mean, x.shape[:-1], torch.float32, x.device)
+        _check_like("rstd", rstd, x.shape[:-1], torch.float32, x.device)
     elif return_stats:
-        mean, rstd = (_empty(x.shape[:-1], torch.float32, x.device, stream) for _ in range(2))
-    for name, t in (("mean", mean), ("rstd", rstd)):
-        _check_like(name, t, x.shape[:-1], torch.float32, x.device)
+        mean = _new(x, x.shape[:-1], stream, torch.float32)
+        rstd = _like(mean, stream)
     _launch("la_layer_norm_forward", lib().la_layer_norm_forward, x.device, stream, x.data_ptr(), _ptr(weight),
             _ptr(bias), y.data_ptr(), _ptr(mean), _ptr(rstd), dt, B, N, C, pb, float(eps))
     return (y, mean, rstd) if return_stats else y
@@ -686,22 +699,24 @@ def layer_norm_backward(dy, x, weight, mean, rstd, per_batch=None, weight_grad=T
         B, N = x.shape[0], x.numel() // (x.shape[0] * C)
     _check_stream(x.device, stream)
     _check_like("dy", dy, x.shape, x.dtype, x.device)
-    for name, t in (("mean", mean), ("rstd", rstd)):
-        if t is None:
-            raise ValueError(f"{name} is missing (layer_norm_forward with return_stats gives it)")
-        _check_like(name, t, x.shape[:-1], torch.float32, x.device)
+    if mean is None or rstd is None:
+        raise ValueError("mean or rstd is missing (layer_norm_forward with return_stats gives them)")
+    lead = x.shape[:-1]
+    _check_like("mean", mean, lead, torch.float32, x.device)
+    _check_like("rstd", rstd, lead, torch.float32, x.device)
     vec = (B, C) if pb else (C,)
     if grads is None:
-        grads = (_empty(x.shape, x.dtype, x.device, stream),
-                 _empty(vec, x.dtype, x.device, stream) if weight_grad else None,
-                 _empty(vec, x.dtype, x.device, stream) if bias_grad else None)
-    dx, dw, db = grads
-    for name, t, shape in (("dx", dx, x.shape), ("dweight", dw, vec), ("dbias", db, vec)):
-        _check_like(name, t, shape, x.dtype, x.device)
-    if dx is None:
-        raise ValueError("dx is missing")
+        dx = _like(x, stream)
+        dw = _new(x, vec, stream) if weight_grad else None
+        db = _new(x, vec, stream) if bias_grad else None
+    else:
+        dx, dw, db = grads
+        if dx is None:
+            raise ValueError("dx is missing")
+        for name, t, shape in (("dx", dx, x.shape), ("dweight", dw, vec), ("dbias", db, vec)):
+            _check_like(name, t, shape, x.dtype, x.device)
     if dw is not None or db is not None:
-        ws = _workspace("la_layer_norm_backward_workspace_size", (B, N, C, pb), ws, x.device, stream)
+        ws = _workspace("la_layer_norm_backward_workspace_size", (B, N, C, pb), ws, x, stream)
     _launch("la_layer_norm_backward", lib().la_layer_norm_backward, x.device, stream, dy.data_ptr(), x.data_ptr(),
             _ptr(weight), mean.data_ptr(), rstd.data_ptr(), dx.data_ptr(), _ptr(dw), _ptr(db), dt, B, N, C, pb,
             _ptr(ws), 0 if ws is None else ws.nbytes)
@@ -738,12 +753,13 @@ def linear_forward(x, weight, bias=None, act="none", residual=None, return_pre=F
     shape = (*x.shape[:-1], N)
     _check_stream(x.device, stream)
     _check_like("bias", bias, (N,), x.dtype, x.device)
-    for name, t in (("residual", residual), ("out", out), ("pre", pre)):
-        _check_like(name, t, shape, x.dtype, x.device)
-    y = _empty(shape, x.dtype, x.device, stream) if out is None else out
+    _check_like("residual", residual, shape, x.dtype, x.device)
+    _check_like("out", out, shape, x.dtype, x.device)
+    _check_like("pre", pre, shape, x.dtype, x.device)
+    y = _new(x, shape, stream) if out is None else out
     if return_pre and pre is None and code:
-        pre = _empty(shape, x.dtype, x.device, stream)
-    ws = _workspace("la_linear_workspace_size", (R, K, N, dt), ws, x.device, stream)
+        pre = _like(y, stream)
+    ws = _workspace("la_linear_workspace_size", (R, K, N, dt), ws, x, stream)
     _launch("la_linear_forward", lib().la_linear_forward, x.device, stream, x.data_ptr(), weight.data_ptr(), _ptr(bias),
             _ptr(residual), y.data_ptr(), _ptr(pre), dt, code, R, K, N, ws.data_ptr(), ws.nbytes)
     return (y, pre) if return_pre else y
@@ -763,13 +779,14 @@ def linear_backward(dy, x, weight, pre=None, act="none", input_grad=True, weight
     if code and pre is None:
         raise ValueError("pre is missing (linear_forward with return_pre gives it)")
     if grads is None:
-        grads = (_empty(x.shape, x.dtype, x.device, stream) if input_grad else None,
-                 _empty((N, K), x.dtype, x.device, stream) if weight_grad else None,
-                 _empty((N,), x.dtype, x.device, stream) if bias_grad else None)
-    dx, dw, db = grads
-    for name, t, sh in (("dx", dx, x.shape), ("dweight", dw, (N, K)), ("dbias", db, (N,))):
-        _check_like(name, t, sh, x.dtype, x.device)
-    ws = _workspace("la_linear_backward_workspace_size", (R, K, N, dt, code), ws, x.device, stream)
+        dx = _like(x, stream) if input_grad else None
+        dw = _like(weight, stream) if weight_grad else None
+        db = _new(x, N, stream) if bias_grad else None
+    else:
+        dx, dw, db = grads
+        for name, t, sh in (("dx", dx, x.shape), ("dweight", dw, (N, K)), ("dbias", db, (N,))):
+            _check_like(name, t, sh, x.dtype, x.device)
+    ws = _workspace("la_linear_backward_workspace_size", (R, K, N, dt, code), ws, x, stream)
     _launch("la_linear_backward", lib().la_linear_backward, x.device, stream, dy.data_ptr(), x.data_ptr(),
             weight.data_ptr(), _ptr(pre), _ptr(dx), _ptr(dw), _ptr(db), dt, code, R, K, N, ws.data_ptr(), ws.nbytes)
     return dx, dw, db
@@ -816,12 +833,12 @@ def cross_attention_forward(q, k, v, kv_len=None, scale=None, return_lse=False, 
     _check_stream(q.device, stream)
     _check_like("out", out, q.shape, q.dtype, q.device)
     _check_like("lse", lse, (B, H, N), torch.float32, q.device)
-    o = _empty(q.shape, q.dtype, q.device, stream) if out is None else out
+    o = _like(q, stream) if out is None else out
     if return_lse and lse is None:
-        lse = _empty((B, H, N), torch.float32, q.device, stream)
+        lse = _new(q, (B, H, N), stream, torch.float32)
     if d not in (32, 64):
         raise LAError(LA_EUNSUPPORTED, "la_cross_attention_forward")
-    ws = _workspace("la_cross_attention_workspace_size", (dt, B, N, M, H, d), ws, q.device, stream)
+    ws = _workspace("la_cross_attention_workspace_size", (dt, B, N, M, H, d), ws, q, stream)
     _launch("la_cross_attention_forward", lib().la_cross_attention_forward, q.device, stream, q.data_ptr(), k.data_ptr(),
             v.data_ptr(), _ptr(kv_len), o.data_ptr(), _ptr(lse), dt, B, N, M, H, d, ldk, ldv, sc, ws.data_ptr(),
             ws.nbytes)
@@ -834,18 +851,22 @@ def cross_attention_backward(q, k, v, out, lse, dout, kv_len=None, scale=None, w
     be views of a wider tensor, as k and v."""
     dt, B, N, M, H, d, ldk, ldv, sc = _cross_sizes(q, k, v, kv_len, scale)
     _check_stream(q.device, stream)
-    for name, t in (("out", out), ("dout", dout)):
-        _check_like(name, t, q.shape, q.dtype, q.device)
+    if out is None or lse is None or dout is None:
+        raise ValueError("out, lse (of cross_attention_forward with return_lse) and dout are needed")
+    _check_like("out", out, q.shape, q.dtype, q.device)
+    _check_like("dout", dout, q.shape, q.dtype, q.device)
     _check_like("lse", lse, (B, H, N), torch.float32, q.device)
     if grads is None:
-        grads = (_empty(q.shape, q.dtype, q.device, stream),
-                 *(_empty((B, M, H, d), q.dtype, q.device, stream) for _ in range(2)))
-    dq, dk, dv = grads
-    _check_like("dq", dq, q.shape, q.dtype, q.device)
-    lddk, lddv = _check_states("dk", dk, q, M), _check_states("dv", dv, q, M)
+        dq, dk, dv, lddk, lddv = _like(q, stream), *(_new(q, (B, M, H, d), stream) for _ in range(2)), H * d, H * d
+    else:
+        dq, dk, dv = grads
+        if dq is None or dk is None or dv is None:
+            raise ValueError("dq, dk and dv are all written")
+        _check_like("dq", dq, q.shape, q.dtype, q.device)
+        lddk, lddv = _check_states("dk", dk, q, M), _check_states("dv", dv, q, M)
     if d not in (32, 64):
         raise LAError(LA_EUNSUPPORTED, "la_cross_attention_backward")
-    ws = _workspace("la_cross_attention_backward_workspace_size", (dt, B, N, M, H, d), ws, q.device, stream)
+    ws = _workspace("la_cross_attention_backward_workspace_size", (dt, B, N, M, H, d), ws, q, stream)
     _launch("la_cross_attention_backward", lib().la_cross_attention_backward, q.device, stream, q.data_ptr(),
             k.data_ptr(), v.data_ptr(), _ptr(kv_len), out.data_ptr(), lse.data_ptr(), dout.data_ptr(), dq.data_ptr(),
             dk.data_ptr(), dv.data_ptr(), dt, B, N, M, H, d, ldk, ldv, lddk, lddv, sc, ws.data_ptr(), ws.nbytes)
