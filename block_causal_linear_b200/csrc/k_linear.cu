@@ -1,18 +1,13 @@
 // k_linear.cu -- the parts of the linear layer that run on the CUDA cores:
-// fp32 matrix products, products with few rows, the activation's derivative
-// and column sums.
+// products with few rows, the activation's derivative and column sums.
 //
 //   C[m][n] = sum_k A(m, k) B(n, k);  z = C + bias;  pre = z;  y = act(z) + residual
-// The three products of a linear layer are this one with other layouts:
-// forward A = x, B = W; dx: A = dz, B = W read along its rows; dW: both read
-// along their rows.
 #include "la_dit.cuh"
-#include "la_sm100.cuh"
 
 namespace la {
 namespace {
 
-constexpr int kBK = 16, kThreads = 256;
+constexpr int kThreads = 256;
 
 template <typename T>
 __device__ __forceinline__ void epilogue(const GemmPlan &g, long long m, long long n, float z) {
@@ -22,87 +17,6 @@ __device__ __forceinline__ void epilogue(const GemmPlan &g, long long m, long lo
     z = act_f(z, g.act);
     if (g.res) z += to_f(((const T *)g.res)[o]);
     ((T *)g.y)[o] = from_f<T>(z);
-}
-
-// fp32 products: BT x BT tiles, BT/16 x BT/16 outputs a thread, the next 16 k
-// loaded into registers while the current ones are multiplied.  Two fused
-// multiply-adds an instruction.  AMN / BMN: the operand's m (n) index is contiguous.
-template <int BT, bool AMN, bool BMN>
-__global__ void __launch_bounds__(kThreads)
-gemm_f32(const GemmPlan g) {
-    constexpr int TM = BT / 16, LD = BT * kBK / kThreads;
-    __shared__ float sa[2][kBK][BT + 4], sb[2][kBK][BT + 4];
-    const float *A = (const float *)g.a, *B = (const float *)g.b;
-    const long long nt = (g.N + BT - 1) / BT;
-    const long long m0 = (long long)blockIdx.x / nt * BT, n0 = (long long)blockIdx.x % nt * BT;
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    float2 acc[TM][TM / 2];
-#pragma unroll
-    for (int i = 0; i < TM; ++i)
-#pragma unroll
-        for (int j = 0; j < TM / 2; ++j) acc[i][j] = make_float2(0.f, 0.f);
-    float ra[LD], rb[LD];
-    auto fetch = [&](long long k0) {
-#pragma unroll
-        for (int i = 0; i < LD; ++i) {
-            const int e = threadIdx.x + i * kThreads;
-            const int m = AMN ? e % BT : e / kBK, ka = AMN ? e / BT : e % kBK;
-            const int n = BMN ? e % BT : e / kBK, kb = BMN ? e / BT : e % kBK;
-            ra[i] = m0 + m < g.M && k0 + ka < g.K ? (AMN ? A[(k0 + ka) * g.lda + m0 + m] : A[(m0 + m) * g.lda + k0 + ka]) : 0.f;
-            rb[i] = n0 + n < g.N && k0 + kb < g.K ? (BMN ? B[(k0 + kb) * g.ldb + n0 + n] : B[(n0 + n) * g.ldb + k0 + kb]) : 0.f;
-        }
-    };
-    auto put = [&](int buf) {
-#pragma unroll
-        for (int i = 0; i < LD; ++i) {
-            const int e = threadIdx.x + i * kThreads;
-            sa[buf][AMN ? e / BT : e % kBK][AMN ? e % BT : e / kBK] = ra[i];
-            sb[buf][BMN ? e / BT : e % kBK][BMN ? e % BT : e / kBK] = rb[i];
-        }
-    };
-    fetch(0);
-    put(0);
-    __syncthreads();
-    int buf = 0;
-    for (long long k0 = 0; k0 < g.K; k0 += kBK, buf ^= 1) {
-        if (k0 + kBK < g.K) fetch(k0 + kBK);
-#pragma unroll
-        for (int k = 0; k < kBK; ++k) {
-            float a[TM];
-            float2 b[TM / 2];
-            // columns and rows in groups of 4, 64 apart: whole 16-byte reads without bank conflicts
-#pragma unroll
-            for (int i = 0; i < TM / 4; ++i) {
-                const float4 t = *reinterpret_cast<const float4 *>(&sa[buf][k][i * 64 + ty * 4]);
-                a[4 * i] = t.x, a[4 * i + 1] = t.y, a[4 * i + 2] = t.z, a[4 * i + 3] = t.w;
-                const float4 u = *reinterpret_cast<const float4 *>(&sb[buf][k][i * 64 + tx * 4]);
-                b[2 * i] = make_float2(u.x, u.y), b[2 * i + 1] = make_float2(u.z, u.w);
-            }
-#pragma unroll
-            for (int i = 0; i < TM; ++i)
-#pragma unroll
-                for (int j = 0; j < TM / 2; ++j) acc[i][j] = sm100::ffma2(make_float2(a[i], a[i]), b[j], acc[i][j]);
-        }
-        if (k0 + kBK < g.K) put(buf ^ 1);
-        __syncthreads();
-    }
-#pragma unroll
-    for (int i = 0; i < TM; ++i)
-#pragma unroll
-        for (int j = 0; j < TM; ++j) {
-            const long long m = m0 + i / 4 * 64 + ty * 4 + i % 4, n = n0 + j / 4 * 64 + tx * 4 + j % 4;
-            if (m < g.M && n < g.N) epilogue<float>(g, m, n, j & 1 ? acc[i][j / 2].y : acc[i][j / 2].x);
-        }
-}
-
-template <int BT>
-int gemm_f32_t(const GemmPlan &g, cudaStream_t s) {
-    const long long grid = ((g.M + BT - 1) / BT) * ((g.N + BT - 1) / BT);
-    if (grid > 0x7fffffffLL) return -1;
-    auto f = g.a_mn ? (g.b_mn ? gemm_f32<BT, true, true> : gemm_f32<BT, true, false>)
-                    : (g.b_mn ? gemm_f32<BT, false, true> : gemm_f32<BT, false, false>);
-    f<<<(unsigned)grid, kThreads, 0, s>>>(g);
-    return cudaGetLastError() == cudaSuccess ? 1 : -1;
 }
 
 // Products with at most 8 rows, both operands k-contiguous: the weight's bytes
@@ -228,12 +142,6 @@ int act_col_t(const void *dy, const void *pre, void *dz, float *part, long long 
 }
 
 }  // namespace
-
-int launch_gemm_f32(const GemmPlan &g, cudaStream_t s) {
-    // 128-wide tiles (8 x 8 outputs a thread) where they fill the GPU
-    const long long big = ((g.M + 127) / 128) * ((g.N + 127) / 128);
-    return big >= kSmCount ? gemm_f32_t<128>(g, s) : gemm_f32_t<64>(g, s);
-}
 
 int launch_gemm_rows(int is_bf16, const GemmPlan &g, cudaStream_t s) {
     if (is_bf16) return g.K % 8 == 0 ? rows_r<__nv_bfloat16, 8>(g, s) : rows_r<__nv_bfloat16, 1>(g, s);

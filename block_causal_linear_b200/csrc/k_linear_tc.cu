@@ -1,5 +1,5 @@
-// k_linear_tc.cu -- bf16 matrix products with a fused epilogue on the tensor
-// cores (tcgen05, accumulators in TMEM, operands by TMA).
+// k_linear_tc.cu -- matrix products with a fused epilogue on the tensor cores
+// (tcgen05, accumulators in TMEM, operands by TMA), of bf16 and of fp32.
 //
 //   C[m][n] = sum_k A(m, k) B(n, k);  z = C + bias;  pre = z;  y = act(z) + residual
 //
@@ -14,8 +14,14 @@
 // boxes of 64 rows x 64 k): the three products of a linear layer need no
 // transposed copies.  The residual arrives and the outputs leave by TMA
 // through per-warp buffers of 32 x 32.
+// fp32 operands are split into three bf16 parts each, x = hi + mid + lo exactly
+// (24 bits), and the product is the sum of the six part products down to 2^-24
+// of it: lo hi, hi lo, mid mid, mid hi, hi mid, hi hi, accumulated in fp32 one
+// after another along k.  Six products at the tensor cores' bf16 rate are three
+// times what the CUDA cores' fp32 units can do.
 #include <cudaTypedefs.h>
 #include <mutex>
+#include <type_traits>
 
 #include "la_sm100_dit.cuh"
 
@@ -53,6 +59,7 @@ struct TcArgs {
     int kiters;              // K in stages of 64
     int mt, nt;
     int tail, splits, kper;  // tiles from `tail` on are cut into `splits` pieces of kper stages each
+    int kblk;                // fp32: stages of one part product
     int a_mn, b_mn;
     const __nv_bfloat16 *bias, *res;
     __nv_bfloat16 *pre, *y;
@@ -87,7 +94,7 @@ struct Work {
 __device__ __forceinline__ Work work_of(const TcArgs &a, int w) {
     if (w < a.tail) return {w, -1, 0, a.kiters};
     const int i = w - a.tail, piece = i % a.splits, k0 = piece * a.kper;
-    return {a.tail + i / a.splits, a.splits > 1 ? piece : -1, k0, k0 + a.kper < a.kiters ? k0 + a.kper : a.kiters};
+    return {a.tail + i / a.splits, piece, k0, k0 + a.kper < a.kiters ? k0 + a.kper : a.kiters};
 }
 
 // act over a chunk, the choice made once
@@ -117,7 +124,9 @@ __device__ __forceinline__ void put_chunk(uint8_t *buf, const float (&v)[32], in
                        pack_bf2(v[8 * j + 4], v[8 * j + 5]), pack_bf2(v[8 * j + 6], v[8 * j + 7]));
 }
 
-template <int BN, int CG>
+// PARTS: the operands are three bf16 planes each (maps of three dimensions),
+// the k stages run through the six part products; all tiles leave their sums.
+template <int BN, int CG, bool PARTS>
 __global__ void __launch_bounds__(kThreads, 1)
 gemm_tc(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
         const __grid_constant__ CUtensorMap tm_y, const __grid_constant__ CUtensorMap tm_pre,
@@ -180,21 +189,26 @@ gemm_tc(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtens
                 if (one) {
                     // the leader's barrier counts both CTAs' copies
                     if (rank == 0) mbar_arrive_expect_tx(&full[s], CG * C::kStage);
-                    auto load = [&](void *dst, const CUtensorMap *m, int c0, int c1) {
-                        if constexpr (CG == 2) tma_load_2d_pair(dst, m, &full[s], c0, c1);
+                    // (0, 1, 2: hi, mid, lo; the products of smaller parts first)
+                    const int seg = PARTS ? k / a.kblk : 0, kc = (PARTS ? k - seg * a.kblk : k) * kBK;
+                    const int pa = PARTS ? (0x201100 >> (4 * (5 - seg))) & 15 : 0, pb = PARTS ? (0x021010 >> (4 * (5 - seg))) & 15 : 0;
+                    auto load = [&](void *dst, const CUtensorMap *m, int c0, int c1, int part) {
+                        if constexpr (PARTS && CG == 2) tma_load_3d_pair(dst, m, &full[s], c0, c1, part);
+                        else if constexpr (PARTS) tma_load_3d(dst, m, &full[s], c0, c1, part);
+                        else if constexpr (CG == 2) tma_load_2d_pair(dst, m, &full[s], c0, c1);
                         else tma_load_2d(dst, m, &full[s], c0, c1);
                     };
                     if (a.a_mn) {
-                        load(sa, &tm_a, m0, k * kBK);
-                        load(sa + 8192, &tm_a, m0 + 64, k * kBK);
+                        load(sa, &tm_a, m0, kc, pa);
+                        load(sa + 8192, &tm_a, m0 + 64, kc, pa);
                     } else {
-                        load(sa, &tm_a, k * kBK, m0);
+                        load(sa, &tm_a, kc, m0, pa);
                     }
                     if (a.b_mn) {
 #pragma unroll
-                        for (int j = 0; j < C::kBRows / 64; ++j) load(sb + j * 8192, &tm_b, n0 + j * 64, k * kBK);
+                        for (int j = 0; j < C::kBRows / 64; ++j) load(sb + j * 8192, &tm_b, n0 + j * 64, kc, pb);
                     } else {
-                        load(sb, &tm_b, k * kBK, n0);
+                        load(sb, &tm_b, kc, n0, pb);
                     }
                 }
                 __syncwarp();
@@ -378,7 +392,7 @@ gemm_tc(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtens
 
 // y, pre of the tail tiles from their pieces' sums, in piece order: a thread 4
 // columns, a CTA 1024 outputs of one tile.
-template <int BN, int CG>
+template <typename T, int BN, int CG>
 __global__ void __launch_bounds__(256)
 gemm_finish(const TcArgs a) {
     pdl_wait();
@@ -396,39 +410,60 @@ gemm_finish(const TcArgs a) {
     }
     float z[4] = {s.x, s.y, s.z, s.w};
     const long long e = m * a.N + n;
-    if (a.N % 4 == 0) {                                         // whole 8-byte groups
-        auto get = [&](const __nv_bfloat16 *p, float (&f)[4]) {
-            const uint2 u = *reinterpret_cast<const uint2 *>(p);
-            f[0] = bf_lo(u.x), f[1] = bf_hi(u.x), f[2] = bf_lo(u.y), f[3] = bf_hi(u.y);
+    const T *bias = (const T *)a.bias, *res = (const T *)a.res;
+    T *pre = (T *)a.pre, *y = (T *)a.y;
+    if (a.N % 4 == 0) {                                         // whole groups of four
+        struct alignas(4 * sizeof(T)) Four {
+            T v[4];
         };
-        auto put = [&](__nv_bfloat16 *p) { *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf2(z[0], z[1]), pack_bf2(z[2], z[3])); };
-        float f[4];
-        if (a.bias) {
-            get(a.bias + n, f);
+        auto add = [&](const T *p) {
+            const Four f = *reinterpret_cast<const Four *>(p);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) z[j] += f[j];
-        }
-        if (a.pre) put(a.pre + e);
+            for (int j = 0; j < 4; ++j) z[j] += to_f(f.v[j]);
+        };
+        auto put = [&](T *p) {
+            Four f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f.v[j] = from_f<T>(z[j]);
+            *reinterpret_cast<Four *>(p) = f;
+        };
+        if (bias) add(bias + n);
+        if (pre) put(pre + e);
 #pragma unroll
         for (int j = 0; j < 4; ++j) z[j] = act_f(z[j], a.act);
-        if (a.res) {
-            get(a.res + e, f);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) z[j] += f[j];
-        }
-        put(a.y + e);
+        if (res) add(res + e);
+        put(y + e);
         return;
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         if (n + j >= a.N) break;
         float f = z[j];
-        if (a.bias) f += __bfloat162float(a.bias[n + j]);
-        if (a.pre) a.pre[e + j] = __float2bfloat16_rn(f);
+        if (bias) f += to_f(bias[n + j]);
+        if (pre) pre[e + j] = from_f<T>(f);
         f = act_f(f, a.act);
-        if (a.res) f += __bfloat162float(a.res[e + j]);
-        a.y[e + j] = __float2bfloat16_rn(f);
+        if (res) f += to_f(res[e + j]);
+        y[e + j] = from_f<T>(f);
     }
+}
+
+// The three bf16 parts of a fp32 matrix, planes of `rows` rows at a pitch of ldo
+// elements.  hi is the nearest bf16, or the next one towards zero where that
+// would be infinite.
+__global__ void __launch_bounds__(256)
+split_parts(const float *__restrict__ x, __nv_bfloat16 *__restrict__ o, long long rows, long long cols, long long ldo) {
+    const long long plane = rows * ldo;
+    for (long long r = blockIdx.y; r < rows; r += gridDim.y)
+        for (long long c = (long long)blockIdx.x * 256 + threadIdx.x; c < cols; c += (long long)gridDim.x * 256) {
+            const float f = x[r * cols + c];
+            float hi = __bfloat162float(__float2bfloat16_rn(f));
+            if (fabsf(hi) > 3.4e38f && fabsf(f) <= 3.4028235e38f) hi = __uint_as_float(__float_as_uint(f) & 0xFFFF0000u);
+            const float a = f - hi, mid = __bfloat162float(__float2bfloat16_rn(a));
+            __nv_bfloat16 *d = o + r * ldo + c;
+            d[0] = __float2bfloat16_rn(hi);
+            d[plane] = __float2bfloat16_rn(mid);
+            d[2 * plane] = __float2bfloat16_rn(a - mid);
+        }
 }
 
 // Rows of `cols` elements at any pitch, copied to rows of ldo (a multiple of 8) elements.
@@ -455,7 +490,8 @@ struct TcPlan {
 // two full waves on (8190 x 2048 x 5120: 110 us, against 128, 138 and 191 for
 // the others), 128 x 64 where that is what fills the SMs (300 x 2048 x 2048:
 // 8.5 us against 15.2, 9.7 and 9.1).  Joining pieces costs 6 and their bytes.
-TcPlan tc_plan(long long M, long long N, long long K) {
+// fp32: six times the stages, and every tile's sums are joined.
+TcPlan tc_plan(long long M, long long N, long long K, bool parts = false) {
     static const struct { int cg, bn; float stage, tile, fix; } kTile[4] = {
         {2, 256, 0.31f, 1.7f, 4.5f}, {2, 128, 0.18f, 0.9f, 3.5f}, {1, 128, 0.18f, 0.9f, 3.f}, {1, 64, 0.155f, 0.4f, 3.f}};
     TcPlan best{};
@@ -464,16 +500,26 @@ TcPlan tc_plan(long long M, long long N, long long K) {
         TcPlan p{};
         p.cg = k.cg;
         p.bn = k.bn;
-        p.kiters = (int)((K + kBK - 1) / kBK);
+        p.kiters = (int)((K + kBK - 1) / kBK) * (parts ? 6 : 1);
         p.mt = (int)((M + k.cg * kBM - 1) / (k.cg * kBM));
         p.nt = (int)((N + k.bn - 1) / k.bn);
         const long long tiles = (long long)p.mt * p.nt, slots = kSmCount / k.cg, left = tiles % slots;
         const float whole = p.kiters * k.stage + k.tile;
         float us = k.fix + (float)(tiles / slots) * whole + (left ? whole : 0.f);
-        p.tail = (int)tiles;
+        p.tail = parts ? 0 : (int)tiles;
         p.splits = 1;
         p.kper = p.kiters;
-        if (left) {
+        if (parts) {
+            long long s = slots / tiles;
+            if (s > p.kiters / 4) s = p.kiters / 4;
+            if (s > 8) s = 8;
+            if (s < 1) s = 1;
+            p.kper = (int)((p.kiters + s - 1) / s);
+            p.splits = (p.kiters + p.kper - 1) / p.kper;
+            const double bytes = (double)tiles * p.splits * k.cg * kBM * k.bn * 4;
+            us = k.fix + (float)((tiles * p.splits + slots - 1) / slots) * (p.kper * k.stage + k.tile) + 6.f + (float)(2 * bytes / 5e6);
+            p.part = align256((size_t)bytes);
+        } else if (left) {
             long long s = slots / left;
             if (s > p.kiters / 4) s = p.kiters / 4;
             if (s > 1) {
@@ -494,27 +540,32 @@ TcPlan tc_plan(long long M, long long N, long long K) {
     return best;
 }
 
+template <bool PARTS>
 bool setup() {
-    return set_smem((const void *)gemm_tc<256, 2>, Cfg<256, 2>::kSmem) &&
-           set_smem((const void *)gemm_tc<128, 2>, Cfg<128, 2>::kSmem) &&
-           set_smem((const void *)gemm_tc<128, 1>, Cfg<128, 1>::kSmem) &&
-           set_smem((const void *)gemm_tc<64, 1>, Cfg<64, 1>::kSmem);
+    return set_smem((const void *)gemm_tc<256, 2, PARTS>, Cfg<256, 2>::kSmem) &&
+           set_smem((const void *)gemm_tc<128, 2, PARTS>, Cfg<128, 2>::kSmem) &&
+           set_smem((const void *)gemm_tc<128, 1, PARTS>, Cfg<128, 1>::kSmem) &&
+           set_smem((const void *)gemm_tc<64, 1, PARTS>, Cfg<64, 1>::kSmem);
 }
-bool g_ready[128] = {};
+bool g_ready[2][128] = {};
 
-// An operand's map: rows of `inner` elements at pitch ld, boxes of 64 x box_rows, 128-byte swizzle.
-bool operand_map(CUtensorMap *m, const void *base, long long inner, long long rows, long long ld, int box_rows) {
-    const cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)ld * 2};
-    const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
-    return make_dit_map(m, base, 2, dims, strides, box, 128);
+// An operand's map: rows of `inner` elements at pitch ld (and three planes of
+// them), boxes of 64 x box_rows, 128-byte swizzle.
+bool operand_map(CUtensorMap *m, const void *base, long long inner, long long rows, long long ld, int box_rows, bool parts) {
+    const cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)rows, 3};
+    const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)ld * 2 * (cuuint64_t)rows};
+    const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
+    return make_dit_map(m, base, parts ? 3 : 2, dims, strides, box, 128);
 }
 
-template <int BN, int CG>
+template <int BN, int CG, bool PARTS>
 int run_tc(const GemmPlan &g, const TcPlan &p, TcArgs &a, cudaStream_t s) {
     CUtensorMap ma, mb, my, mp, mr;
     // K-major: rows are m (n), boxes 64 k x tile rows; MN-major: rows are k, boxes 64 m (n) x 64 k
-    if (!(g.a_mn ? operand_map(&ma, g.a, g.M, g.K, g.lda, kBK) : operand_map(&ma, g.a, g.K, g.M, g.lda, kBM))) return -1;
-    if (!(g.b_mn ? operand_map(&mb, g.b, g.N, g.K, g.ldb, kBK) : operand_map(&mb, g.b, g.K, g.N, g.ldb, BN / CG))) return -1;
+    if (!(g.a_mn ? operand_map(&ma, g.a, g.M, g.K, g.lda, kBK, PARTS) : operand_map(&ma, g.a, g.K, g.M, g.lda, kBM, PARTS)))
+        return -1;
+    if (!(g.b_mn ? operand_map(&mb, g.b, g.N, g.K, g.ldb, kBK, PARTS) : operand_map(&mb, g.b, g.K, g.N, g.ldb, BN / CG, PARTS)))
+        return -1;
     my = mp = mr = ma;
     if (p.tail > 0 && !a.direct) {
         const cuuint64_t dims[2] = {(cuuint64_t)g.N, (cuuint64_t)g.M}, strides[1] = {(cuuint64_t)g.N * 2};
@@ -537,9 +588,27 @@ int run_tc(const GemmPlan &g, const TcPlan &p, TcArgs &a, cudaStream_t s) {
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    if (cudaLaunchKernelEx(&cfg, gemm_tc<BN, CG>, ma, mb, my, mp, mr, a) != cudaSuccess) return -1;
+    if (cudaLaunchKernelEx(&cfg, gemm_tc<BN, CG, PARTS>, ma, mb, my, mp, mr, a) != cudaSuccess) return -1;
     if (!left) return 1;
-    return launch_pdl(gemm_finish<BN, CG>, (unsigned)left * (CG * kBM * BN / 1024), 256, 0, s, a) ? 2 : -1;
+    using T = std::conditional_t<PARTS, float, __nv_bfloat16>;
+    return launch_pdl(gemm_finish<T, BN, CG>, (unsigned)left * (CG * kBM * BN / 1024), 256, 0, s, a) ? 2 : -1;
+}
+
+template <bool PARTS>
+int run_tile(const GemmPlan &g, const TcPlan &p, void *ws, cudaStream_t s) {
+    if (!once_per_device(&g_ready[PARTS], setup<PARTS>)) return -1;
+    TcArgs a{};
+    a.M = g.M; a.N = g.N;
+    a.kiters = p.kiters; a.mt = p.mt; a.nt = p.nt; a.tail = p.tail; a.splits = p.splits; a.kper = p.kper;
+    a.kblk = p.kiters / (PARTS ? 6 : 1);
+    a.a_mn = g.a_mn; a.b_mn = g.b_mn;
+    a.bias = (const __nv_bfloat16 *)g.bias; a.res = (const __nv_bfloat16 *)g.res;
+    a.pre = (__nv_bfloat16 *)g.pre; a.y = (__nv_bfloat16 *)g.y;
+    a.part = (float *)ws;
+    a.act = g.act;
+    a.direct = g.N % 8 != 0;
+    if (p.cg == 2) return p.bn == 256 ? run_tc<256, 2, PARTS>(g, p, a, s) : run_tc<128, 2, PARTS>(g, p, a, s);
+    return p.bn == 128 ? run_tc<128, 1, PARTS>(g, p, a, s) : run_tc<64, 1, PARTS>(g, p, a, s);
 }
 
 }  // namespace
@@ -580,25 +649,35 @@ bool gemm_tc_fits(long long M, long long N, long long K) {
 
 namespace {
 
-// Workspace of a product: the splits' sums, then copies of operands whose rows are not whole 16 bytes.
+// Workspace of a product: the pieces' sums, then copies of operands whose rows
+// are not whole 16 bytes, or of fp32 ones their parts.
 struct TcWs {
     size_t a, b, total;
 };
 long long pitch8(long long ld) { return (ld + 7) / 8 * 8; }
-TcWs tc_ws(const GemmPlan &g, const TcPlan &p) {
+TcWs tc_ws(const GemmPlan &g, const TcPlan &p, bool parts) {
+    auto bytes = [&](long long rows, long long ld) -> size_t {
+        return parts || ld % 8 ? align256(size_t(rows) * pitch8(ld) * 2 * (parts ? 3 : 1)) : 0;
+    };
     TcWs w;
     w.a = p.part;
-    w.b = w.a + (g.lda % 8 ? align256(size_t(g.a_mn ? g.K : g.M) * pitch8(g.lda) * 2) : 0);
-    w.total = w.b + (g.ldb % 8 ? align256(size_t(g.b_mn ? g.K : g.N) * pitch8(g.ldb) * 2) : 0);
+    w.b = w.a + bytes(g.a_mn ? g.K : g.M, g.lda);
+    w.total = w.b + bytes(g.b_mn ? g.K : g.N, g.ldb);
     return w;
 }
 
-// The operand at a pitch of whole 16 bytes: copied if its rows are not.
-bool packed(const void *&x, long long &ld, long long rows, void *to, cudaStream_t s) {
-    if (ld % 8 == 0) return true;
+// The operand as the kernel reads it: rows at a pitch of whole 16 bytes, in bf16.
+bool packed(const void *&x, long long &ld, long long rows, void *to, bool parts, cudaStream_t s) {
+    if (!parts && ld % 8 == 0) return true;
     const long long ldo = pitch8(ld);
-    repack<<<(unsigned)(rows < 16 * kSmCount ? rows : 16 * kSmCount), 256, 0, s>>>((const __nv_bfloat16 *)x,
-                                                                                  (__nv_bfloat16 *)to, rows, ld, ldo);
+    if (parts) {
+        const long long cx = (ld + 255) / 256 < 64 ? (ld + 255) / 256 : 64, ry = 32 * kSmCount / cx;
+        split_parts<<<dim3((unsigned)cx, (unsigned)(rows < ry ? rows : ry)), 256, 0, s>>>((const float *)x, (__nv_bfloat16 *)to,
+                                                                                         rows, ld, ldo);
+    } else {
+        repack<<<(unsigned)(rows < 16 * kSmCount ? rows : 16 * kSmCount), 256, 0, s>>>((const __nv_bfloat16 *)x,
+                                                                                      (__nv_bfloat16 *)to, rows, ld, ldo);
+    }
     x = to;
     ld = ldo;
     return cudaGetLastError() == cudaSuccess;
@@ -606,26 +685,16 @@ bool packed(const void *&x, long long &ld, long long rows, void *to, cudaStream_
 
 }  // namespace
 
-size_t gemm_tc_ws(const GemmPlan &g) { return tc_ws(g, tc_plan(g.M, g.N, g.K)).total; }
+size_t gemm_tc_ws(int is_bf16, const GemmPlan &g) { return tc_ws(g, tc_plan(g.M, g.N, g.K, !is_bf16), !is_bf16).total; }
 
-int launch_gemm_tc(const GemmPlan &g0, void *ws, cudaStream_t s) {
-    if (!once_per_device(&g_ready, setup)) return -1;
+int launch_gemm_tc(int is_bf16, const GemmPlan &g0, void *ws, cudaStream_t s) {
     GemmPlan g = g0;
-    const TcPlan p = tc_plan(g.M, g.N, g.K);
-    const TcWs w = tc_ws(g, p);
-    if (!packed(g.a, g.lda, g.a_mn ? g.K : g.M, (char *)ws + w.a, s)) return -1;
-    if (!packed(g.b, g.ldb, g.b_mn ? g.K : g.N, (char *)ws + w.b, s)) return -1;
-    TcArgs a{};
-    a.M = g.M; a.N = g.N;
-    a.kiters = p.kiters; a.mt = p.mt; a.nt = p.nt; a.tail = p.tail; a.splits = p.splits; a.kper = p.kper;
-    a.a_mn = g.a_mn; a.b_mn = g.b_mn;
-    a.bias = (const __nv_bfloat16 *)g.bias; a.res = (const __nv_bfloat16 *)g.res;
-    a.pre = (__nv_bfloat16 *)g.pre; a.y = (__nv_bfloat16 *)g.y;
-    a.part = (float *)ws;
-    a.act = g.act;
-    a.direct = g.N % 8 != 0;
-    if (p.cg == 2) return p.bn == 256 ? run_tc<256, 2>(g, p, a, s) : run_tc<128, 2>(g, p, a, s);
-    return p.bn == 128 ? run_tc<128, 1>(g, p, a, s) : run_tc<64, 1>(g, p, a, s);
+    const bool parts = !is_bf16;
+    const TcPlan p = tc_plan(g.M, g.N, g.K, parts);
+    const TcWs w = tc_ws(g, p, parts);
+    if (!packed(g.a, g.lda, g.a_mn ? g.K : g.M, (char *)ws + w.a, parts, s)) return -1;
+    if (!packed(g.b, g.ldb, g.b_mn ? g.K : g.N, (char *)ws + w.b, parts, s)) return -1;
+    return parts ? run_tile<true>(g, p, ws, s) : run_tile<false>(g, p, ws, s);
 }
 
 int read_and_clear_linear_flag(unsigned *flag_out) {

@@ -40,17 +40,15 @@ struct GemmPlan {
     void *pre, *y;               // [M][N] or null (pre), [M][N]
     int act;
 };
-// fp32 products on the CUDA cores
-int launch_gemm_f32(const GemmPlan &g, cudaStream_t s);
 // at most kFewRows rows, both operands k-contiguous
 constexpr int kFewRows = 8;
 int launch_gemm_rows(int is_bf16, const GemmPlan &g, cudaStream_t s);
-// bf16 products on the tensor cores (k_linear_tc.cu); lda, ldb are the
-// operands' row lengths, of any size (rows that are not whole 16 bytes are
-// copied to the workspace first)
+// products on the tensor cores (k_linear_tc.cu); lda, ldb are the operands' row
+// lengths, of any size (bf16 rows that are not whole 16 bytes are copied to the
+// workspace first, fp32 ones split into their parts there)
 bool gemm_tc_fits(long long M, long long N, long long K);
-size_t gemm_tc_ws(const GemmPlan &g);
-int launch_gemm_tc(const GemmPlan &g, void *ws, cudaStream_t s);
+size_t gemm_tc_ws(int is_bf16, const GemmPlan &g);
+int launch_gemm_tc(int is_bf16, const GemmPlan &g, void *ws, cudaStream_t s);
 int read_and_clear_linear_flag(unsigned *flag_out);
 // dz = dy * act'(pre) (with an activation and dz not null) and the column sums
 // of dz (colsum not null), in a fixed order; ws holds act_col_ws bytes

@@ -74,12 +74,12 @@ la::GemmPlan dw_product(long long R, long long K, long long N) {
 }
 size_t product_ws(la_dtype dt, const la::GemmPlan &g) {
     const bool few = g.M <= la::kFewRows && !g.a_mn && !g.b_mn;
-    return dt == LA_BF16 && !few ? la::gemm_tc_ws(g) : 0;
+    return few ? 0 : la::gemm_tc_ws(dt == LA_BF16, g);
 }
 // A product on the kernel for its type and shape.
 int product(la_dtype dt, const la::GemmPlan &g, void *ws, cudaStream_t s) {
     if (g.M <= la::kFewRows && !g.a_mn && !g.b_mn) return la::launch_gemm_rows(dt == LA_BF16, g, s);
-    return dt == LA_BF16 ? la::launch_gemm_tc(g, ws, s) : la::launch_gemm_f32(g, s);
+    return la::launch_gemm_tc(dt == LA_BF16, g, ws, s);
 }
 
 bool linear_sizes_ok(int R, int K, int N, la_dtype dt) {
