@@ -604,9 +604,9 @@ int fwd_t(const void *q, const void *k, const void *v, const FwdShape &f, FwdArg
 
 }  // namespace
 
-// (items are counted in ints)
+// (items are counted in ints; there are pieces only where there are fewer items than SMs)
 bool cross_tc_fits(const CrossPlan &p) {
-    return (long long)p.B * p.H * ((p.N + 2 * kQT - 1) / (2 * kQT)) < (1LL << 29) / (2 * kSmCount);
+    return (long long)p.B * p.H * ((p.N + 2 * kQT - 1) / (2 * kQT)) < (1LL << 30);
 }
 
 size_t cross_fwd_tc_ws(const CrossPlan &p) { return fwd_shape(p).part; }

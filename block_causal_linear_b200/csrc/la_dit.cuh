@@ -78,6 +78,7 @@ __device__ __forceinline__ float act_slope(float z, int act) {
         return s * (1.f + z * (1.f - s));
     }
     if (act == 3) {
+        z = fminf(fmaxf(z, -30.f), 30.f);   // the slope is 0 or 1 there; z^3 of a huge z would meet 1 - s = 0 as inf
         const float s = sigmoid_f(kGeluA * (z + 0.044715f * z * z * z));
         return s * (1.f + z * (1.f - s) * kGeluA * (1.f + 0.134145f * z * z));
     }

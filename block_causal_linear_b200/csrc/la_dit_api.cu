@@ -23,7 +23,7 @@ bool count_ok(long long a, long long b, long long c) {
 la_status norm_plan(la::NormPlan &p, int B, int N, int C, int per_batch, float eps) {
     if (!count_ok(B, N, C)) return LA_EINVAL;
     if (!(eps >= 0.0f) || !std::isfinite(eps)) return LA_EINVAL;
-    if (per_batch && B > 65535) return LA_EUNSUPPORTED;
+    if ((per_batch && B > 65535) || (long long)B * N > 0x7fffffffLL) return LA_EUNSUPPORTED;
     p.B = B; p.N = N; p.C = C;
     p.rows = (long long)B * N;
     p.per_batch = per_batch ? 1 : 0;

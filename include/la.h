@@ -360,7 +360,8 @@ LA_API la_status la_dwconv3d(const void *x, void *y, la_dtype dt, int B, int T, 
  *   g = weight dy,  dx = rstd (g - mean_C(g) - xh mean_C(g xh)),
  *   dweight = sum dy xh,  dbias = sum dy  over the rows that share the vector
  * ([C] or [B][C], type dt).  dweight and dbias may each be NULL (ws may be
- * NULL if both are).  B at most 65535 with per_batch, else LA_EUNSUPPORTED.
+ * NULL if both are).  B N below 2^31, and B at most 65535 with per_batch, else
+ * LA_EUNSUPPORTED.
  */
 LA_API la_status la_layer_norm_forward(const void *x, const void *weight, const void *bias, void *y, float *mean,
                                        float *rstd, la_dtype dt, int B, int N, int C, int per_batch, float eps,

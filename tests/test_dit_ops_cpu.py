@@ -42,6 +42,7 @@ def test_norm_refusals(la):
         dict(mean=FAKE + 4), dict(rstd=FAKE + 4), dict(dt=2), dict(B=0), dict(N=-1), dict(C=0),
         dict(B=1 << 30, N=1 << 30), dict(eps=-1.0), dict(eps=NAN), dict(eps=INF))])
     assert fwd(B=65536, pb=1) == la.LA_EUNSUPPORTED
+    assert fwd(B=1 << 20, N=1 << 12, C=8) == la.LA_EUNSUPPORTED      # rows past 2^31
     need = L.la_layer_norm_backward_workspace_size(2, 3, 8, 0)
     assert need > 0 and need % 256 == 0 and L.la_layer_norm_backward_workspace_size(0, 3, 8, 0) == 0
     bwd = caller(L.la_layer_norm_backward, dict(dy=FAKE, x=FAKE, w=FAKE, mean=FAKE, rstd=FAKE, dx=FAKE, dw=FAKE,
@@ -85,7 +86,7 @@ def test_cross_refusals(la):
     fwd = caller(L.la_cross_attention_forward, dict(**args, **sizes, scale=0.2, ws=FAKE, n=need, stream=None))
     common = ([("inval", k) for k in (
         dict(dt=2), dict(B=0), dict(N=0), dict(M=0), dict(H=0), dict(d=0), dict(ldk=127), dict(ldv=124),
-        dict(ldk=132), dict(ldk=BIG), dict(kv_len=FAKE + 2), dict(scale=0.0), dict(scale=-1.0), dict(scale=NAN),
+        dict(ldk=132), dict(ldk=BIG), dict(kv_len=FAKE + 2), dict(scale=0.0), dict(scale=1e-21), dict(scale=-1.0), dict(scale=NAN),
         dict(scale=INF))] +
         [("unsup", dict(d=48)), ("unsup", dict(d=128, ldk=512, ldv=512)),
          ("unsup", dict(B=1 << 14)), ("ws", dict(ws=None)), ("ws", dict(n=need - 1)), ("ws", dict(ws=FAKE + 32))])

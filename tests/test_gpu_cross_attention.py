@@ -75,6 +75,9 @@ CASES = [  # B, N, M, H, d, dtype, fused, lengths
     (4, 200, 512, 2, 32, BF, True, [512, 385, 384, 128]), (2, 390, 513, 2, 32, BF, False, [513, 512]),
     (2, 500, 1100, 1, 64, BF, True, [1100, 700]), (1, 1000, 33, 4, 32, BF, True, [-5]), (2, 64, 40, 2, 64, BF, False, [99, 7]),
     (1, 2000, 300, 1, 64, BF, True, None), (2, 31, 16, 2, 32, BF, True, [15, 16]), (1, 260, 257, 20, 32, BF, True, None),
+    (1, 8, 200, 2, 32, BF, True, None), (1, 9, 200, 2, 64, BF, True, None), (2, 5, 260, 3, 64, BF, False, [260, 0]),
+    (1, 385, 150, 3, 32, BF, True, None), (1, 769, 65, 2, 64, BF, True, None), (2, 100, 2100, 2, 32, BF, True, [2100, 900]),
+    (1, 300, 3000, 1, 64, BF, True, None), (3, 1300, 130, 2, 32, BF, True, [130, 128, 2]), (40, 130, 66, 1, 32, BF, True, None),
     (2, 77, 40, 3, 32, F32, True, [40, 9]), (1, 391, 77, 8, 64, F32, False, None), (2, 130, 70, 2, 64, F32, True, [0, 70]),
     (1, 1, 500, 4, 32, F32, True, None), (3, 64, 5, 2, 32, F32, False, [5, 1, 12]),
 ]
@@ -130,6 +133,13 @@ def test_gradients_into_a_wider_tensor(la, dtype):
     la.cross_attention_backward(q, k, v, out, lse, dout, grads=(dq, dkv[:, :, 0], dkv[:, :, 2]))
     assert torch.equal(dq, want[0]) and torch.equal(dkv[:, :, 0], want[1]) and torch.equal(dkv[:, :, 2], want[2])
     assert (dkv[:, :, 1] == 7).all()
+
+
+@pytest.mark.parametrize("scale", [1e-20, 1e-4, 30.0])
+def test_scales(la, scale):
+    """Scales from the smallest taken (all states alike) to one that leaves one state a query."""
+    q, k, v, dout = draw(2, 140, 130, 2, 32, BF, True, 9)
+    run_case(la, q, k, v, dout, [130, 77], BF, scale=scale)
 
 
 def test_gradient_against_differences(la):

@@ -38,6 +38,7 @@ CASES = [  # R, K, N, dtype, act, bias, residual
     (257, 1000, 520, BF, "relu", True, True), (640, 320, 72, BF, "silu", False, True),
     (100, 63, 65, BF, "gelu", True, True), (333, 130, 1, BF, "none", True, False), (333, 1, 130, BF, "silu", True, True),
     (1030, 264, 776, BF, "silu", True, True), (2500, 128, 64, BF, "none", True, False),
+    (2700, 640, 2048, BF, "silu", True, True), (2305, 264, 2056, BF, "gelu", True, True),   # whole waves and tail tiles
     (40, 4104, 200, BF, "gelu", True, False), (20, 200, 4104, BF, "none", False, True),
     (1, 70, 300, F32, "gelu", True, False), (5, 33, 17, F32, "relu", True, True), (130, 127, 129, F32, "silu", True, True),
     (300, 256, 384, F32, "none", True, True), (513, 100, 64, F32, "gelu", False, True), (64, 2000, 40, F32, "none", True, False),
@@ -97,6 +98,35 @@ def test_activations_far_out(la, act, dtype):
     dx, _, _ = la.linear_backward(torch.ones_like(y), x, w, pre=pre, act=act)
     (rdx, sdx), _, _ = ref.linear_backward(torch.ones_like(y), x, w, pre, act, dtype)
     ref.check("dx", dx, rdx, sdx, dtype)
+
+
+def test_fp32_over_the_whole_range(la):
+    """fp32 operands from 1e-30 to the largest finite value: exponents far apart in one row, and products that
+    come back to order one."""
+    g = torch.Generator().manual_seed(5)
+    R, K, N = 150, 48, 70
+    e = torch.randint(-30, 31, (R, 1), generator=g).double()
+    x = (torch.randn(R, K, generator=g).double() * 10.0 ** e).to(F32).cuda()
+    w = torch.randn(N, K, generator=g).to(F32).cuda()
+    y = la.linear_forward(x, w)
+    ry, _, sy, _ = ref.linear_forward(x, w, None, "none", None)
+    ref.check("y", y, ry, sy, F32)
+    big = torch.zeros(R, K, device="cuda")
+    big[:, 0] = torch.finfo(F32).max
+    small = torch.zeros(N, K, device="cuda")
+    small[:, 0] = 2.0 ** -100
+    y = la.linear_forward(big, small)
+    ry, _, sy, _ = ref.linear_forward(big, small, None, "none", None)
+    ref.check("y", y, ry, sy, F32)
+
+
+def test_slopes_of_huge_inputs(la):
+    """Activations and slopes at +-1e30: the identity or zero, never NaN."""
+    x, w = torch.tensor([[1e30], [-1e30]], device="cuda"), torch.ones(1, 1, device="cuda")
+    for act in ("relu", "silu", "gelu"):
+        y, pre = la.linear_forward(x, w, act=act, return_pre=True)
+        dx, _, _ = la.linear_backward(torch.ones_like(y), x, w, pre=pre, act=act)
+        assert y[0] == 1e30 and y[1] == 0 and dx[0] == 1 and dx[1] == 0
 
 
 def test_linear_writes_only_its_outputs(la):

@@ -41,6 +41,8 @@ CASES = [  # B, N, C, dtype, vectors
     (2, 301, 2048, BF, "batch"), (1, 190, 2048, F32, "channel"), (2, 65, 2056, BF, "batch"),
     (1, 40, 5120, BF, "channel"), (2, 21, 5119, BF, "batch"), (1, 9, 8200, F32, "channel"),
     (1, 3, 20000, BF, "channel"), (2, 2, 33333, F32, "batch"), (4, 700, 96, BF, "batch"),
+    (1, 7200, 2048, BF, "channel"), (2400, 3, 1024, BF, "batch"), (3, 2500, 768, F32, "batch"),     # rings of rows
+    (1, 40, 8192, F32, "channel"), (2, 70, 4096, BF, "batch"), (3, 1, 8192, BF, "batch"),
     (1, 5000, 40, BF, "none"), (5, 260, 512, F32, "none"), (1, 2500, 1152, BF, "channel"),
 ]
 
