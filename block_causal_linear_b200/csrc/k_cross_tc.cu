@@ -15,8 +15,9 @@
 // of them to a polynomial on the FMA pipe measured 1% slower: the steps'
 // latencies, not the unit alone, are what is left).
 //
-// Few queries against many states are cut along the states into pieces whose
-// unnormalised sums a second kernel joins.
+// Few queries against many states are cut along the states: up to 8 of them
+// into the CTAs of a cluster, which joins its sums through shared memory; more
+// into pieces whose unnormalised sums a second kernel joins.
 #include "la_sm100_dit.cuh"
 
 namespace la {
@@ -405,15 +406,19 @@ cross_fwd_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
     }
 }
 
+constexpr int kFewPieces = 8;    // most pieces (CTAs of a cluster) of the few-query form
+
 // A few queries (at most NQ a CTA) on the CUDA cores: K and V are streamed once,
 // D / 8 lanes a state with 16 bytes each, the CTA's 4 warps every 4th group of
-// states; each lane group keeps its own maximum and sums, joined at the end.
+// states; each lane group keeps its own maximum and sums, joined at the end,
+// then over the cluster's CTAs (the pieces of the states) in their order.
 template <int D, int NQ>
 __global__ void __launch_bounds__(128)
 cross_few(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restrict__ k, const __nv_bfloat16 *__restrict__ v,
           const FwdArgs a) {
     constexpr int LG = D / 8, G = 32 / LG, U = 4;      // lanes a state, states a warp and step, steps in flight
     __shared__ float sm[4 * G][NQ], sl[4 * G][NQ], so[4 * G][NQ][D];
+    __shared__ float cm[NQ], cl[NQ], co[NQ][D];        // this piece's
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane / LG, part = lane % LG;
     const int sp = blockIdx.x, b = blockIdx.y / a.p.H, h = blockIdx.y % a.p.H, n0 = blockIdx.z * NQ;
     pdl_wait();
@@ -480,7 +485,6 @@ cross_few(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restrict__
     __syncthreads();
     for (int x = threadIdx.x; x < NQ * D; x += 128) {
         const int n = x / D, e = x % D;
-        if (n0 + n >= a.p.N) break;
         float mx = -INFINITY, ls = 0.f, os = 0.f;
 #pragma unroll
         for (int i = 0; i < 4 * G; ++i) mx = fmaxf(mx, sm[i][n]);
@@ -491,16 +495,36 @@ cross_few(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restrict__
             ls += sl[i][n] * f;
             os += so[i][n][e] * f;
         }
-        const long long bhn = ((long long)b * a.p.H + h) * a.p.N + n0 + n;
-        if (a.splits > 1) {
-            const long long rows = (long long)a.p.B * a.p.H * a.p.N, r = sp * rows + bhn;
-            a.part[r * D + e] = os;
-            if (e == 0) reinterpret_cast<float2 *>(a.part + a.splits * rows * D)[r] = make_float2(base, ls);
-        } else {
-            a.out[(((long long)b * a.p.N + n0 + n) * a.p.H + h) * D + e] = __float2bfloat16_rn(len > 0 ? os / ls : 0.f);
-            if (e == 0 && a.lse) a.lse[bhn] = len > 0 ? (base + __log2f(ls)) * kLn2 : -INFINITY;
-        }
+        co[n][e] = os;
+        if (e == 0) cm[n] = base, cl[n] = ls;
     }
+    if (a.splits > 1) cluster_sync();
+    else __syncthreads();
+    for (int x = sp * 128 + threadIdx.x; x < NQ * D; x += a.splits * 128) {
+        const int n = x / D, e = x % D;
+        if (n0 + n >= a.p.N) break;
+        float base = cm[n], ls = cl[n], os = co[n][e];
+        if (a.splits > 1) {
+            float pm[kFewPieces];
+            base = -3.0e38f;
+#pragma unroll
+            for (int c2 = 0; c2 < kFewPieces; ++c2) {
+                pm[c2] = c2 < a.splits ? ld_dsmem_f32(&cm[n], c2) : -INFINITY;
+                base = fmaxf(base, pm[c2]);
+            }
+            ls = os = 0.f;
+#pragma unroll
+            for (int c2 = 0; c2 < kFewPieces; ++c2) {
+                if (c2 >= a.splits) break;
+                const float f = ex2(pm[c2] - base);
+                ls += ld_dsmem_f32(&cl[n], c2) * f;
+                os += ld_dsmem_f32(&co[n][e], c2) * f;
+            }
+        }
+        a.out[(((long long)b * a.p.N + n0 + n) * a.p.H + h) * D + e] = __float2bfloat16_rn(len > 0 ? os / ls : 0.f);
+        if (e == 0 && a.lse) a.lse[((long long)b * a.p.H + h) * a.p.N + n0 + n] = len > 0 ? (base + __log2f(ls)) * kLn2 : -INFINITY;
+    }
+    if (a.splits > 1) cluster_sync();      // the others may still read this CTA's sums
 }
 
 // out, lse from the pieces, in piece order: D / 4 threads a query.
@@ -543,18 +567,22 @@ struct FwdShape {
 };
 
 // Queries a CTA of the few-query form, and the pieces along the states: enough
-// items for every SM (the few-query form: eight a SM), with at least 4 steps
-// (128 states) each.
+// items for every SM, with at least 4 steps each (the few-query form: eight
+// CTAs a SM, 1 to 8 pieces of 64 states or more).
 FwdShape fwd_shape(const CrossPlan &p) {
     FwdShape f{};
     f.few = p.N <= kFew;
     f.nq = p.N <= 1 ? 1 : (p.N <= 2 ? 2 : 4);
     const int rows = kQT * (p.d == 32 ? FC<32>::kStreams : FC<64>::kStreams);
     f.groups = (p.N + rows - 1) / rows;
-    const long long items = (long long)p.B * p.H * (f.few ? (p.N + f.nq - 1) / f.nq : f.groups);
-    const int want = (f.few ? 8 : 1) * kSmCount, per = f.few ? 128 : 4 * kKT;
-    long long s = want / items;
-    if (s > p.M / per) s = p.M / per;
+    f.splits = 1;
+    if (f.few) {
+        const long long items = (long long)p.B * p.H * ((p.N + f.nq - 1) / f.nq);
+        while (f.splits < kFewPieces && items * f.splits < 8 * kSmCount && p.M >= 128 * f.splits) f.splits *= 2;
+        return f;
+    }
+    long long s = kSmCount / ((long long)p.B * p.H * f.groups);
+    if (s > p.M / (4 * kKT)) s = p.M / (4 * kKT);
     f.splits = (int)(s < 1 ? 1 : s);
     f.part = f.splits > 1 ? align256(size_t(f.splits) * p.B * p.H * p.N * (p.d + 2) * sizeof(float)) : 0;
     return f;
@@ -581,14 +609,18 @@ int fwd_t(const void *q, const void *k, const void *v, const FwdShape &f, FwdArg
         cfg.gridDim = dim3((unsigned)f.splits, (unsigned)(a.p.B * a.p.H), (unsigned)((a.p.N + f.nq - 1) / f.nq));
         cfg.blockDim = dim3(128);
         cfg.stream = s;
-        cudaLaunchAttribute attr[1];
+        cudaLaunchAttribute attr[2];
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = (unsigned)f.splits;
+        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
         cfg.attrs = attr;
-        cfg.numAttrs = 1;
+        cfg.numAttrs = 2;
         auto fn = f.nq == 1 ? cross_few<D, 1> : (f.nq == 2 ? cross_few<D, 2> : cross_few<D, 4>);
-        if (cudaLaunchKernelEx(&cfg, fn, (const bf *)q, (const bf *)k, (const bf *)v, a) != cudaSuccess) return -1;
-    } else {
+        return cudaLaunchKernelEx(&cfg, fn, (const bf *)q, (const bf *)k, (const bf *)v, a) == cudaSuccess ? 1 : -1;
+    }
+    {
         if (!once_per_device(&g_ready, setup)) return -1;
         CUtensorMap mq, mk, mv, mo;
         if (!head_map(&mq, q, a.p, a.p.N, (long long)a.p.H * D, kQT) || !head_map(&mk, k, a.p, a.p.M, a.p.ldk, kKT) ||

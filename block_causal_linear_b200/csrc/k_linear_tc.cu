@@ -452,18 +452,36 @@ gemm_finish(const TcArgs a) {
 // would be infinite.
 __global__ void __launch_bounds__(256)
 split_parts(const float *__restrict__ x, __nv_bfloat16 *__restrict__ o, long long rows, long long cols, long long ldo) {
-    const long long plane = rows * ldo;
-    for (long long r = blockIdx.y; r < rows; r += gridDim.y)
-        for (long long c = (long long)blockIdx.x * 256 + threadIdx.x; c < cols; c += (long long)gridDim.x * 256) {
-            const float f = x[r * cols + c];
-            float hi = __bfloat162float(__float2bfloat16_rn(f));
-            if (fabsf(hi) > 3.4e38f && fabsf(f) <= 3.4028235e38f) hi = __uint_as_float(__float_as_uint(f) & 0xFFFF0000u);
-            const float a = f - hi, mid = __bfloat162float(__float2bfloat16_rn(a));
-            __nv_bfloat16 *d = o + r * ldo + c;
-            d[0] = __float2bfloat16_rn(hi);
-            d[plane] = __float2bfloat16_rn(mid);
-            d[2 * plane] = __float2bfloat16_rn(a - mid);
+    const long long plane = rows * ldo, groups = rows * (ldo / 8);
+    const int per = (int)(ldo / 8);
+    // a thread 8 columns of a row: whole 16 bytes of each part (reads of odd rows are element by element)
+    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < groups; i += (long long)gridDim.x * 256) {
+        const long long r = i / per;
+        const int c = (int)(i - r * per) * 8;
+        const float *s = x + r * cols + c;
+        float f[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = c + e < cols ? s[e] : 0.f;
+        uint32_t h[4], m[4], l[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float hi[2], mid[2], lo[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const float v = f[2 * e + u];
+                hi[u] = __bfloat162float(__float2bfloat16_rn(v));
+                if (fabsf(hi[u]) > 3.4e38f && fabsf(v) <= 3.4028235e38f) hi[u] = __uint_as_float(__float_as_uint(v) & 0xFFFF0000u);
+                const float a = v - hi[u];
+                mid[u] = __bfloat162float(__float2bfloat16_rn(a));
+                lo[u] = a - mid[u];
+            }
+            h[e] = pack_bf2(hi[0], hi[1]), m[e] = pack_bf2(mid[0], mid[1]), l[e] = pack_bf2(lo[0], lo[1]);
         }
+        uint4 *d = reinterpret_cast<uint4 *>(o + r * ldo + c);
+        d[0] = make_uint4(h[0], h[1], h[2], h[3]);
+        d[plane / 8] = make_uint4(m[0], m[1], m[2], m[3]);
+        d[2 * (plane / 8)] = make_uint4(l[0], l[1], l[2], l[3]);
+    }
 }
 
 // Rows of `cols` elements at any pitch, copied to rows of ldo (a multiple of 8) elements.
@@ -671,9 +689,9 @@ bool packed(const void *&x, long long &ld, long long rows, void *to, bool parts,
     if (!parts && ld % 8 == 0) return true;
     const long long ldo = pitch8(ld);
     if (parts) {
-        const long long cx = (ld + 255) / 256 < 64 ? (ld + 255) / 256 : 64, ry = 32 * kSmCount / cx;
-        split_parts<<<dim3((unsigned)cx, (unsigned)(rows < ry ? rows : ry)), 256, 0, s>>>((const float *)x, (__nv_bfloat16 *)to,
-                                                                                         rows, ld, ldo);
+        const long long want = (rows * (ldo / 8) + 255) / 256;
+        split_parts<<<(unsigned)(want < 16 * kSmCount ? want : 16 * kSmCount), 256, 0, s>>>((const float *)x, (__nv_bfloat16 *)to,
+                                                                                           rows, ld, ldo);
     } else {
         repack<<<(unsigned)(rows < 16 * kSmCount ? rows : 16 * kSmCount), 256, 0, s>>>((const __nv_bfloat16 *)x,
                                                                                       (__nv_bfloat16 *)to, rows, ld, ldo);
