@@ -363,13 +363,14 @@ norm_fwd(const T *__restrict__ x, const T *__restrict__ w, const T *__restrict__
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = (i * TPR + t) * VEC;
-        if (ok && c < p.C) {
-            v[i] = load_pack<T, VEC>(xr + c);
-        } else {
+        v[i] = load_pack<T, VEC>(xr + (c < p.C ? c : 0));      // (loads under no branch: all in flight at once)
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        if ((i * TPR + t) * VEC >= p.C) {
 #pragma unroll
             for (int j = 0; j < VEC; ++j) v[i].v[j] = from_f<T>(0.f);
         }
-    }
     auto row_sum = [&](float s, int which) {
         s = warp_sum(s);
         if constexpr (WPR > 1) {
@@ -394,15 +395,13 @@ norm_fwd(const T *__restrict__ x, const T *__restrict__ w, const T *__restrict__
             s += (i * TPR + t) * VEC < p.C ? d * d : 0.f;
         }
     const float rstd = rsqrtf(row_sum(s, 1) / (float)p.C + p.eps);
-    if (!ok) return;
-    const long long vo = p.per_batch ? r / p.N * p.C : 0;
+    const long long vo = p.per_batch ? (ok ? r : 0) / p.N * p.C : 0;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = (i * TPR + t) * VEC;
-        if (c >= p.C) break;
+        const int c = (i * TPR + t) * VEC, cc = c < p.C ? c : 0;
         Pack<T, VEC> wk, bk, o;
-        if (w) wk = load_pack<T, VEC>(w + vo + c);
-        if (b) bk = load_pack<T, VEC>(b + vo + c);
+        if (w) wk = load_pack<T, VEC>(w + vo + cc);
+        if (b) bk = load_pack<T, VEC>(b + vo + cc);
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
             float f = (to_f(v[i].v[j]) - mean) * rstd;
@@ -410,8 +409,9 @@ norm_fwd(const T *__restrict__ x, const T *__restrict__ w, const T *__restrict__
             if (b) f += to_f(bk.v[j]);
             o.v[j] = from_f<T>(f);
         }
-        *reinterpret_cast<Pack<T, VEC> *>(y + r * p.C + c) = o;
+        if (ok && c < p.C) *reinterpret_cast<Pack<T, VEC> *>(y + r * p.C + c) = o;
     }
+    if (!ok) return;
     if (t == 0) {
         if (mean_out) mean_out[r] = mean;
         if (rstd_out) rstd_out[r] = rstd;
@@ -467,7 +467,7 @@ norm_fwd_wide(const T *__restrict__ x, const T *__restrict__ w, const T *__restr
 // the next rows loaded before the current ones are reduced; the channels' sums
 // stay in registers and leave as one piece, part[group][split][2][C].
 template <typename T, int kEpt, int MAXT>
-__global__ void __launch_bounds__(MAXT)
+__global__ void __launch_bounds__(MAXT, kEpt == 4 ? 2 : 1)
 norm_bwd(const T *__restrict__ dy, const T *__restrict__ x, const T *__restrict__ w, const float *__restrict__ mean,
          const float *__restrict__ rstd, T *__restrict__ dx, float *__restrict__ part, const NormPlan p, int tpr,
          int splits) {
@@ -495,16 +495,16 @@ norm_bwd(const T *__restrict__ dy, const T *__restrict__ x, const T *__restrict_
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * tpr + t) * VEC;
-            if (ok && c < p.C) {
-                xp[i] = load_pack<T, VEC>(x + r * p.C + c);
-                dp[i] = load_pack<T, VEC>(dy + r * p.C + c);
-            } else {
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) xp[i].v[j] = dp[i].v[j] = from_f<T>(0.f);
-            }
+            const long long at = (ok ? r : r0) * p.C + (c < p.C ? c : 0);      // (under no branch: all in flight at once)
+            xp[i] = load_pack<T, VEC>(x + at);
+            dp[i] = load_pack<T, VEC>(dy + at);
         }
-        m = ok ? mean[r] : 0.f;
-        rs = ok ? rstd[r] : 0.f;
+        m = mean[ok ? r : r0];
+        rs = rstd[ok ? r : r0];
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (!ok || (i * tpr + t) * VEC >= p.C) xp[i].v[0] = dp[i].v[0] = from_f<T>(0.f);
+        if (!ok) m = rs = 0.f;
     };
     fetch(r0 + yy);
     int par = 0;
@@ -620,27 +620,28 @@ norm_dw_wide(const T *__restrict__ dy, const T *__restrict__ x, const float *__r
 }
 
 // out[group][e] = sum over splits of part[group][split][e], e < width: 32
-// columns a CTA, its 8 warps taking every 8th split, then the warps' sums in
+// columns a CTA, its 32 warps taking every 32nd split, then the warps' sums in
 // warp order.  Columns below `cut` go to out0, the rest to out1.
+constexpr int kSumWarps = 32;
 template <typename T>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(32 * kSumWarps)
 split_sum(const float *__restrict__ part, T *__restrict__ out0, T *__restrict__ out1, long long width, long long cut,
           int splits) {
-    __shared__ float red[8][32];
+    __shared__ float red[kSumWarps][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const long long e = (long long)blockIdx.x * 32 + lane, g = blockIdx.y;
     float a = 0.f;
     if (e < width) {
         const float *src = part + g * splits * width + e;
-#pragma unroll 4
-        for (int s = warp; s < splits; s += 8) a += src[s * width];
+#pragma unroll 8
+        for (int s = warp; s < splits; s += kSumWarps) a += src[s * width];
     }
     red[warp][lane] = a;
     __syncthreads();
     if (warp || e >= width) return;
     a = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) a += red[i][lane];
+    for (int i = 0; i < kSumWarps; ++i) a += red[i][lane];
     T *o = e < cut ? out0 : out1;
     if (o) o[e < cut ? g * cut + e : g * (width - cut) + e - cut] = from_f<T>(a);
 }
@@ -675,11 +676,11 @@ BwdShape bwd_shape(const NormPlan &p, int esize) {
         b.splits = (int)(s < 1 ? 1 : s);
         return b;
     }
-    b.ept = p.C <= 4096 ? 8 : 16;
+    b.ept = p.C <= 2048 ? 4 : (p.C <= 4096 ? 8 : 16);
     b.tpr = ((p.C + b.ept - 1) / b.ept + 31) / 32 * 32;
     if (b.tpr > 512) b.tpr = 256;
     b.threads = b.tpr >= 256 ? b.tpr : 256 / b.tpr * b.tpr;
-    const int resident = b.threads <= 256 ? 4 : 2;
+    const int resident = b.ept == 4 ? 1024 / b.threads : 1;
     long long s = (long long)resident * kSmCount / groups;
     if (s > (rows + 7) / 8) s = (rows + 7) / 8;
     b.splits = (int)(s < 1 ? 1 : s);
@@ -705,6 +706,17 @@ int fwd_launch(const T *x, const T *w, const T *b, T *y, float *mean, float *rst
 
 template <typename T, int VEC>
 int fwd_pick(const T *x, const T *w, const T *b, T *y, float *mean, float *rstd, const NormPlan &p, cudaStream_t s) {
+    if constexpr (VEC == 1) {
+        // element loads: few a thread (32 a thread took 155 registers and left one CTA on a SM: 24 us for 3510 rows
+        // of 1001 fp32)
+        if (p.C <= 256) return fwd_launch<T, 1, 8, 1>(x, w, b, y, mean, rstd, p, s);
+        if (p.C <= 512) return fwd_launch<T, 1, 8, 2>(x, w, b, y, mean, rstd, p, s);
+        if (p.C <= 1024) return fwd_launch<T, 1, 8, 4>(x, w, b, y, mean, rstd, p, s);
+        if (p.C <= 2048) return fwd_launch<T, 1, 8, 8>(x, w, b, y, mean, rstd, p, s);
+        if (p.C <= 4096) return fwd_launch<T, 1, 16, 8>(x, w, b, y, mean, rstd, p, s);
+        if (p.C <= 8192) return fwd_launch<T, 1, 32, 8>(x, w, b, y, mean, rstd, p, s);
+        return fwd_launch<T, 1, 64, 8>(x, w, b, y, mean, rstd, p, s);
+    }
     if (p.C <= 256) return fwd_launch<T, VEC, 8, 1>(x, w, b, y, mean, rstd, p, s);
     if (p.C <= 512) return fwd_launch<T, VEC, 16, 1>(x, w, b, y, mean, rstd, p, s);
     if (p.C <= 1024) return fwd_launch<T, VEC, 32, 1>(x, w, b, y, mean, rstd, p, s);
@@ -757,7 +769,7 @@ int norm_bwd_t(const T *dy, const T *x, const T *w, const float *mean, const flo
     } else if (p.C <= kWideBwd) {
         // the CTA's pieces at the end, or two rounds of two sums a warp
         const int smem = b.threads > b.tpr ? b.threads * 2 * b.ept * 4 : b.threads / 32 * 16;
-        auto f = b.ept == 16 ? norm_bwd<T, 16, 512> : (b.threads > 256 ? norm_bwd<T, 8, 512> : norm_bwd<T, 8, 256>);
+        auto f = b.ept == 16 ? norm_bwd<T, 16, 512> : (b.ept == 8 ? norm_bwd<T, 8, 512> : norm_bwd<T, 4, 512>);
         f<<<grid, b.threads, smem, s>>>(dy, x, w, mean, rstd, dx, part, p, b.tpr, b.splits);
     } else {
         const long long grid = p.rows < (1 << 30) ? p.rows : (1 << 30);
@@ -769,7 +781,7 @@ int norm_bwd_t(const T *dy, const T *x, const T *w, const float *mean, const flo
     }
     if (cudaGetLastError() != cudaSuccess) return -1;
     if (!part) return 1;
-    split_sum<T><<<dim3((unsigned)((2 * (long long)p.C + 31) / 32), groups), kThreads, 0, s>>>(part, dw, db, 2 * (long long)p.C,
+    split_sum<T><<<dim3((unsigned)((2 * (long long)p.C + 31) / 32), groups), 32 * kSumWarps, 0, s>>>(part, dw, db, 2 * (long long)p.C,
                                                                                               p.C, b.splits);
     return cudaGetLastError() == cudaSuccess ? 2 : -1;
 }
@@ -800,8 +812,8 @@ int launch_norm_bwd(int is_bf16, const void *dy, const void *x, const void *w, c
 int launch_split_sum(int is_bf16, const float *part, void *out, long long width, int splits, cudaStream_t s) {
     using bf = __nv_bfloat16;
     const unsigned grid = (unsigned)((width + 31) / 32);
-    if (is_bf16) split_sum<bf><<<grid, kThreads, 0, s>>>(part, (bf *)out, nullptr, width, width, splits);
-    else split_sum<float><<<grid, kThreads, 0, s>>>(part, (float *)out, nullptr, width, width, splits);
+    if (is_bf16) split_sum<bf><<<grid, 32 * kSumWarps, 0, s>>>(part, (bf *)out, nullptr, width, width, splits);
+    else split_sum<float><<<grid, 32 * kSumWarps, 0, s>>>(part, (float *)out, nullptr, width, width, splits);
     return cudaGetLastError() == cudaSuccess ? 1 : -1;
 }
 
