@@ -553,47 +553,61 @@ cross_bwd_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
 
 // dk, dv of the units that more than one CTA worked on, from their sums in CTA
 // order; zeros behind a sample's length, and zero dq where there are no states.
-// One CTA a (b, h, 128 states).
+// One CTA a (b, h, `rows` states, 16 to 128): narrow where there are few CTAs
+// (20 CTAs of 128 rows 35 us, 160 of 16 rows 8.5; 384 of 128 rows 15, 960 of 32
+// rows 10), wide where finding the parts would cost as much as adding them
+// (15680 CTAs of 16 rows 44 us, 1984 of 128 rows 19).
 template <int D>
 __global__ void __launch_bounds__(256)
-cross_bwd_join(const BwdArgs a, int C) {
+cross_bwd_join(const BwdArgs a, int C, int rows) {
     constexpr int G = BC<D>::G;
+    __shared__ short which[kSmCount];    // the CTAs with granules of the unit, in order
+    __shared__ int count;
     pdl_wait();
-    const int jt = blockIdx.x, h = blockIdx.y % a.p.H, b = blockIdx.y / a.p.H, g = jt / G;
+    const int m0 = blockIdx.x * rows, jt = m0 / kT, h = blockIdx.y % a.p.H, b = blockIdx.y / a.p.H, g = jt / G;
     const int len = cross_len(a.p, b), st = state_tiles(len);
-    if (len == 0 && jt == 0)
+    if (len == 0 && blockIdx.x == 0)
         for (long long e = threadIdx.x; e < (long long)a.p.N * (D / 8); e += 256)
             *reinterpret_cast<uint4 *>(a.dq + (((long long)b * a.p.N + e / (D / 8)) * a.p.H + h) * D + e % (D / 8) * 8) =
                 make_uint4(0, 0, 0, 0);
-    // the CTAs [c0, c1] whose ranges hold the unit's granules
-    long long c0 = 0, c1 = -1, T = 1, base = 0;
-    int kt = 1;
-    if (jt < st) {
-        const long long per = (long long)a.p.H * a.nq;
-        T = tiles_of(a.p, 0, a.p.B) * per;
-        base = tiles_of(a.p, 0, b) * per + ((long long)h * st + g * G) * a.nq;
-        kt = st - g * G < G ? st - g * G : G;
+    long long c0 = 0;
+    bool whole = false;                  // written by one CTA, but for the rows behind the length
+    if (m0 < len) {
+        const long long per = (long long)a.p.H * a.nq, T = tiles_of(a.p, 0, a.p.B) * per;
+        const long long base = tiles_of(a.p, 0, b) * per + ((long long)h * st + g * G) * a.nq;
+        const int kt = st - g * G < G ? st - g * G : G;
         c0 = base * C / T;
-        c1 = (base + (long long)(a.nq - 1) * kt) * C / T;
+        const long long c1 = (base + (long long)(a.nq - 1) * kt) * C / T;
+        whole = c0 == c1;
+        if (whole && m0 + rows <= len) return;
+        if (!whole && threadIdx.x < 32) {
+            int n = 0;
+            for (long long x = c0; x <= c1; x += 32) {
+                const long long c = x + threadIdx.x, lo = (c * T + C - 1) / C, hi = ((c + 1) * T + C - 1) / C;
+                const long long k = lo <= base ? 0 : (lo - base + kt - 1) / kt;
+                const bool has = c <= c1 && k < a.nq && base + k * kt < hi;
+                const unsigned all = __ballot_sync(0xffffffffu, has);
+                if (has) which[n + __popc(all & ((1u << threadIdx.x) - 1))] = (short)c;
+                n += __popc(all);
+            }
+            if (threadIdx.x == 0) count = n;
+        }
     }
-    const bool whole = jt < st && c0 == c1;      // written by that CTA, but for the rows behind the length
-    auto granules = [&](long long c) {   // whether CTA c has granules of the unit
-        const long long lo = (c * T + C - 1) / C, hi = ((c + 1) * T + C - 1) / C;
-        const long long k = lo <= base ? 0 : (lo - base + kt - 1) / kt;
-        return k < a.nq && base + k * kt < hi;
-    };
-    for (int e = threadIdx.x; e < kT * (2 * D / 4); e += 256) {
-        const int row = e / (D / 2), f = e % (D / 2) * 4, m = jt * kT + row;
+    __syncthreads();
+    for (int e = threadIdx.x; e < rows * (2 * D / 4); e += 256) {
+        const int row = e / (D / 2), f = e % (D / 2) * 4, m = m0 + row;
         if (m >= a.p.M) break;
         if (whole && m < len) continue;
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (m < len)
-            for (long long c = c0; c <= c1; ++c) {
-                if (c > c0 && !granules(c)) continue;
-                const float4 x = *reinterpret_cast<const float4 *>(
-                    a.part + ((c * 2 + (c == c0)) * (G * kT) + (jt - g * G) * kT + row) * 2 * D + f);
+        if (m < len) {
+            const float *src = a.part + ((long long)(m - g * G * kT) * 2 * D + f);
+#pragma unroll 4
+            for (int i = 0; i < count; ++i) {
+                const long long c = which[i];
+                const float4 x = *reinterpret_cast<const float4 *>(src + (c * 2 + (c == c0)) * (G * kT * 2 * D));
                 s.x += x.x, s.y += x.y, s.z += x.z, s.w += x.w;
             }
+        }
         const float sc = f < D ? a.p.scale : 1.f;
         __nv_bfloat16 *to = f < D ? a.dk + ((long long)b * a.p.M + m) * a.p.lddk + h * D + f
                                   : a.dv + ((long long)b * a.p.M + m) * a.p.lddv + h * D + f - D;
@@ -659,7 +673,9 @@ int bwd_t(const void *q, const void *k, const void *v, const void *out, const vo
     const int grid = granules < kSmCount ? (int)granules : kSmCount;
     if (!launch_pdl(cross_bwd_tc<D>, (unsigned)grid, kThreads, BC<D>::kSmem, s, mq, mg, mo, mk, mv, a)) return -1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((a.p.M + kT - 1) / kT), (unsigned)(a.p.B * a.p.H));
+    int rows = kT;
+    while (rows > 16 && (long long)((a.p.M + rows - 1) / rows) * a.p.B * a.p.H < 4 * kSmCount) rows /= 2;
+    cfg.gridDim = dim3((unsigned)((a.p.M + rows - 1) / rows), (unsigned)(a.p.B * a.p.H));
     cfg.blockDim = dim3(256);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -667,7 +683,7 @@ int bwd_t(const void *q, const void *k, const void *v, const void *out, const vo
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, cross_bwd_join<D>, a, grid) != cudaSuccess) return -1;
+    if (cudaLaunchKernelEx(&cfg, cross_bwd_join<D>, a, grid, rows) != cudaSuccess) return -1;
     if (a.ng == 1) return 2;
     return launch_pdl(cross_dq_join<D>, 8 * kSmCount, 256, 0, s, a) ? 3 : -1;
 }
