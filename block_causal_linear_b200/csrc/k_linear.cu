@@ -13,7 +13,8 @@ template <typename T>
 __device__ __forceinline__ void epilogue(const GemmPlan &g, long long m, long long n, float z) {
     const long long o = m * g.N + n;
     if (g.bias) z += to_f(((const T *)g.bias)[n]);
-    if (g.pre) ((T *)g.pre)[o] = from_f<T>(z);
+    using P = typename PreOf<T>::type;
+    if (g.pre) ((P *)g.pre)[o] = to_pre<P>(z, g.act);
     z = act_f(z, g.act);
     if (g.res) z += to_f(((const T *)g.res)[o]);
     ((T *)g.y)[o] = from_f<T>(z);
@@ -86,8 +87,9 @@ int rows_r(const GemmPlan &g, cudaStream_t s) {
 // part[split][C].  dz or part may be null.
 template <typename T, int VEC>
 __global__ void __launch_bounds__(kThreads)
-act_col(const T *__restrict__ dy, const T *__restrict__ pre, T *__restrict__ dz, float *__restrict__ part, long long R,
-        long long C, int act) {
+act_col(const T *__restrict__ dy, const typename PreOf<T>::type *__restrict__ pre, T *__restrict__ dz,
+        float *__restrict__ part, long long R, long long C, int act) {
+    using P = typename PreOf<T>::type;
     __shared__ float red[8][32 * VEC];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const long long c = ((long long)blockIdx.x * 32 + lane) * VEC;
@@ -99,10 +101,10 @@ act_col(const T *__restrict__ dy, const T *__restrict__ pre, T *__restrict__ dz,
         for (long long r = R * sp / splits + warp; r < r1; r += 8) {
             Pack<T, VEC> d = *reinterpret_cast<const Pack<T, VEC> *>(dy + r * C + c);
             if (act) {
-                const Pack<T, VEC> z = *reinterpret_cast<const Pack<T, VEC> *>(pre + r * C + c);
+                const Pack<P, VEC> z = *reinterpret_cast<const Pack<P, VEC> *>(pre + r * C + c);
 #pragma unroll
                 for (int j = 0; j < VEC; ++j) {
-                    const float f = to_f(d.v[j]) * act_slope(to_f(z.v[j]), act);
+                    const float f = to_f(d.v[j]) * act_slope(from_pre(z.v[j]), act);
                     a[j] += f;
                     d.v[j] = from_f<T>(f);
                 }
@@ -137,7 +139,8 @@ int col_splits(long long R, long long C) {
 template <typename T, int VEC>
 int act_col_t(const void *dy, const void *pre, void *dz, float *part, long long R, long long C, int act, cudaStream_t s) {
     const dim3 grid((unsigned)((C + 32 * VEC - 1) / (32 * VEC)), (unsigned)col_splits(R, C));
-    act_col<T, VEC><<<grid, kThreads, 0, s>>>((const T *)dy, (const T *)pre, (T *)dz, part, R, C, act);
+    act_col<T, VEC><<<grid, kThreads, 0, s>>>((const T *)dy, (const typename PreOf<T>::type *)pre, (T *)dz, part, R,
+                                             C, act);
     return cudaGetLastError() == cudaSuccess ? 1 : -1;
 }
 

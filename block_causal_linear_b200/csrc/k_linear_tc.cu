@@ -7,18 +7,22 @@
 // of CTAs (cta_group::2, each holding 128 rows of A and half of B's, so that a
 // stage's copies and the MMA's reads stay within a SM's 128 bytes of shared
 // memory a clock: a 128 x 256 tile on one CTA needs 192, and ran at 66%), or
-// 128 x 128 and 128 x 64 on one CTA for small outputs.  Warp 0 fills a ring of K = 64 stages by TMA, warp 1 issues the MMAs, warps
-// 2-9 run the epilogue of one tile while the MMAs of the next fill the other
-// half of TMEM.  Either operand may be stored with its k index contiguous
-// (K-major boxes of 64 x rows) or with its row index contiguous (MN-major
-// boxes of 64 rows x 64 k): the three products of a linear layer need no
-// transposed copies.  The residual arrives and the outputs leave by TMA
-// through per-warp buffers of 32 x 32.
+// 128 x 128 and 128 x 64 on one CTA for small outputs.  Warp 0 fills a ring of
+// K = 64 stages by TMA, warp 1 issues the MMAs, warps 2-9 run the epilogue of
+// one tile while the MMAs of the next fill the other half of TMEM.  Either
+// operand may be stored with its k index contiguous (K-major boxes of 64 x
+// rows) or with its row index contiguous (MN-major boxes of 64 rows x 64 k):
+// the three products of a linear layer need no transposed copies.  The
+// residual arrives and the outputs leave by TMA through per-warp buffers of 32
+// x 32.  Bound by the tensor cores: 8190 x 2048 -> 5120 with bias and SiLU
+// KFIG.
 // fp32 operands are split into three bf16 parts each, x = hi + mid + lo exactly
 // (24 bits), and the product is the sum of the six part products down to 2^-24
-// of it: lo hi, hi lo, mid mid, mid hi, hi mid, hi hi, accumulated in fp32 one
-// after another along k.  Six products at the tensor cores' bf16 rate are three
-// times what the CUDA cores' fp32 units can do.
+// of it: lo hi, hi lo, mid mid, mid hi, hi mid, hi hi, one after another along
+// k.  The tensor cores round their running sums towards zero (1.5e-6 of the
+// result, rms, over 1023 k), so only 256 k at a time are left to them; the
+// epilogue adds these in registers (2.6e-7).  Six products at the tensor cores'
+// bf16 rate are three times what the CUDA cores' fp32 units can do.
 #include <cudaTypedefs.h>
 #include <mutex>
 #include <type_traits>
@@ -39,6 +43,7 @@ constexpr int kEpi = 8;                           // epilogue warps: two a quart
 constexpr int kThreads = 64 + 32 * kEpi;
 constexpr int kChunk = 32;                        // output columns an epilogue step
 constexpr int kBuf = 32 * kChunk * 2;             // one warp's 32 x 32 bf16 buffer
+constexpr int kRun = 4;                           // fp32: stages whose products the tensor cores add up
 
 // CG CTAs share a tile of CG * 128 x BN: each holds its 128 rows of A and BN / CG of B's.
 template <int BN, int CG>
@@ -62,7 +67,8 @@ struct TcArgs {
     int kblk;                // fp32: stages of one part product
     int a_mn, b_mn;
     const __nv_bfloat16 *bias, *res;
-    __nv_bfloat16 *pre, *y;
+    void *pre;
+    __nv_bfloat16 *y;
     float *part;             // the pieces' sums, fp32 [tile - tail][piece][CG * 128][BN]
     int act;
     int direct;              // rows of y are not whole 16 bytes: no TMA on y, pre, res
@@ -79,12 +85,12 @@ __device__ __forceinline__ void block_in(uint8_t *buf, const __nv_bfloat16 *src,
             *reinterpret_cast<__nv_bfloat16 *>(buf + sw64(r, lane >> 3) + (lane & 7) * 2) =
                 src[(row0 + r) * a.N + col0 + lane];
 }
-__device__ __forceinline__ void block_out(const uint8_t *buf, __nv_bfloat16 *dst, long long row0, long long col0,
+__device__ __forceinline__ void block_out(const uint8_t *buf, uint16_t *dst, long long row0, long long col0,
                                           const TcArgs &a, int lane) {
     for (int r = 0; r < 32; ++r)
         if (row0 + r < a.M && col0 + lane < a.N)
             dst[(row0 + r) * a.N + col0 + lane] =
-                *reinterpret_cast<const __nv_bfloat16 *>(buf + sw64(r, lane >> 3) + (lane & 7) * 2);
+                *reinterpret_cast<const uint16_t *>(buf + sw64(r, lane >> 3) + (lane & 7) * 2);
 }
 
 // One piece of work: a whole tile, or one of the pieces along k of a tail tile.
@@ -122,6 +128,16 @@ __device__ __forceinline__ void put_chunk(uint8_t *buf, const float (&v)[32], in
         *reinterpret_cast<uint4 *>(buf + sw64(lane, j)) =
             make_uint4(pack_bf2(v[8 * j], v[8 * j + 1]), pack_bf2(v[8 * j + 2], v[8 * j + 3]),
                        pack_bf2(v[8 * j + 4], v[8 * j + 5]), pack_bf2(v[8 * j + 6], v[8 * j + 7]));
+}
+
+__device__ __forceinline__ void put_pre(uint8_t *buf, const float (&v)[32], int act, int lane) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        __half2 h[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[i] = pre_half2(v[8 * j + 2 * i], v[8 * j + 2 * i + 1], act);
+        *reinterpret_cast<uint4 *>(buf + sw64(lane, j)) = *reinterpret_cast<const uint4 *>(h);
+    }
 }
 
 // PARTS: the operands are three bf16 planes each (maps of three dimensions),
@@ -221,40 +237,83 @@ gemm_tc(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtens
         // one MMA's 16 k: 32 bytes along a K-major row, two 8-k groups of 1024 bytes MN-major (in 16-byte units)
         const uint64_t astep = (a.a_mn ? 2048 : 32) >> 4, bstep = (a.b_mn ? 2048 : 32) >> 4;
         bool ok = true;
-        for (int w = first; ok && w < works; w += step, ++tiles) {
+        for (int w = first; ok && w < works; w += step) {
             const Work k_ = work_of(a, w);
-            const int k0 = k_.k0, k1 = k_.k1;
-            const int buf = tiles & 1;
-            if (!(ok = mbar_poll(&acc_empty[buf], ((uint32_t)(tiles >> 1) & 1u) ^ 1u, abort_word, &g_linear_flag, 2)))
-                break;
-            tc_fence_after();
-            for (int k = k0; k < k1; ++k, ++issued) {
-                const int s = issued % C::kStages;
-                if (!(ok = mbar_poll(&full[s], (uint32_t)(issued / C::kStages) & 1u, abort_word, &g_linear_flag, 3)))
+            const int run = PARTS ? kRun : k_.k1 - k_.k0;
+            for (int k0 = k_.k0; ok && k0 < k_.k1; k0 += run, ++tiles) {
+                const int k1 = k0 + run < k_.k1 ? k0 + run : k_.k1, buf = tiles & 1;
+                if (!(ok = mbar_poll(&acc_empty[buf], ((uint32_t)(tiles >> 1) & 1u) ^ 1u, abort_word, &g_linear_flag, 2)))
                     break;
                 tc_fence_after();
-                const uint32_t sa = smem_u32(smem + s * C::kStage);
-                uint64_t da = smem_desc(sa, a.a_mn ? 8192 : 16, 1024, kLayoutSw128);
-                uint64_t db = smem_desc(sa + C::kA, a.b_mn ? 8192 : 16, 1024, kLayoutSw128);
-                if (one) {
+                for (int k = k0; k < k1; ++k, ++issued) {
+                    const int s = issued % C::kStages;
+                    if (!(ok = mbar_poll(&full[s], (uint32_t)(issued / C::kStages) & 1u, abort_word, &g_linear_flag, 3)))
+                        break;
+                    tc_fence_after();
+                    const uint32_t sa = smem_u32(smem + s * C::kStage);
+                    uint64_t da = smem_desc(sa, a.a_mn ? 8192 : 16, 1024, kLayoutSw128);
+                    uint64_t db = smem_desc(sa + C::kA, a.b_mn ? 8192 : 16, 1024, kLayoutSw128);
+                    if (one) {
 #pragma unroll
-                    for (int kk = 0; kk < kBK / 16; ++kk, da += astep, db += bstep) {
-                        const uint32_t acc = k > k0 || kk > 0 ? 1u : 0u;
-                        if constexpr (CG == 2) mma_bf16_pair(tmem + buf * BN, da, db, id, acc);
-                        else mma_bf16(tmem + buf * BN, da, db, id, acc);
+                        for (int kk = 0; kk < kBK / 16; ++kk, da += astep, db += bstep) {
+                            const uint32_t acc = k > k0 || kk > 0 ? 1u : 0u;
+                            if constexpr (CG == 2) mma_bf16_pair(tmem + buf * BN, da, db, id, acc);
+                            else mma_bf16(tmem + buf * BN, da, db, id, acc);
+                        }
+                        if constexpr (CG == 2) mma_commit_pair(&empty[s]);
+                        else mma_commit(&empty[s]);
                     }
-                    if constexpr (CG == 2) mma_commit_pair(&empty[s]);
-                    else mma_commit(&empty[s]);
+                    __syncwarp();
+                }
+                if (ok && one) {
+                    if constexpr (CG == 2) mma_commit_pair(&acc_full[buf]);
+                    else mma_commit(&acc_full[buf]);
                 }
                 __syncwarp();
             }
-            if (ok && one) {
-                if constexpr (CG == 2) mma_commit_pair(&acc_full[buf]);
-                else mma_commit(&acc_full[buf]);
-            }
-            __syncwarp();
         }
-    } else if (warp >= 2) {
+    } else if (PARTS && warp >= 2) {
+        // a tile's runs are added in registers: its 32 lanes x BN / 2 columns
+        constexpr int NC = BN / (2 * kChunk);
+        const int e = warp - 2, q = warp & 3;
+        int t = 0;
+        bool ok = true;
+        for (int w = first; ok && w < works; w += step) {
+            const Work k_ = work_of(a, w);
+            float sum[NC][32] = {};
+            for (int k0 = k_.k0; k0 < k_.k1; k0 += kRun, ++t) {
+                const int buf = t & 1;
+                if (!(ok = mbar_poll(&acc_full[buf], (uint32_t)(t >> 1) & 1u, abort_word, &g_linear_flag, 4))) break;
+                tc_fence_after();
+                __syncwarp();
+#pragma unroll
+                for (int c = 0; c < NC; ++c) {
+                    float x[32];
+                    tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + buf * BN + (e >> 2) * (BN / 2) + c * kChunk, x);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) sum[c][j] += x[j];
+                }
+                tc_fence_before();
+                if constexpr (CG == 2) mbar_arrive_leader(&acc_empty[buf]);
+                else mbar_arrive(&acc_empty[buf]);
+            }
+            if (!ok) break;
+            const long long row = ((long long)(k_.tile / a.nt) * CG + rank) * kBM + q * 32 + lane;
+            const long long n0 = (long long)(k_.tile % a.nt) * BN + (e >> 2) * (BN / 2);
+            if (row >= a.M) continue;
+            float *o = a.part + (((long long)k_.tile * a.splits + k_.piece) * (CG * kBM) + rank * kBM + q * 32 + lane) * BN +
+                       (e >> 2) * (BN / 2);
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+                if (n0 + c * kChunk < a.N) {
+#pragma unroll
+                    for (int j = 0; j < 32; j += 4)
+                        *reinterpret_cast<float4 *>(o + c * kChunk + j) =
+                            make_float4(sum[c][j], sum[c][j + 1], sum[c][j + 2], sum[c][j + 3]);
+                }
+        }
+    } else if (!PARTS && warp >= 2) {
         constexpr int NC = BN / (2 * kChunk);                   // column chunks of this warp in a tile
         const int e = warp - 2, q = warp & 3;                   // q: this warp's quarter of the TMEM lanes
         uint8_t *bufs = smem + C::kStg + e * 2 * kBuf;
@@ -332,7 +391,7 @@ gemm_tc(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtens
                     for (int j = 0; j < 32; ++j)
                         if (col + j < a.N) x[j] += __bfloat162float(a.bias[col + j]);
                 }
-                if (a.pre) put_chunk(pb, x, lane);
+                if (a.pre) put_pre(pb, x, a.act, lane);
                 act_chunk(x, a.act);
                 if (a.res) {
                     if (tma) {
@@ -356,8 +415,8 @@ gemm_tc(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtens
                     }
                 } else {
                     __syncwarp();
-                    block_out(yb, a.y, row0, col, a, lane);
-                    if (a.pre) block_out(pb, a.pre, row0, col, a, lane);
+                    block_out(yb, (uint16_t *)a.y, row0, col, a, lane);
+                    if (a.pre) block_out(pb, (uint16_t *)a.pre, row0, col, a, lane);
                     __syncwarp();
                 }
             }
@@ -411,7 +470,9 @@ gemm_finish(const TcArgs a) {
     float z[4] = {s.x, s.y, s.z, s.w};
     const long long e = m * a.N + n;
     const T *bias = (const T *)a.bias, *res = (const T *)a.res;
-    T *pre = (T *)a.pre, *y = (T *)a.y;
+    using Pre = typename PreOf<T>::type;
+    Pre *pre = (Pre *)a.pre;
+    T *y = (T *)a.y;
     if (a.N % 4 == 0) {                                         // whole groups of four
         struct alignas(4 * sizeof(T)) Four {
             T v[4];
@@ -421,18 +482,22 @@ gemm_finish(const TcArgs a) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) z[j] += to_f(f.v[j]);
         };
-        auto put = [&](T *p) {
-            Four f;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) f.v[j] = from_f<T>(z[j]);
-            *reinterpret_cast<Four *>(p) = f;
-        };
         if (bias) add(bias + n);
-        if (pre) put(pre + e);
+        if (pre) {
+            struct alignas(4 * sizeof(T)) FourPre {
+                Pre v[4];
+            } f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f.v[j] = to_pre<Pre>(z[j], a.act);
+            *reinterpret_cast<FourPre *>(pre + e) = f;
+        }
 #pragma unroll
         for (int j = 0; j < 4; ++j) z[j] = act_f(z[j], a.act);
         if (res) add(res + e);
-        put(y + e);
+        Four f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f.v[j] = from_f<T>(z[j]);
+        *reinterpret_cast<Four *>(y + e) = f;
         return;
     }
 #pragma unroll
@@ -440,7 +505,7 @@ gemm_finish(const TcArgs a) {
         if (n + j >= a.N) break;
         float f = z[j];
         if (bias) f += to_f(bias[n + j]);
-        if (pre) pre[e + j] = from_f<T>(f);
+        if (pre) pre[e + j] = to_pre<Pre>(f, a.act);
         f = act_f(f, a.act);
         if (res) f += to_f(res[e + j]);
         y[e + j] = from_f<T>(f);
@@ -621,7 +686,7 @@ int run_tile(const GemmPlan &g, const TcPlan &p, void *ws, cudaStream_t s) {
     a.kblk = p.kiters / (PARTS ? 6 : 1);
     a.a_mn = g.a_mn; a.b_mn = g.b_mn;
     a.bias = (const __nv_bfloat16 *)g.bias; a.res = (const __nv_bfloat16 *)g.res;
-    a.pre = (__nv_bfloat16 *)g.pre; a.y = (__nv_bfloat16 *)g.y;
+    a.pre = g.pre; a.y = (__nv_bfloat16 *)g.y;
     a.part = (float *)ws;
     a.act = g.act;
     a.direct = g.N % 8 != 0;

@@ -563,6 +563,7 @@ def full_backward(q, k, v, dout, tokens_per_block=0, rope: Optional[la_rope] = N
 # ---------------------------------------------------------------- layer norm, linear, cross attention
 
 LA_ACT = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
+_PRE_DTYPE = {torch.bfloat16: torch.float16, torch.float32: torch.float32}   # of linear's pre
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
@@ -746,7 +747,8 @@ def linear_forward(x, weight, bias=None, act="none", residual=None, return_pre=F
     """act(x weight^T + bias) + residual: x [..., K], weight [N, K], bias [N], residual
     [..., N]; act "none", "relu", "silu" or "gelu" (tanh form).  Returns y, or with
     return_pre (y, z), z being what the activation acts on, for linear_backward (None
-    without an activation, where the backward pass needs none).  out may be the
+    without an activation, where the backward pass needs none): fp32, or of bf16
+    tensors fp16 held to +-65504.  pre may give its buffer, out may be the
     residual's tensor."""
     R, K, N, dt = _linear_sizes(x, weight)
     code = _act_code(act)
@@ -755,10 +757,10 @@ def linear_forward(x, weight, bias=None, act="none", residual=None, return_pre=F
     _check_like("bias", bias, (N,), x.dtype, x.device)
     _check_like("residual", residual, shape, x.dtype, x.device)
     _check_like("out", out, shape, x.dtype, x.device)
-    _check_like("pre", pre, shape, x.dtype, x.device)
+    _check_like("pre", pre, shape, _PRE_DTYPE[x.dtype], x.device)
     y = _new(x, shape, stream) if out is None else out
     if return_pre and pre is None and code:
-        pre = _like(y, stream)
+        pre = _new(x, shape, stream, _PRE_DTYPE[x.dtype])
     ws = _workspace("la_linear_workspace_size", (R, K, N, dt), ws, x, stream)
     _launch("la_linear_forward", lib().la_linear_forward, x.device, stream, x.data_ptr(), weight.data_ptr(), _ptr(bias),
             _ptr(residual), y.data_ptr(), _ptr(pre), dt, code, R, K, N, ws.data_ptr(), ws.nbytes)
@@ -775,7 +777,7 @@ def linear_backward(dy, x, weight, pre=None, act="none", input_grad=True, weight
     shape = (*x.shape[:-1], N)
     _check_stream(x.device, stream)
     _check_like("dy", dy, shape, x.dtype, x.device)
-    _check_like("pre", pre, shape, x.dtype, x.device)
+    _check_like("pre", pre, shape, _PRE_DTYPE[x.dtype], x.device)
     if code and pre is None:
         raise ValueError("pre is missing (linear_forward with return_pre gives it)")
     if grads is None:

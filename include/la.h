@@ -380,12 +380,15 @@ LA_API la_status la_layer_norm_backward(const void *dy, const void *x, const voi
  * with act none, ReLU, SiLU (z / (1 + e^-z)) or GELU in its tanh form
  * (z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3)))).  y may be the residual's
  * buffer (the residual stream updated in place).  pre, if not NULL, receives
- * z (rounded to dt) for the backward pass.
+ * z for the backward pass: fp32 with LA_F32; with LA_BF16 fp16, held to +-65504
+ * (and with ReLU a positive z to at least 2^-24).
  * Backward, given dy:  dz = dy act'(z),
  *   dx = dz weight [R][K],  dweight = dz^T x [N][K],  dbias = sum_rows dz [N];
  * the residual's gradient is dy itself.  dx, dweight and dbias may each be
  * NULL (then weight, x are not needed).  pre is read only with an
  * activation, and dz is then rounded to dt once, as the products' operand.
+ * With more than 8 rows an infinite element of a LA_F32 operand makes the
+ * results it enters NaN (the product runs on the elements' bf16 parts).
  */
 typedef enum { LA_ACT_NONE = 0, LA_ACT_RELU = 1, LA_ACT_SILU = 2, LA_ACT_GELU = 3 } la_act;
 LA_API size_t la_linear_workspace_size(int R, int K, int N, la_dtype dt);

@@ -117,6 +117,10 @@ def linear_forward(x, w, b, name, res):
     return y, z, sy, sz
 
 
+# half the distance of fp16's subnormal numbers, which hold a small z of bf16 products
+PRE_ABS = 2.0 ** -25
+
+
 def linear_backward(dy, x, w, pre, name, dtype):
     """dx, dw, db and their slacks, from the given pre (an input of the call)."""
     dy, x, w = dy.double(), x.double(), w.double()

@@ -54,7 +54,8 @@ def test_linear_matches_reference(la, case):
     ref.check("y", y, ry, sy, dtype)
     assert (pre is None) == (act == "none")
     if pre is not None:
-        ref.check("pre", pre, rz, sz, dtype)
+        assert pre.dtype == (torch.float16 if dtype is BF else F32)
+        ref.check("pre", pre, rz, sz + ref.PRE_ABS, pre.dtype)
     assert torch.equal(la.linear_forward(x, w, b, act=act, residual=r), y)
     got = la.linear_backward(dy, x, w, pre=pre, act=act)
     for name, g, (want, s) in zip(("dx", "dw", "db"), got, ref.linear_backward(dy, x, w, pre, act, dtype)):
@@ -75,10 +76,10 @@ def test_linear_parts(la, R):
         got = la.linear_backward(dy, x, w, pre=pre, act="silu", input_grad=want[0], weight_grad=want[1],
                                  bias_grad=want[2])
         assert [g is not None for g in got] == want and torch.equal(got[i], full[i])
-    z = torch.empty_like(y)
+    z = torch.empty_like(y, dtype=torch.float16)
     la.linear_forward(x, w, b, return_pre=True, pre=z)
     _, rz, _, sz = ref.linear_forward(x, w, b, "none", None)
-    ref.check("pre", z, rz, sz, BF)
+    ref.check("pre", z, rz, sz + ref.PRE_ABS, z.dtype)
     inplace = r.clone()
     la.linear_forward(x, w, b, act="silu", residual=inplace, out=inplace)
     assert torch.equal(inplace, y)
@@ -127,6 +128,20 @@ def test_slopes_of_huge_inputs(la):
         y, pre = la.linear_forward(x, w, act=act, return_pre=True)
         dx, _, _ = la.linear_backward(torch.ones_like(y), x, w, pre=pre, act=act)
         assert y[0] == 1e30 and y[1] == 0 and dx[0] == 1 and dx[1] == 0
+
+
+@pytest.mark.parametrize("rows", [1, 40])
+@pytest.mark.parametrize("act", ["relu", "silu", "gelu"])
+def test_slopes_at_the_ends_of_fp16(la, act, rows):
+    """bf16 z beyond fp16's range, and below its smallest number: the slopes are those of z."""
+    z = torch.tensor([1e30, 1e6, 7e4, 6e4, 1e-9, 1e-30, 0.0, -0.0, -1e-30, -1e-9, -6e4, -7e4, -1e6, -1e30],
+                     dtype=BF, device="cuda")
+    x, w = torch.ones(rows, 1, dtype=BF, device="cuda"), z[:, None].contiguous()
+    y, pre = la.linear_forward(x, w, act=act, return_pre=True)
+    assert pre.isfinite().all() and pre.abs().max() == 65504
+    got = la.linear_backward(torch.ones_like(y), x, w, pre=pre, act=act)[2]      # db: the slopes' sums over the rows
+    slope = ref.act(z.double().clamp(-100, 100), act)[1]
+    ref.check("db", got, rows * slope, rows * (ref.half(BF) + ref.ACT_REL + 1e-6), BF)
 
 
 def test_linear_writes_only_its_outputs(la):
