@@ -24,6 +24,13 @@
 // device).  A unit that one CTA finishes is written at once; the others leave
 // fp32 sums that a second kernel joins in CTA order.  More states than a group
 // holds: dq is summed over the groups the same way.
+//
+// D_i = dout_i . out_i carries the rounding of out, which is coherent over a
+// query's states: 1e-3 of dq and dk with 17 states, 3e-3 with 2, beside the
+// 2.35e-3 of rounding ds and the results.  Up to 128 states a pass before takes
+// D_i = sum_j p_ij dp_ij instead (128 us before this kernel's 231, for 4 x 8190
+// queries against 128 states, 64 heads of 32); above, the error from out is
+// below 4e-4.
 #include "la_sm100_dit.cuh"
 
 namespace la {
@@ -66,6 +73,7 @@ struct BwdArgs {
     int nq, ng;                      // query tiles, groups of state tiles (of M)
     __nv_bfloat16 *dq, *dk, *dv;
     const float *lse;
+    float *dsum;                     // D [B][H][N] from cross_dsum, or null: from out
     float *part;                     // [CTA][2][G * 128][2 D]: dk, dv of a unit begun earlier (0) or not finished (1)
     float *dqp;                      // ng > 1: [ng][B][N][H][D]
 };
@@ -226,10 +234,10 @@ cross_bwd_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 if (!(ok = mbar_poll(&q_empty[s], ((uint32_t)(qt >> 1) & 1u) ^ 1u, abort_word, flag, 2))) break;
                 if (one) {
                     uint8_t *st = smem + C::kQ + s * C::kStage;
-                    mbar_arrive_expect_tx(&q_full[s], C::kStage);
+                    mbar_arrive_expect_tx(&q_full[s], (a.dsum ? 2 : 3) * C::kTile);
                     tma_load_3d(st, &tm_q, &q_full[s], sg.h * D, k * kT, sg.b);
                     tma_load_3d(st + C::kTile, &tm_do, &q_full[s], sg.h * D, k * kT, sg.b);
-                    tma_load_3d(st + 2 * C::kTile, &tm_o, &q_full[s], sg.h * D, k * kT, sg.b);
+                    if (!a.dsum) tma_load_3d(st + 2 * C::kTile, &tm_o, &q_full[s], sg.h * D, k * kT, sg.b);
                 }
                 __syncwarp();
             }
@@ -393,17 +401,19 @@ cross_bwd_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 const int i = k * kT + r;
                 // (a row behind the last query: p = exp2 of far less than -126, which is 0, for any scale the entry points take)
                 const float ls = i < a.p.N ? -a.lse[bh + i] * per : -1e30f;
+                float d = a.dsum && i < a.p.N ? a.dsum[bh + i] : 0.f;
                 if (!mbar_poll(&q_full[t & 1], (uint32_t)(t >> 1) & 1u, abort_word, flag, 10)) return false;
                 const uint8_t *st = smem + C::kQ + (t & 1) * C::kStage;
-                float d = 0.f;
+                if (!a.dsum) {
 #pragma unroll
-                for (int ch = 0; ch < D / 8; ++ch) {
-                    const int off = D == 32 ? r * 64 + ((ch ^ ((r >> 1) & 3)) << 4) : r * 128 + ((ch ^ (r & 7)) << 4);
-                    const uint4 x = *reinterpret_cast<const uint4 *>(st + C::kTile + off);
-                    const uint4 y = *reinterpret_cast<const uint4 *>(st + 2 * C::kTile + off);
-                    const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+                    for (int ch = 0; ch < D / 8; ++ch) {
+                        const int off = D == 32 ? r * 64 + ((ch ^ ((r >> 1) & 3)) << 4) : r * 128 + ((ch ^ (r & 7)) << 4);
+                        const uint4 x = *reinterpret_cast<const uint4 *>(st + C::kTile + off);
+                        const uint4 y = *reinterpret_cast<const uint4 *>(st + 2 * C::kTile + off);
+                        const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) d += bf_lo(xw[e]) * bf_lo(yw[e]) + bf_hi(xw[e]) * bf_hi(yw[e]);
+                        for (int e = 0; e < 4; ++e) d += bf_lo(xw[e]) * bf_lo(yw[e]) + bf_hi(xw[e]) * bf_hi(yw[e]);
+                    }
                 }
                 uint8_t *ext = smem + C::kExt + (t & 1) * 2 * C::kExtTile + (r >> 3) * 256 + (r & 7) * 16;
                 *reinterpret_cast<uint4 *>(ext) = parts(ls);
@@ -551,6 +561,187 @@ cross_bwd_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
     }
 }
 
+// D_i = sum_j p_ij (dout_i . v_j), for up to 128 states: S = Q K^T and dP = dO
+// V^T of a tile of 128 queries in two buffers of TMEM, four warps a buffer, a
+// thread a query; one CTA a SM, persistent over (b, h, query tile).  Bound by
+// the rate at which a SM copies rows of 64 or 128 bytes (about 430 a us: 4 x 8190
+// queries against 128 states, 64 heads of 32: 128 us, 16357 against 77, 32 heads
+// of 64: 35).  Keeping k and v while the (b, h) stays measured 60 -> 50 us for
+// 60311 queries against 17 states but 128 -> 142 and 35 -> 38 there.
+template <int D>
+struct DC {
+    static constexpr int kTile = kT * D * 2, kStage = 4 * kTile;   // q, dout, k, v
+    static constexpr int kStages = D == 32 ? 6 : 3;
+    static constexpr int kBar = kStages * kStage, kBars = 2 * kStages + 5;
+    static constexpr int kSmem = kBar + kBars * 8 + 16 + 1024;
+};
+constexpr int kDThreads = 64 + 256;
+
+template <int D>
+__global__ void __launch_bounds__(kDThreads, 1)
+cross_dsum(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
+           const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const BwdArgs a,
+           const unsigned items) {
+    using C = DC<D>;
+    constexpr uint32_t kLay = BC<D>::kLayout;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = align1024(smem_raw);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::kBar), *empty = full + C::kStages;
+    uint64_t *acc_full = empty + C::kStages, *acc_free = acc_full + 2, *fin = acc_free + 2;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(fin + 1);
+    volatile int *abort_word = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    const int warp = uniform_warp(), lane = threadIdx.x & 31;
+    unsigned *const flag = &g_cross_bwd_flag;
+
+    if (threadIdx.x == 64) {
+        prefetch_tmap(&tm_q);
+        prefetch_tmap(&tm_do);
+        prefetch_tmap(&tm_k);
+        prefetch_tmap(&tm_v);
+    }
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::kStages; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
+        for (int i = 0; i < 2; ++i) mbar_init(&acc_full[i], 1), mbar_init(&acc_free[i], 128);
+        mbar_init(fin, 1);
+        *abort_word = 0;
+        fence_barrier_init();
+    }
+    pdl_wait();            // (before the allocation, as in cross_bwd_tc)
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;    // buffer i: S at 256 i, dP at 256 i + 128
+    pdl_trigger();
+    // item w = ((b H + h) nq + query tile); the ones of samples without states are left out by every role
+    unsigned w = blockIdx.x;
+    int b = -1, h = 0, k = 0, len = 0, t = 0;              // t: items so far
+    // the next item with states
+    auto item = [&] {
+        for (; w < items; w += gridDim.x) {
+            const unsigned bh = w / (unsigned)a.nq;
+            const int nb = (int)(bh / (unsigned)a.p.H);
+            h = (int)(bh - (unsigned)nb * (unsigned)a.p.H);
+            k = (int)(w - bh * (unsigned)a.nq);
+            if (nb != b) b = nb, len = cross_len(a.p, b);
+            if (len > 0) {
+                w += gridDim.x;
+                return true;
+            }
+        }
+        return false;
+    };
+
+    if (warp == 0) {
+        const bool one = elect_one();
+        while (item()) {
+            const int s = t % C::kStages;
+            if (!mbar_poll(&empty[s], (uint32_t)(t / C::kStages) & 1u ^ 1u, abort_word, flag, 18)) break;
+            if (one) {
+                uint8_t *st = smem + s * C::kStage;
+                mbar_arrive_expect_tx(&full[s], C::kStage);
+                tma_load_3d(st, &tm_q, &full[s], h * D, k * kT, b);
+                tma_load_3d(st + C::kTile, &tm_do, &full[s], h * D, k * kT, b);
+                tma_load_3d(st + 2 * C::kTile, &tm_k, &full[s], h * D, 0, b);
+                tma_load_3d(st + 3 * C::kTile, &tm_v, &full[s], h * D, 0, b);
+            }
+            __syncwarp();
+            ++t;
+        }
+        if (*abort_word && one)        // let the copies in flight land
+            for (int i = t > C::kStages ? t - C::kStages : 0; i < t; ++i)
+                final_wait(&full[i % C::kStages], (uint32_t)(i / C::kStages) & 1u);
+        __syncwarp();
+    } else if (warp == 1) {
+        const bool one = elect_one();
+        constexpr uint64_t tile = C::kTile >> 4;
+        const uint64_t d0 = smem_desc(smem_u32(smem), 16, BC<D>::kGroup, kLay);
+        while (item()) {
+            const int s = t % C::kStages, i = t & 1;
+            if (!mbar_poll(&acc_free[i], (uint32_t)(t >> 1) & 1u ^ 1u, abort_word, flag, 19)) break;
+            if (!mbar_poll(&full[s], (uint32_t)(t / C::kStages) & 1u, abort_word, flag, 20)) break;
+            tc_fence_after();
+            const uint64_t ds = d0 + (uint64_t)(s * C::kStage >> 4);
+            const uint32_t id = idesc_bf16(kT, (len + 15) / 16 * 16, 0, 0);
+            if (one) {
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) mma_bf16(tmem + 256 * i, ds + 2 * kk, ds + 2 * tile + 2 * kk, id, kk > 0);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) mma_bf16(tmem + 256 * i + 128, ds + tile + 2 * kk, ds + 3 * tile + 2 * kk, id, kk > 0);
+                mma_commit(&empty[s]);
+                mma_commit(&acc_full[i]);
+            }
+            __syncwarp();
+            ++t;
+        }
+        if (*abort_word && one) {
+            mma_commit(fin);
+            final_wait(fin, 0);
+        }
+        __syncwarp();
+    } else {
+        const int g = (warp - 2) >> 2, q = warp & 3;       // the buffer, the quarter of the TMEM lanes
+        const uint32_t tl = tmem + ((uint32_t)(q * 32) << 16) + 256 * g;
+        const float c = a.p.scale * kLog2e;
+        // this group's items, a step ahead for the latency of lse
+        long long at = 0;
+        bool in = false;
+        float m = 0.f;
+        auto next = [&] {
+            while (item()) {
+                if ((t++ & 1) != g) continue;
+                const int r = k * kT + q * 32 + lane;
+                at = ((long long)b * a.p.H + h) * a.p.N + r;
+                in = r < a.p.N;
+                m = in ? a.lse[at] * kLog2e : 0.f;
+                return true;
+            }
+            return false;
+        };
+        uint32_t ph = 0;
+        for (bool more = next(); more; ph ^= 1u) {
+            const long long at0 = at;
+            const bool in0 = in;
+            const float m0 = m;
+            const int len0 = len;
+            more = next();
+            if (!mbar_poll(&acc_full[g], ph, abort_word, flag, 21)) break;
+            tc_fence_after();
+            __syncwarp();
+            float2 sum = make_float2(0.f, 0.f);
+#pragma unroll 1
+            for (int c0 = 0; c0 < len0; c0 += 32) {
+                float s[32], dp[32];
+                tmem_ld32(tl + c0, s);
+                tmem_ld32(tl + 128 + c0, dp);
+                tmem_wait_ld();
+                if (len0 - c0 < 32) {                      // states behind the length may hold NaN
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (c0 + e >= len0) s[e] = -INFINITY, dp[e] = 0.f;
+                }
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) {
+                    const float2 x = ffma2(make_float2(s[e], s[e + 1]), make_float2(c, c), make_float2(-m0, -m0));
+                    sum = ffma2(make_float2(ex2(x.x), ex2(x.y)), make_float2(dp[e], dp[e + 1]), sum);
+                }
+            }
+            tc_fence_before();
+            mbar_arrive(&acc_free[g]);
+            if (in0) a.dsum[at0] = sum.x + sum.y;
+        }
+    }
+    __syncwarp();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
 // dk, dv of the units that more than one CTA worked on, from their sums in CTA
 // order; zeros behind a sample's length, and zero dq where there are no states.
 // One CTA a (b, h, `rows` states, 16 to 128): narrow where there are few CTAs
@@ -638,14 +829,16 @@ cross_dq_join(const BwdArgs a) {
 int groups_of(const CrossPlan &p) { return (p.M + kT * (p.d == 32 ? 4 : 2) - 1) / (kT * (p.d == 32 ? 4 : 2)); }
 
 struct BwdWs {
-    size_t dqp, total;
+    size_t dqp, dsum, total;
 };
+constexpr int kSumStates = kT;           // states up to which D is summed from them
 BwdWs bwd_ws(const CrossPlan &p) {
     BwdWs w;
     const int G = p.d == 32 ? 4 : 2;
     w.dqp = align256(size_t(kSmCount) * 2 * G * kT * 2 * p.d * sizeof(float));
     const int ng = groups_of(p);
-    w.total = w.dqp + (ng > 1 ? align256(size_t(ng) * p.B * p.N * p.H * p.d * sizeof(float)) : 0);
+    w.dsum = w.dqp + (ng > 1 ? align256(size_t(ng) * p.B * p.N * p.H * p.d * sizeof(float)) : 0);
+    w.total = w.dsum + (p.M <= kSumStates ? align256(size_t(p.B) * p.N * p.H * sizeof(float)) : 0);
     return w;
 }
 
@@ -658,7 +851,8 @@ bool head_map(CUtensorMap *m, const void *base, const CrossPlan &p, int rows, lo
 
 bool g_ready[128] = {};
 bool setup() {
-    return set_smem((const void *)cross_bwd_tc<32>, BC<32>::kSmem) && set_smem((const void *)cross_bwd_tc<64>, BC<64>::kSmem);
+    return set_smem((const void *)cross_bwd_tc<32>, BC<32>::kSmem) && set_smem((const void *)cross_bwd_tc<64>, BC<64>::kSmem) &&
+           set_smem((const void *)cross_dsum<32>, DC<32>::kSmem) && set_smem((const void *)cross_dsum<64>, DC<64>::kSmem);
 }
 
 template <int D>
@@ -669,6 +863,12 @@ int bwd_t(const void *q, const void *k, const void *v, const void *out, const vo
     if (!head_map(&mq, q, a.p, a.p.N, ld) || !head_map(&mg, dout, a.p, a.p.N, ld) || !head_map(&mo, out, a.p, a.p.N, ld) ||
         !head_map(&mk, k, a.p, a.p.M, a.p.ldk) || !head_map(&mv, v, a.p, a.p.M, a.p.ldv))
         return -1;
+    if (a.dsum) {
+        const unsigned items = (unsigned)(a.p.B * a.p.H) * (unsigned)a.nq;      // (below 2^31: cross_tc_fits)
+        if (!launch_pdl(cross_dsum<D>, items < kSmCount ? items : kSmCount, kDThreads, DC<D>::kSmem, s, mq, mg, mk, mv, a,
+                        items))
+            return -1;
+    }
     const long long granules = (long long)a.p.B * a.p.H * a.ng * a.nq;
     const int grid = granules < kSmCount ? (int)granules : kSmCount;
     if (!launch_pdl(cross_bwd_tc<D>, (unsigned)grid, kThreads, BC<D>::kSmem, s, mq, mg, mo, mk, mv, a)) return -1;
@@ -703,7 +903,9 @@ int launch_cross_bwd_tc(const void *q, const void *k, const void *v, const void 
     a.dv = (__nv_bfloat16 *)dv;
     a.lse = lse;
     a.part = (float *)ws;
-    a.dqp = (float *)((char *)ws + bwd_ws(p).dqp);
+    const BwdWs w = bwd_ws(p);
+    a.dqp = (float *)((char *)ws + w.dqp);
+    a.dsum = p.M <= kSumStates ? (float *)((char *)ws + w.dsum) : nullptr;
     return p.d == 32 ? bwd_t<32>(q, k, v, out, dout, a, s) : bwd_t<64>(q, k, v, out, dout, a, s);
 }
 

@@ -196,9 +196,13 @@ def cross_backward(q, k, v, out, lse, dout, lens, scale, dtype):
         es = scale * (d + 4) * U * (Q.abs() @ T(K.abs())) + 4 * U * (s.abs() + lse[b].double()[..., None].abs())
         p = torch.exp(s - lse[b].double()[..., None])
         ep = p * (es + EXP_REL[dtype]) + FLUSH
-        dp, D = G @ T(V), (G * oh[b]).sum(-1, keepdim=True)
-        eD = (d + 4) * U * (G * oh[b]).abs().sum(-1, keepdim=True)
-        edp = (d + 4) * U * (G.abs() @ T(V.abs()))
+        dp, edp = G @ T(V), (d + 4) * U * (G.abs() @ T(V.abs()))
+        if dtype == torch.bfloat16 and M <= 128:       # the call takes D from the states, else from out
+            D = (p * dp).sum(-1, keepdim=True)
+            eD = (ep * dp.abs() + p * edp + (n + 4) * U * (p * dp).abs()).sum(-1, keepdim=True)
+        else:
+            D = (G * oh[b]).sum(-1, keepdim=True)
+            eD = (d + 4) * U * (G * oh[b]).abs().sum(-1, keepdim=True)
         ds = p * (dp - D)
         eds = ep * (dp - D).abs() + p * (edp + eD + U * (dp.abs() + D.abs())) + (ph + 2 * U) * ds.abs() + FLUSH
         epr = ep + ph * p

@@ -74,7 +74,7 @@ CASES = [  # B, N, M, H, d, dtype, fused, lengths
     (3, 257, 300, 4, 32, BF, True, [300, 0, 1]), (2, 300, 77, 5, 64, BF, False, [76, 65]),
     (4, 200, 512, 2, 32, BF, True, [512, 385, 384, 128]), (2, 390, 513, 2, 32, BF, False, [513, 512]),
     (2, 500, 1100, 1, 64, BF, True, [1100, 700]), (1, 1000, 33, 4, 32, BF, True, [-5]), (2, 64, 40, 2, 64, BF, False, [99, 7]),
-    (1, 2000, 300, 1, 64, BF, True, None), (2, 31, 16, 2, 32, BF, True, [15, 16]), (1, 260, 257, 20, 32, BF, True, None),
+    (1, 2000, 300, 1, 64, BF, True, None), (2, 31, 16, 2, 32, BF, True, [15, 16]), (3, 700, 2, 3, 64, BF, True, [2, 0, 1]), (2, 1300, 17, 30, 32, BF, False, [0, 17]), (1, 260, 257, 20, 32, BF, True, None),
     (1, 8, 200, 2, 32, BF, True, None), (1, 9, 200, 2, 64, BF, True, None), (2, 5, 260, 3, 64, BF, False, [260, 0]),
     (1, 385, 150, 3, 32, BF, True, None), (1, 769, 65, 2, 64, BF, True, None), (2, 100, 2100, 2, 32, BF, True, [2100, 900]),
     (1, 300, 3000, 1, 64, BF, True, None), (3, 1300, 130, 2, 32, BF, True, [130, 128, 2]), (40, 130, 66, 1, 32, BF, True, None),
@@ -91,10 +91,10 @@ def test_cross_matches_reference(la, case):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
-@pytest.mark.parametrize("N", [2, 140])
-def test_nothing_behind_the_lengths_is_used(la, dtype, N):
-    q, k, v, dout = draw(3, N, 150, 2, 32, dtype, True, 1)
-    lens = [150, 100, 3]
+@pytest.mark.parametrize("N,M", [(2, 150), (140, 150), (140, 90)])
+def test_nothing_behind_the_lengths_is_used(la, dtype, N, M):
+    q, k, v, dout = draw(3, N, M, 2, 32, dtype, True, 1)
+    lens = [M, 2 * M // 3, 3]
     k, v = k.clone(), v.clone()
     plain = run_case(la, q, k, v, dout, lens, dtype)
     for b, n in enumerate(lens):
