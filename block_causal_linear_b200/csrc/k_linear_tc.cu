@@ -512,49 +512,66 @@ gemm_finish(const TcArgs a) {
     }
 }
 
-// The three bf16 parts of a fp32 matrix, planes of `rows` rows at a pitch of ldo
-// elements.  hi is the nearest bf16, or the next one towards zero where that
-// would be infinite.
+// Up to three operands made ready by one launch, job i on the blocks from first[i] on.
+struct PackJobs {
+    struct {
+        const void *x;
+        __nv_bfloat16 *o;
+        long long rows, cols, ldo;
+    } j[3];
+    unsigned first[4];
+};
+
+// PARTS: the three bf16 parts of fp32 rows, planes of `rows` rows at a pitch of
+// ldo elements.  hi is the nearest bf16, or the next one towards zero where
+// that would be infinite.  Else: rows of bf16 copied to the pitch.  A thread 8
+// columns of a row: whole 16 bytes of each part (reads of odd rows are element
+// by element).
+template <bool PARTS>
 __global__ void __launch_bounds__(256)
-split_parts(const float *__restrict__ x, __nv_bfloat16 *__restrict__ o, long long rows, long long cols, long long ldo) {
-    const long long plane = rows * ldo, groups = rows * (ldo / 8);
-    const int per = (int)(ldo / 8);
-    // a thread 8 columns of a row: whole 16 bytes of each part (reads of odd rows are element by element)
-    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < groups; i += (long long)gridDim.x * 256) {
+gemm_pack(const __grid_constant__ PackJobs p) {
+    pdl_wait();
+    pdl_trigger();
+    const int n = blockIdx.x >= p.first[2] ? 2 : (blockIdx.x >= p.first[1] ? 1 : 0);
+    const auto &q = p.j[n];
+    const long long plane = q.rows * q.ldo, groups = q.rows * (q.ldo / 8), step = (long long)(p.first[n + 1] - p.first[n]) * 256;
+    const int per = (int)(q.ldo / 8);
+    for (long long i = (long long)(blockIdx.x - p.first[n]) * 256 + threadIdx.x; i < groups; i += step) {
         const long long r = i / per;
         const int c = (int)(i - r * per) * 8;
-        const float *s = x + r * cols + c;
-        float f[8];
+        uint4 *d = reinterpret_cast<uint4 *>(q.o + r * q.ldo + c);
+        if constexpr (PARTS) {
+            const float *s = (const float *)q.x + r * q.cols + c;
+            float f[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = c + e < cols ? s[e] : 0.f;
-        uint32_t h[4], m[4], l[4];
+            for (int e = 0; e < 8; ++e) f[e] = c + e < q.cols ? s[e] : 0.f;
+            uint32_t h[4], m[4], l[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            float hi[2], mid[2], lo[2];
+            for (int e = 0; e < 4; ++e) {
+                float hi[2], mid[2], lo[2];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const float v = f[2 * e + u];
-                hi[u] = __bfloat162float(__float2bfloat16_rn(v));
-                if (fabsf(hi[u]) > 3.4e38f && fabsf(v) <= 3.4028235e38f) hi[u] = __uint_as_float(__float_as_uint(v) & 0xFFFF0000u);
-                const float a = v - hi[u];
-                mid[u] = __bfloat162float(__float2bfloat16_rn(a));
-                lo[u] = a - mid[u];
+                for (int u = 0; u < 2; ++u) {
+                    const float v = f[2 * e + u];
+                    hi[u] = __bfloat162float(__float2bfloat16_rn(v));
+                    if (fabsf(hi[u]) > 3.4e38f && fabsf(v) <= 3.4028235e38f) hi[u] = __uint_as_float(__float_as_uint(v) & 0xFFFF0000u);
+                    const float a = v - hi[u];
+                    mid[u] = __bfloat162float(__float2bfloat16_rn(a));
+                    lo[u] = a - mid[u];
+                }
+                h[e] = pack_bf2(hi[0], hi[1]), m[e] = pack_bf2(mid[0], mid[1]), l[e] = pack_bf2(lo[0], lo[1]);
             }
-            h[e] = pack_bf2(hi[0], hi[1]), m[e] = pack_bf2(mid[0], mid[1]), l[e] = pack_bf2(lo[0], lo[1]);
+            d[0] = make_uint4(h[0], h[1], h[2], h[3]);
+            d[plane / 8] = make_uint4(m[0], m[1], m[2], m[3]);
+            d[2 * (plane / 8)] = make_uint4(l[0], l[1], l[2], l[3]);
+        } else {
+            const uint16_t *s = (const uint16_t *)q.x + r * q.cols + c;
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                w[e] = (c + 2 * e < q.cols ? s[2 * e] : 0u) | (uint32_t)(c + 2 * e + 1 < q.cols ? s[2 * e + 1] : 0u) << 16;
+            *d = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        uint4 *d = reinterpret_cast<uint4 *>(o + r * ldo + c);
-        d[0] = make_uint4(h[0], h[1], h[2], h[3]);
-        d[plane / 8] = make_uint4(m[0], m[1], m[2], m[3]);
-        d[2 * (plane / 8)] = make_uint4(l[0], l[1], l[2], l[3]);
     }
-}
-
-// Rows of `cols` elements at any pitch, copied to rows of ldo (a multiple of 8) elements.
-__global__ void __launch_bounds__(256)
-repack(const __nv_bfloat16 *__restrict__ x, __nv_bfloat16 *__restrict__ o, long long rows, long long cols,
-       long long ldo) {
-    for (long long r = blockIdx.x; r < rows; r += gridDim.x)
-        for (long long c = threadIdx.x; c < cols; c += 256) o[r * ldo + c] = x[r * cols + c];
 }
 
 // ---------------------------------------------------------------- host
@@ -730,54 +747,34 @@ bool gemm_tc_fits(long long M, long long N, long long K) {
            (M + kBM - 1) / kBM * ((N + 63) / 64) < (1LL << 30);
 }
 
-namespace {
+size_t gemm_tc_ws(int is_bf16, const GemmPlan &g) { return tc_plan(g.M, g.N, g.K, !is_bf16).part; }
 
-// Workspace of a product: the pieces' sums, then copies of operands whose rows
-// are not whole 16 bytes, or of fp32 ones their parts.
-struct TcWs {
-    size_t a, b, total;
-};
-long long pitch8(long long ld) { return (ld + 7) / 8 * 8; }
-TcWs tc_ws(const GemmPlan &g, const TcPlan &p, bool parts) {
-    auto bytes = [&](long long rows, long long ld) -> size_t {
-        return parts || ld % 8 ? align256(size_t(rows) * pitch8(ld) * 2 * (parts ? 3 : 1)) : 0;
-    };
-    TcWs w;
-    w.a = p.part;
-    w.b = w.a + bytes(g.a_mn ? g.K : g.M, g.lda);
-    w.total = w.b + bytes(g.b_mn ? g.K : g.N, g.ldb);
-    return w;
+int launch_gemm_tc(int is_bf16, const GemmPlan &g, void *ws, cudaStream_t s) {
+    const TcPlan p = tc_plan(g.M, g.N, g.K, !is_bf16);
+    return is_bf16 ? run_tile<false>(g, p, ws, s) : run_tile<true>(g, p, ws, s);
 }
 
-// The operand as the kernel reads it: rows at a pitch of whole 16 bytes, in bf16.
-bool packed(const void *&x, long long &ld, long long rows, void *to, bool parts, cudaStream_t s) {
-    if (!parts && ld % 8 == 0) return true;
-    const long long ldo = pitch8(ld);
-    if (parts) {
-        const long long want = (rows * (ldo / 8) + 255) / 256;
-        split_parts<<<(unsigned)(want < 16 * kSmCount ? want : 16 * kSmCount), 256, 0, s>>>((const float *)x, (__nv_bfloat16 *)to,
-                                                                                           rows, ld, ldo);
-    } else {
-        repack<<<(unsigned)(rows < 16 * kSmCount ? rows : 16 * kSmCount), 256, 0, s>>>((const __nv_bfloat16 *)x,
-                                                                                      (__nv_bfloat16 *)to, rows, ld, ldo);
+size_t gemm_pack_bytes(int is_bf16, long long rows, long long ld) {
+    const long long ldo = (ld + 7) / 8 * 8;
+    return is_bf16 && ldo == ld ? 0 : align256(size_t(rows) * ldo * 2 * (is_bf16 ? 1 : 3));
+}
+
+int launch_gemm_pack(int is_bf16, GemmOperand *ops, int n, cudaStream_t s) {
+    PackJobs p{};
+    int jobs = 0;
+    for (int i = 0; i < n; ++i) {
+        if (!gemm_pack_bytes(is_bf16, ops[i].rows, ops[i].ld)) continue;
+        const long long ldo = (ops[i].ld + 7) / 8 * 8, want = (ops[i].rows * (ldo / 8) + 255) / 256;
+        p.j[jobs] = {ops[i].x, (__nv_bfloat16 *)ops[i].to, ops[i].rows, ops[i].ld, ldo};
+        p.first[jobs + 1] = p.first[jobs] + (unsigned)(want < 16 * kSmCount ? want : 16 * kSmCount);
+        ++jobs;
+        ops[i].x = ops[i].to;
+        ops[i].ld = ldo;
     }
-    x = to;
-    ld = ldo;
-    return cudaGetLastError() == cudaSuccess;
-}
-
-}  // namespace
-
-size_t gemm_tc_ws(int is_bf16, const GemmPlan &g) { return tc_ws(g, tc_plan(g.M, g.N, g.K, !is_bf16), !is_bf16).total; }
-
-int launch_gemm_tc(int is_bf16, const GemmPlan &g0, void *ws, cudaStream_t s) {
-    GemmPlan g = g0;
-    const bool parts = !is_bf16;
-    const TcPlan p = tc_plan(g.M, g.N, g.K, parts);
-    const TcWs w = tc_ws(g, p, parts);
-    if (!packed(g.a, g.lda, g.a_mn ? g.K : g.M, (char *)ws + w.a, parts, s)) return -1;
-    if (!packed(g.b, g.ldb, g.b_mn ? g.K : g.N, (char *)ws + w.b, parts, s)) return -1;
-    return parts ? run_tile<true>(g, p, ws, s) : run_tile<false>(g, p, ws, s);
+    if (!jobs) return 0;
+    const unsigned grid = p.first[jobs];
+    for (int i = jobs; i < 3; ++i) p.first[i + 1] = grid;
+    return launch_pdl(is_bf16 ? gemm_pack<false> : gemm_pack<true>, grid, 256, 0, s, p) ? 1 : -1;
 }
 
 int read_and_clear_linear_flag(unsigned *flag_out) {

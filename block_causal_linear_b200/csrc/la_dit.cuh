@@ -44,12 +44,19 @@ struct GemmPlan {
 // at most kFewRows rows, both operands k-contiguous
 constexpr int kFewRows = 8;
 int launch_gemm_rows(int is_bf16, const GemmPlan &g, cudaStream_t s);
-// products on the tensor cores (k_linear_tc.cu); lda, ldb are the operands' row
-// lengths, of any size (bf16 rows that are not whole 16 bytes are copied to the
-// workspace first, fp32 ones split into their parts there)
+// Products on the tensor cores (k_linear_tc.cu), on operands whose rows are whole
+// 16 bytes: launch_gemm_pack copies others (fp32 ones as their bf16 parts) into
+// `to`, pack_bytes of them, in one launch, and names the copies in x and ld.
 bool gemm_tc_fits(long long M, long long N, long long K);
 size_t gemm_tc_ws(int is_bf16, const GemmPlan &g);
 int launch_gemm_tc(int is_bf16, const GemmPlan &g, void *ws, cudaStream_t s);
+struct GemmOperand {
+    const void *x;               // [rows][ld]
+    long long rows, ld;
+    void *to;
+};
+size_t gemm_pack_bytes(int is_bf16, long long rows, long long ld);
+int launch_gemm_pack(int is_bf16, GemmOperand *ops, int n, cudaStream_t s);
 int read_and_clear_linear_flag(unsigned *flag_out);
 // dz = dy * act'(pre) (with an activation and dz not null) and the column sums
 // of dz (colsum not null), in a fixed order; ws holds act_col_ws bytes

@@ -72,36 +72,50 @@ la::GemmPlan dw_product(long long R, long long K, long long N) {
     g.ldb = K; g.b_mn = 1;
     return g;
 }
-size_t product_ws(la_dtype dt, const la::GemmPlan &g) {
-    const bool few = g.M <= la::kFewRows && !g.a_mn && !g.b_mn;
-    return few ? 0 : la::gemm_tc_ws(dt == LA_BF16, g);
-}
-// A product on the kernel for its type and shape.
-int product(la_dtype dt, const la::GemmPlan &g, void *ws, cudaStream_t s) {
-    if (g.M <= la::kFewRows && !g.a_mn && !g.b_mn) return la::launch_gemm_rows(dt == LA_BF16, g, s);
-    return la::launch_gemm_tc(dt == LA_BF16, g, ws, s);
-}
+bool few_rows(const la::GemmPlan &g) { return g.M <= la::kFewRows && !g.a_mn && !g.b_mn; }
 
 bool linear_sizes_ok(int R, int K, int N, la_dtype dt) {
     return dtype_ok(dt) && count_ok(R, K, 1) && count_ok(N, K, 1) && count_ok(R, N, 1) &&
            la::gemm_tc_fits(R, N, K) && la::gemm_tc_fits(R, K, N) && la::gemm_tc_fits(N, K, R);
 }
 
-// Backward of linear: the workspace holds dz (with an activation), then what
-// one step at a time needs: the column sums' pieces or a product's workspace.
+// Workspace of linear's forward pass: x and weight as the tensor cores read
+// them (where they do not as they are), the product's sums.
+struct LinFwdWs {
+    size_t w, sums, total;
+};
+LinFwdWs lin_fwd_ws(int R, int K, int N, la_dtype dt) {
+    LinFwdWs l{};
+    const la::GemmPlan g = fwd_product(R, K, N);
+    if (!few_rows(g)) {
+        const int bf = dt == LA_BF16;
+        l.w = la::gemm_pack_bytes(bf, R, K);
+        l.sums = l.w + la::gemm_pack_bytes(bf, N, K);
+        l.total = l.sums + la::gemm_tc_ws(bf, g);
+    }
+    if (!l.total) l.total = 256;
+    return l;
+}
+
+// Of its backward pass: dz (with an activation); dz, weight and x as the tensor
+// cores read them; the sums of one step at a time (dbias, dx, dweight).
 struct LinBwdWs {
-    size_t step, total;
+    size_t z, w, x, sums, total;
 };
 LinBwdWs lin_bwd_ws(int R, int K, int N, la_dtype dt, la_act act) {
-    LinBwdWs w;
-    w.step = act == LA_ACT_NONE ? 0 : la::align256(size_t(R) * N * (dt == LA_BF16 ? 2 : 4));
+    LinBwdWs l;
+    const int bf = dt == LA_BF16;
+    l.z = act == LA_ACT_NONE ? 0 : la::align256(size_t(R) * N * (bf ? 2 : 4));
+    l.w = l.z + la::gemm_pack_bytes(bf, R, N);
+    l.x = l.w + la::gemm_pack_bytes(bf, N, K);
+    l.sums = l.x + la::gemm_pack_bytes(bf, R, K);
     size_t most = la::act_col_ws(R, N);
     for (const la::GemmPlan &g : {dx_product(R, K, N), dw_product(R, K, N)}) {
-        const size_t n = product_ws(dt, g);
+        const size_t n = la::gemm_tc_ws(bf, g);
         if (n > most) most = n;
     }
-    w.total = w.step + most;
-    return w;
+    l.total = l.sums + most;
+    return l;
 }
 
 bool act_ok(la_act a) { return a == LA_ACT_NONE || a == LA_ACT_RELU || a == LA_ACT_SILU || a == LA_ACT_GELU; }
@@ -144,9 +158,7 @@ la_status la_layer_norm_backward(const void *dy, const void *x, const void *weig
 }
 
 size_t la_linear_workspace_size(int R, int K, int N, la_dtype dt) {
-    if (!linear_sizes_ok(R, K, N, dt)) return 0;
-    const size_t n = product_ws(dt, fwd_product(R, K, N));
-    return n ? n : 256;
+    return linear_sizes_ok(R, K, N, dt) ? lin_fwd_ws(R, K, N, dt).total : 0;
 }
 
 la_status la_linear_forward(const void *x, const void *weight, const void *bias, const void *residual, void *y,
@@ -155,14 +167,22 @@ la_status la_linear_forward(const void *x, const void *weight, const void *bias,
     if (!x || !weight || !y) return LA_EINVAL;
     if (!al16(x) || !al16(weight) || !al16(bias) || !al16(residual) || !al16(y) || !al16(pre)) return LA_EINVAL;
     if (!dtype_ok(dt) || !act_ok(act)) return LA_EINVAL;
-    const size_t need = la_linear_workspace_size(R, K, N, dt);
-    if (!need) return LA_EINVAL;
-    if (!ws_ok(ws, ws_bytes, need)) return LA_EWORKSPACE;
+    if (!linear_sizes_ok(R, K, N, dt)) return LA_EINVAL;
+    const LinFwdWs l = lin_fwd_ws(R, K, N, dt);
+    if (!ws_ok(ws, ws_bytes, l.total)) return LA_EWORKSPACE;
+    const int bf = dt == LA_BF16;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    char *at = static_cast<char *>(ws);
     la::GemmPlan g = fwd_product(R, K, N);
     g.a = x; g.b = weight;
     g.bias = bias; g.res = residual; g.pre = pre; g.y = y;
     g.act = act;
-    return done(product(dt, g, ws, static_cast<cudaStream_t>(stream)));
+    if (few_rows(g)) return done(la::launch_gemm_rows(bf, g, s));
+    la::GemmOperand o[2] = {{x, R, K, at}, {weight, N, K, at + l.w}};
+    if (la::launch_gemm_pack(bf, o, 2, s) < 0) return LA_ECUDA;
+    g.a = o[0].x; g.lda = o[0].ld;
+    g.b = o[1].x; g.ldb = o[1].ld;
+    return done(la::launch_gemm_tc(bf, g, at + l.sums, s));
 }
 
 size_t la_linear_backward_workspace_size(int R, int K, int N, la_dtype dt, la_act act) {
@@ -180,22 +200,28 @@ la_status la_linear_backward(const void *dy, const void *x, const void *weight, 
     const size_t need = la_linear_backward_workspace_size(R, K, N, dt, act);
     if (!need) return LA_EINVAL;
     if (!ws_ok(ws, ws_bytes, need)) return LA_EWORKSPACE;
-    const LinBwdWs w = lin_bwd_ws(R, K, N, dt, act);
+    const LinBwdWs l = lin_bwd_ws(R, K, N, dt, act);
+    const int bf = dt == LA_BF16;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    void *step = static_cast<char *>(ws) + w.step;
+    char *at = static_cast<char *>(ws);
     const void *dz = act == LA_ACT_NONE ? dy : ws;
     if ((act != LA_ACT_NONE || dbias) &&
-        la::launch_act_col(dt == LA_BF16, dy, pre, act == LA_ACT_NONE ? nullptr : ws, dbias, R, N, act, step, s) < 0)
+        la::launch_act_col(bf, dy, pre, act == LA_ACT_NONE ? nullptr : ws, dbias, R, N, act, at + l.sums, s) < 0)
         return LA_ECUDA;
-    if (dx) {
-        la::GemmPlan g = dx_product(R, K, N);
-        g.a = dz; g.b = weight; g.y = dx;
-        if (product(dt, g, step, s) < 0) return LA_ECUDA;
-    }
-    if (dweight) {
-        la::GemmPlan g = dw_product(R, K, N);
-        g.a = dz; g.b = x; g.y = dweight;
-        if (product(dt, g, step, s) < 0) return LA_ECUDA;
+    if (!dx && !dweight) return LA_OK;
+    la::GemmOperand o[3] = {{dz, R, N, at + l.z}};
+    int n = 1;
+    if (dx) o[n++] = {weight, N, K, at + l.w};
+    if (dweight) o[n++] = {x, R, K, at + l.x};
+    if (la::launch_gemm_pack(bf, o, n, s) < 0) return LA_ECUDA;
+    for (const bool first : {true, false}) {
+        if (!(first ? dx : dweight)) continue;
+        const la::GemmOperand &b = first ? o[1] : o[n - 1];
+        la::GemmPlan g = first ? dx_product(R, K, N) : dw_product(R, K, N);
+        g.a = o[0].x; g.lda = o[0].ld;
+        g.b = b.x; g.ldb = b.ld;
+        g.y = first ? dx : dweight;
+        if (la::launch_gemm_tc(bf, g, at + l.sums, s) < 0) return LA_ECUDA;
     }
     return LA_OK;
 }
