@@ -47,7 +47,10 @@ finish_kernel(const float *__restrict__ partials, float *__restrict__ seff,
     const long long part_bh = STRIDED ? part_bh_rt : (long long)(p.sk_layout ? p.skP : p.P) * kKVZ;
     const long long part_sp = STRIDED ? part_sp_rt : (long long)kKVZ;
     // let the apply be scheduled now (it prefetches its q tiles), then wait
-    // for the reduce before reading its partials
+    // for the reduce before reading its partials.  With the ranks' sums this is
+    // the first kernel of its call: q may come from the kernel before it, so
+    // the apply is let in only behind that one
+    if (STRIDED) asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const long long w = (long long)blockIdx.x * kFinThreads + threadIdx.x;

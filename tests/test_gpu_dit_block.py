@@ -205,3 +205,65 @@ def test_two_graphs_of_the_block(la):
     for (_, outs), w in zip(graphs, want):
         assert all(torch.equal(a, b) for a, b in zip(outs, w))
     la.device_status()
+
+
+CONSUMERS = {
+    "block_apply": lambda la, t, o: la.block_apply(t(600, 64, 32), o["sums"], o["state"], commit=False),
+    "full_forward": lambda la, t, o: la.full_forward(t(600, 64, 32), o["k"], t(600, 64, 32), tokens_per_block=200),
+    "full_backward": lambda la, t, o: la.full_backward(o["k"], t(600, 64, 32), o["k"], t(600, 64, 32)),
+    "dwconv": lambda la, t, o: la.dwconv3d(t(10, 6, 10, 2048), o["filter"]),
+    "norm": lambda la, t, o: la.layer_norm_forward(t(600, 2048), return_stats=True),
+    "norm of few rows": lambda la, t, o: la.layer_norm_forward(t(2, 2048)),
+    "norm of many rows": lambda la, t, o: la.layer_norm_forward(t(8000, 2048)),
+    "norm of odd rows": lambda la, t, o: la.layer_norm_forward(t(2048, 1000).view(-1)[:2048 * 999].view(2048, 999)),
+    "norm backward": lambda la, t, o: la.layer_norm_backward(t(600, 2048), o["k"].view(600, 2048), o["w"][0], *o["stats"]),
+    "linear": lambda la, t, o: la.linear_forward(t(600, 2048), o["w"]),
+    "linear of few rows": lambda la, t, o: la.linear_forward(t(2, 2048), o["w"]),
+    "linear of odd rows": lambda la, t, o: la.linear_forward(t(600, 1000).view(-1)[:600 * 999].view(600, 999), o["odd"]),
+    "linear backward": lambda la, t, o: la.linear_backward(t(600, 2048), o["k"].view(600, 2048), o["sq"], o["pre"], "silu"),
+    "cross": lambda la, t, o: la.cross_attention_forward(t(600, 64, 32), o["k"], o["k"], return_lse=True),
+    "cross of few queries": lambda la, t, o: la.cross_attention_forward(t(2, 64, 32), o["k"], o["k"]),
+    "cross backward": lambda la, t, o: la.cross_attention_backward(o["k"], o["k"], o["k"], o["k"], o["lse"], t(600, 64, 32)),
+    "cross backward, few states": lambda la, t, o: la.cross_attention_backward(
+        o["k"], o["k"][:, :100], o["k"][:, :100], o["k"], o["lse"], t(600, 64, 32)),
+}
+
+
+@pytest.mark.parametrize("dtype", [BF, torch.float32])
+@pytest.mark.parametrize("name", CONSUMERS)
+def test_each_call_waits_for_the_one_before(la, name, dtype):
+    """What a long call writes last is read by the next call of the stream: the kernels of one call may be let
+    in while the kernel before them still runs, its results must not be."""
+    g = torch.Generator().manual_seed(3)
+    t = lambda *s: torch.randn(s, generator=g).to(dtype).cuda()  # noqa: E731
+    x, w = t(20000, 2048), t(2048, 448) / 20
+    narrow = x.view(-1)[:20000 * 448].view(20000, 448)      # too few products to cut the last tiles, which end late
+    o = {"k": t(1, 600, 64, 32), "w": t(256, 2048), "odd": t(256, 999), "sq": t(2048, 2048), "filter": t(2048, 1, 3, 3).float(),
+         "pre": torch.zeros(600, 2048, dtype=torch.float16 if dtype is BF else dtype, device="cuda"),
+         "sums": la.block_reduce(t(1, 600, 64, 32), t(1, 600, 64, 32))[None].contiguous()}
+    o["state"] = la.State(1, 64)
+    o["stats"] = la.layer_norm_forward(o["k"].view(600, 2048), return_stats=True)[1:]
+    o["lse"] = la.cross_attention_forward(o["k"], o["k"], o["k"], return_lse=True)[1]
+    buf, other = torch.empty_like(x), torch.empty_like(x)
+
+    def tail(*shape):
+        n = torch.Size(shape).numel()
+        flat = buf.view(-1)[buf.numel() - n:]
+        return flat.view(shape if len(shape) == 2 else (1, *shape))
+
+    def run():
+        r = CONSUMERS[name](la, tail, o)
+        return [r] if torch.is_tensor(r) else list(r)
+
+    for _ in range(5):
+        buf.zero_()
+        torch.cuda.synchronize()
+        for out in [other] * 12 + [buf]:                    # (the first ones while the host queues the rest)
+            if dtype is BF:
+                la.linear_forward(narrow, w, out=out)
+            else:
+                la.layer_norm_forward(x, out=out)
+        got = run()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, run()))
+        la.device_status()
