@@ -11,9 +11,12 @@
 // hundred queries fills the GPU.  The other side's rows pass through shared
 // memory, 4 at a time for independent sums.  Bound by the fp32 units: 8 flops a
 // score and feature forward, 20 backward.
-#include "la_dit.cuh"
+#include "la_sm100_dit.cuh"
 
 namespace la {
+
+using namespace sm100;
+
 namespace {
 
 constexpr int kLanes = 4;                  // lanes a row
@@ -77,6 +80,8 @@ template <int D>
 __global__ void __launch_bounds__(kThreads)
 cross_fwd_f32(const float *__restrict__ q, const float *__restrict__ k, const float *__restrict__ v, float *__restrict__ out,
               float *__restrict__ lse, const CrossPlan p) {
+    pdl_wait_for(q, k, v);
+    pdl_trigger();
     __shared__ __align__(16) float ks[kTile][D], vs[kTile][D];
     const int b = blockIdx.y / p.H, h = blockIdx.y % p.H, part = threadIdx.x % kLanes;
     const long long i = (long long)blockIdx.x * kRows + threadIdx.x / kLanes;
@@ -127,6 +132,8 @@ __global__ void __launch_bounds__(kThreads)
 cross_dq_f32(const float *__restrict__ q, const float *__restrict__ k, const float *__restrict__ v,
              const float *__restrict__ out, const float *__restrict__ dout, const float *__restrict__ lse,
              float *__restrict__ dq, float *__restrict__ delta, const CrossPlan p) {
+    pdl_wait_for(q, k, v, out, dout, lse);
+    pdl_trigger();
     __shared__ __align__(16) float ks[kTile][D], vs[kTile][D];
     const int b = blockIdx.y / p.H, h = blockIdx.y % p.H, part = threadIdx.x % kLanes;
     const long long i = (long long)blockIdx.x * kRows + threadIdx.x / kLanes;
@@ -173,6 +180,8 @@ __global__ void __launch_bounds__(kThreads)
 cross_dkv_f32(const float *__restrict__ q, const float *__restrict__ k, const float *__restrict__ v,
               const float *__restrict__ dout, const float *__restrict__ lse, const float *__restrict__ delta,
               float *__restrict__ sums, const CrossPlan p) {
+    pdl_wait_for(q, k, v, dout, lse, delta);
+    pdl_trigger();
     __shared__ __align__(16) float qs[kTile][D], gs[kTile][D];
     __shared__ float ls[kTile], dl[kTile];
     const int b = blockIdx.y / p.H, h = blockIdx.y % p.H, sp = blockIdx.z, splits = gridDim.z, part = threadIdx.x % kLanes;
@@ -219,6 +228,8 @@ cross_dkv_f32(const float *__restrict__ q, const float *__restrict__ k, const fl
 template <int D>
 __global__ void __launch_bounds__(256)
 cross_dkv_sum(const float *__restrict__ sums, float *__restrict__ dk, float *__restrict__ dv, const CrossPlan p, int splits) {
+    pdl_wait_for(sums);
+    pdl_trigger();
     const long long per = (long long)p.B * p.H * p.M * 2 * D;
     for (long long e = ((long long)blockIdx.x * 256 + threadIdx.x) * 4; e < per; e += (long long)gridDim.x * 1024) {
         const int f = (int)(e % (2 * D));
@@ -251,8 +262,8 @@ size_t dkv_bytes(const CrossPlan &p, int splits) {
 template <int D>
 int fwd_t(const void *q, const void *k, const void *v, void *out, float *lse, const CrossPlan &p, cudaStream_t s) {
     const dim3 grid((unsigned)((p.N + kRows - 1) / kRows), (unsigned)(p.B * p.H));
-    cross_fwd_f32<D><<<grid, kThreads, 0, s>>>((const float *)q, (const float *)k, (const float *)v, (float *)out, lse, p);
-    return cudaGetLastError() == cudaSuccess ? 1 : -1;
+    return launch_dep(cross_fwd_f32<D>, grid, kThreads, 0, s, (const float *)q, (const float *)k, (const float *)v, (float *)out, lse, p)
+               ? 1 : -1;
 }
 
 template <int D>
@@ -261,16 +272,16 @@ int bwd_t(const void *q, const void *k, const void *v, const void *out, const vo
     const int sp = dkv_splits(p);
     float *sums = (float *)ws, *delta = (float *)((char *)ws + dkv_bytes(p, sp));
     const dim3 gq((unsigned)((p.N + kRows - 1) / kRows), (unsigned)(p.B * p.H));
-    cross_dq_f32<D><<<gq, kThreads, 0, s>>>((const float *)q, (const float *)k, (const float *)v, (const float *)out,
-                                            (const float *)dout, lse, (float *)dq, delta, p);
-    if (cudaGetLastError() != cudaSuccess) return -1;
+    if (!launch_dep(cross_dq_f32<D>, gq, kThreads, 0, s, (const float *)q, (const float *)k, (const float *)v, (const float *)out,
+                    (const float *)dout, lse, (float *)dq, delta, p))
+        return -1;
     const dim3 gk((unsigned)((p.M + kRows - 1) / kRows), (unsigned)(p.B * p.H), (unsigned)sp);
-    cross_dkv_f32<D><<<gk, kThreads, 0, s>>>((const float *)q, (const float *)k, (const float *)v, (const float *)dout,
-                                             lse, delta, sums, p);
-    if (cudaGetLastError() != cudaSuccess) return -1;
+    if (!launch_dep(cross_dkv_f32<D>, gk, kThreads, 0, s, (const float *)q, (const float *)k, (const float *)v, (const float *)dout, lse,
+                    delta, sums, p))
+        return -1;
     const long long n = (long long)p.B * p.H * p.M * 2 * D / 4, want = (n + 255) / 256;
-    cross_dkv_sum<D><<<(unsigned)(want < 16 * kSmCount ? want : 16 * kSmCount), 256, 0, s>>>(sums, (float *)dk, (float *)dv, p, sp);
-    return cudaGetLastError() == cudaSuccess ? 3 : -1;
+    return launch_dep(cross_dkv_sum<D>, dim3((unsigned)(want < 16 * kSmCount ? want : 16 * kSmCount)), 256, 0, s, sums, (float *)dk,
+                      (float *)dv, p, sp) ? 3 : -1;
 }
 
 }  // namespace

@@ -421,7 +421,7 @@ cross_few(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restrict__
     __shared__ float cm[NQ], cl[NQ], co[NQ][D];        // this piece's
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane / LG, part = lane % LG;
     const int sp = blockIdx.x, b = blockIdx.y / a.p.H, h = blockIdx.y % a.p.H, n0 = blockIdx.z * NQ;
-    pdl_wait();
+    pdl_wait_for(q, k, v);
     pdl_trigger();
     const int len = cross_len(a.p, b);
     const int j0 = (int)((long long)len * sp / a.splits), j1 = (int)((long long)len * (sp + 1) / a.splits);

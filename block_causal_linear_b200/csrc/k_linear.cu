@@ -2,9 +2,12 @@
 // products with few rows, the activation's derivative and column sums.
 //
 //   C[m][n] = sum_k A(m, k) B(n, k);  z = C + bias;  pre = z;  y = act(z) + residual
-#include "la_dit.cuh"
+#include "la_sm100_dit.cuh"
 
 namespace la {
+
+using namespace sm100;
+
 namespace {
 
 constexpr int kThreads = 256;
@@ -31,6 +34,8 @@ struct alignas(sizeof(T) * VEC) Pack {
 template <typename T, int VEC, int R, int NC>
 __global__ void __launch_bounds__(kThreads)
 gemm_rows(const GemmPlan g) {
+    pdl_wait();
+    pdl_trigger();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const long long n0 = ((long long)blockIdx.x * (kThreads / 32) + warp) * NC;
     const T *A = (const T *)g.a, *B = (const T *)g.b;
@@ -66,11 +71,9 @@ gemm_rows(const GemmPlan g) {
 template <typename T, int VEC, int R>
 int rows_nc(const GemmPlan &g, cudaStream_t s) {
     // 4 columns a warp where that still leaves 4 warps a scheduler of the GPU, else 1
-    if (g.N >= 4 * 16 * kSmCount)
-        gemm_rows<T, VEC, R, 4><<<(unsigned)((g.N + 31) / 32), kThreads, 0, s>>>(g);
-    else
-        gemm_rows<T, VEC, R, 1><<<(unsigned)((g.N + 7) / 8), kThreads, 0, s>>>(g);
-    return cudaGetLastError() == cudaSuccess ? 1 : -1;
+    const bool ok = g.N >= 4 * 16 * kSmCount ? launch_dep(gemm_rows<T, VEC, R, 4>, dim3((unsigned)((g.N + 31) / 32)), kThreads, 0, s, g)
+                                             : launch_dep(gemm_rows<T, VEC, R, 1>, dim3((unsigned)((g.N + 7) / 8)), kThreads, 0, s, g);
+    return ok ? 1 : -1;
 }
 
 template <typename T, int VEC>
@@ -89,6 +92,8 @@ template <typename T, int VEC>
 __global__ void __launch_bounds__(kThreads)
 act_col(const T *__restrict__ dy, const typename PreOf<T>::type *__restrict__ pre, T *__restrict__ dz,
         float *__restrict__ part, long long R, long long C, int act) {
+    pdl_wait_for(dy, pre);
+    pdl_trigger();
     using P = typename PreOf<T>::type;
     __shared__ float red[8][32 * VEC];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -139,9 +144,8 @@ int col_splits(long long R, long long C) {
 template <typename T, int VEC>
 int act_col_t(const void *dy, const void *pre, void *dz, float *part, long long R, long long C, int act, cudaStream_t s) {
     const dim3 grid((unsigned)((C + 32 * VEC - 1) / (32 * VEC)), (unsigned)col_splits(R, C));
-    act_col<T, VEC><<<grid, kThreads, 0, s>>>((const T *)dy, (const typename PreOf<T>::type *)pre, (T *)dz, part, R,
-                                             C, act);
-    return cudaGetLastError() == cudaSuccess ? 1 : -1;
+    return launch_dep(act_col<T, VEC>, grid, kThreads, 0, s, (const T *)dy, (const typename PreOf<T>::type *)pre, (T *)dz, part, R, C,
+                      act) ? 1 : -1;
 }
 
 }  // namespace

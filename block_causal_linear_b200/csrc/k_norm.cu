@@ -119,6 +119,8 @@ norm_fwd_ring(const T *__restrict__ x, const T *__restrict__ w, const T *__restr
         fence_barrier_init();
     }
     __syncthreads();
+    pdl_wait_for(x, w, b);
+    pdl_trigger();
     RowRing<T, 1> rr;
     rr.rowb = (uint32_t)p.C * sizeof(T);
     rr.slots = ring + (size_t)warp * slots * rr.rowb;
@@ -232,6 +234,8 @@ norm_bwd_team(const T *__restrict__ dy, const T *__restrict__ x, const T *__rest
         fence_barrier_init();
     }
     __syncthreads();
+    pdl_wait_for(dy, x, w, mean, rstd);
+    pdl_trigger();
     RowRing<T, 2> rr;
     rr.rowb = (uint32_t)p.C * sizeof(T);
     rr.slots = ring + (size_t)team * slots * 2 * rr.rowb;
@@ -353,6 +357,8 @@ template <typename T, int VEC, int EPT, int WPR>
 __global__ void __launch_bounds__(kThreads)
 norm_fwd(const T *__restrict__ x, const T *__restrict__ w, const T *__restrict__ b, T *__restrict__ y,
          float *__restrict__ mean_out, float *__restrict__ rstd_out, const NormPlan p) {
+    pdl_wait_for(x, w, b);
+    pdl_trigger();
     constexpr int TPR = 32 * WPR, RPC = kThreads / TPR, NV = EPT / VEC;
     __shared__ float red[2][kThreads / 32];
     const int t = threadIdx.x % TPR, warp = threadIdx.x >> 5;
@@ -471,6 +477,8 @@ __global__ void __launch_bounds__(MAXT, kEpt == 4 ? 2 : 1)
 norm_bwd(const T *__restrict__ dy, const T *__restrict__ x, const T *__restrict__ w, const float *__restrict__ mean,
          const float *__restrict__ rstd, T *__restrict__ dx, float *__restrict__ part, const NormPlan p, int tpr,
          int splits) {
+    pdl_wait_for(dy, x, w, mean, rstd);
+    pdl_trigger();
     constexpr int VEC = 1, NV = kEpt;
     extern __shared__ float sh[];          // [2][2][warps], then (at the end) [threads][2 kEpt]
     const int warps = blockDim.x >> 5, wpr = tpr >> 5, ty = blockDim.x / tpr;
@@ -627,6 +635,8 @@ template <typename T>
 __global__ void __launch_bounds__(32 * kSumWarps)
 split_sum(const float *__restrict__ part, T *__restrict__ out0, T *__restrict__ out1, long long width, long long cut,
           int splits) {
+    pdl_wait_for(part);
+    pdl_trigger();
     __shared__ float red[kSumWarps][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const long long e = (long long)blockIdx.x * 32 + lane, g = blockIdx.y;
@@ -700,8 +710,7 @@ int fwd_launch(const T *x, const T *w, const T *b, T *y, float *mean, float *rst
     constexpr int RPC = kThreads / (32 * WPR);
     const long long grid = (p.rows + RPC - 1) / RPC;
     if (grid > 0x7fffffffLL) return -1;
-    norm_fwd<T, VEC, EPT, WPR><<<(unsigned)grid, kThreads, 0, s>>>(x, w, b, y, mean, rstd, p);
-    return cudaGetLastError() == cudaSuccess ? 1 : -1;
+    return launch_dep(norm_fwd<T, VEC, EPT, WPR>, dim3((unsigned)grid), kThreads, 0, s, x, w, b, y, mean, rstd, p) ? 1 : -1;
 }
 
 template <typename T, int VEC>
@@ -737,8 +746,7 @@ int norm_fwd_t(const T *x, const T *w, const T *b, T *y, float *mean, float *rst
         if (slots > kRing) slots = kRing;
         if (!once_per_device(&g_norm_ready<T>, norm_setup<T>)) return -1;
         auto f = p.C <= 1024 ? norm_fwd_ring<T, 32> : norm_fwd_ring<T, 64>;
-        f<<<kSmCount, kFwdThreads, kWarps * slots * row, s>>>(x, w, b, y, mean, rstd, p, slots);
-        return cudaGetLastError() == cudaSuccess ? 1 : -1;
+        return launch_dep(f, dim3(kSmCount), kFwdThreads, kWarps * slots * row, s, x, w, b, y, mean, rstd, p, slots) ? 1 : -1;
     }
     // few rows: all warps of a CTA on each, for the latency of one (2 rows of 2048: 9.3 us with a warp a row)
     if (p.C % V == 0 && p.C > 256 && p.C <= 2048 && p.rows <= 2 * kSmCount) return fwd_launch<T, V, 8, 8>(x, w, b, y, mean, rstd, p, s);
@@ -765,12 +773,13 @@ int norm_bwd_t(const T *dy, const T *x, const T *w, const float *mean, const flo
                  : b.wpr == 4 ? norm_bwd_team<T, 4>
                  : b.wpr == 8 ? norm_bwd_team<T, 8>
                               : norm_bwd_team<T, 16>;
-        f<<<grid, kBwdThreads, rings > sums ? rings : sums, s>>>(dy, x, w, mean, rstd, dx, part, p, b.splits, b.slots);
+        if (!launch_dep(f, dim3(grid), kBwdThreads, rings > sums ? rings : sums, s, dy, x, w, mean, rstd, dx, part, p, b.splits, b.slots))
+            return -1;
     } else if (p.C <= kWideBwd) {
         // the CTA's pieces at the end, or two rounds of two sums a warp
         const int smem = b.threads > b.tpr ? b.threads * 2 * b.ept * 4 : b.threads / 32 * 16;
         auto f = b.ept == 16 ? norm_bwd<T, 16, 512> : (b.ept == 8 ? norm_bwd<T, 8, 512> : norm_bwd<T, 4, 512>);
-        f<<<grid, b.threads, smem, s>>>(dy, x, w, mean, rstd, dx, part, p, b.tpr, b.splits);
+        if (!launch_dep(f, dim3(grid), b.threads, smem, s, dy, x, w, mean, rstd, dx, part, p, b.tpr, b.splits)) return -1;
     } else {
         const long long grid = p.rows < (1 << 30) ? p.rows : (1 << 30);
         norm_dx_wide<T><<<(unsigned)grid, kThreads, 0, s>>>(dy, x, w, mean, rstd, dx, p);
@@ -778,12 +787,11 @@ int norm_bwd_t(const T *dy, const T *x, const T *w, const float *mean, const flo
         if (part)
             norm_dw_wide<T><<<dim3((unsigned)((p.C + kThreads - 1) / kThreads), (unsigned)(groups * b.splits)), kThreads,
                               0, s>>>(dy, x, mean, rstd, part, p, b.splits);
+        if (cudaGetLastError() != cudaSuccess) return -1;
     }
-    if (cudaGetLastError() != cudaSuccess) return -1;
     if (!part) return 1;
-    split_sum<T><<<dim3((unsigned)((2 * (long long)p.C + 31) / 32), groups), 32 * kSumWarps, 0, s>>>(part, dw, db, 2 * (long long)p.C,
-                                                                                              p.C, b.splits);
-    return cudaGetLastError() == cudaSuccess ? 2 : -1;
+    return launch_dep(split_sum<T>, dim3((unsigned)((2 * (long long)p.C + 31) / 32), groups), 32 * kSumWarps, 0, s, part, dw, db,
+                      2 * (long long)p.C, (long long)p.C, b.splits) ? 2 : -1;
 }
 
 }  // namespace
@@ -811,10 +819,10 @@ int launch_norm_bwd(int is_bf16, const void *dy, const void *x, const void *w, c
 
 int launch_split_sum(int is_bf16, const float *part, void *out, long long width, int splits, cudaStream_t s) {
     using bf = __nv_bfloat16;
-    const unsigned grid = (unsigned)((width + 31) / 32);
-    if (is_bf16) split_sum<bf><<<grid, 32 * kSumWarps, 0, s>>>(part, (bf *)out, nullptr, width, width, splits);
-    else split_sum<float><<<grid, 32 * kSumWarps, 0, s>>>(part, (float *)out, nullptr, width, width, splits);
-    return cudaGetLastError() == cudaSuccess ? 1 : -1;
+    const dim3 grid((unsigned)((width + 31) / 32));
+    const bool ok = is_bf16 ? launch_dep(split_sum<bf>, grid, 32 * kSumWarps, 0, s, part, (bf *)out, (bf *)nullptr, width, width, splits)
+                            : launch_dep(split_sum<float>, grid, 32 * kSumWarps, 0, s, part, (float *)out, (float *)nullptr, width, width, splits);
+    return ok ? 1 : -1;
 }
 
 int read_and_clear_norm_flag(unsigned *flag_out) {

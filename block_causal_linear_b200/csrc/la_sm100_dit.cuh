@@ -3,6 +3,8 @@
 // of any matrix, per-device kernel set-up.
 #pragma once
 
+#include <utility>
+
 #include "la_dit.cuh"
 #include "la_sm100.cuh"
 
@@ -28,6 +30,14 @@ __device__ __forceinline__ bool mbar_poll(uint64_t *bar, uint32_t parity, volati
     *abort_word = 1;
     atomicCAS(dev_flag, 0u, 0x100u | (unsigned)where);
     return false;
+}
+
+// pdl_wait for kernels whose pointers are const __restrict__: what the compiler
+// takes for constant it may load early, so the pointers become known only here.
+template <typename... P>
+__device__ __forceinline__ void pdl_wait_for(P &...p) {
+    pdl_wait();
+    (..., [](auto &x) { asm volatile("" : "+l"(x)::"memory"); }(p));
 }
 
 // One lane of the (converged) warp.  Roles that issue copies or MMAs run on the
@@ -217,5 +227,21 @@ bool make_dit_map(CUtensorMap *m, const void *base, int rank, const cuuint64_t *
 // Runs `setup` (function attributes) once on each device that launches; the
 // current device's result.
 bool once_per_device(bool (*done)[128], bool (*setup)());
+
+// launch_pdl of a grid of more dimensions.
+template <typename... KArgs, typename... Args>
+bool launch_dep(void (*kernel)(KArgs...), dim3 grid, int threads, size_t smem, cudaStream_t s, Args &&...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...) == cudaSuccess;
+}
 
 }  // namespace la
