@@ -10,7 +10,8 @@
 // group of 4 features: rows of 64 then fit the registers, and a call of a few
 // hundred queries fills the GPU.  The other side's rows pass through shared
 // memory, 4 at a time for independent sums.  Bound by the fp32 units: 8 flops a
-// score and feature forward, 20 backward.
+// score and feature forward, 20 backward (2 x 391 queries, 77 states, 8 heads of
+// 64: 66 us forward and backward, four launches' latency for the most part).
 #include "la_sm100_dit.cuh"
 
 namespace la {

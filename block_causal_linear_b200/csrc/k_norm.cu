@@ -3,7 +3,9 @@
 //   xh = (x - mean) rstd, mean and variance over C, rstd = 1 / sqrt(var + eps);  y = w xh + b
 //   g = w dy;  dx = rstd (g - mean(g) - xh mean(g xh));  dw = sum dy xh, db = sum dy over the rows
 //
-// Bound by HBM: each element is read once (x; x and dy) and written once.  Many
+// Bound by HBM: each element is read once (x; x and dy) and written once (75600
+// rows of 2048 bf16: 117 us, 5.3 TB/s; 4 x 8190 rows forward and backward 138
+// us, 4.9 TB/s).  Many
 // rows of whole 16 bytes run a warp a row (forward, up to 2048 channels) or a
 // few (backward, up to 8192), the rows arriving by bulk copies in rings of
 // those warps' own, so that what is in flight does not depend on registers or
