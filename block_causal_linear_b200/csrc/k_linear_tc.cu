@@ -77,20 +77,36 @@ struct TcArgs {
 // Byte offset of 16-byte chunk j of row r in a 32-row buffer of 64-byte rows, 64-byte swizzle.
 __device__ __forceinline__ int sw64(int r, int j) { return r * 64 + ((j ^ ((r >> 1) & 3)) << 4); }
 
-// A warp's 32 x 32 block of a row-major matrix whose rows TMA cannot address, into or out of its buffer.
-__device__ __forceinline__ void block_in(uint8_t *buf, const __nv_bfloat16 *src, long long row0, long long col0,
-                                         const TcArgs &a, int lane) {
-    for (int r = 0; r < 32; ++r)
-        if (row0 + r < a.M && col0 + lane < a.N)
-            *reinterpret_cast<__nv_bfloat16 *>(buf + sw64(r, lane >> 3) + (lane & 7) * 2) =
-                src[(row0 + r) * a.N + col0 + lane];
+// A warp's 32 x 32 block of a row-major matrix whose rows TMA cannot address,
+// into or out of its buffer, eight rows in flight.
+__device__ __forceinline__ void block_in(uint8_t *buf, const uint16_t *src, long long row0, long long col0, const TcArgs &a,
+                                         int lane) {
+    const bool col = col0 + lane < a.N;
+    src += row0 * a.N + col0 + lane;
+    const int rows = a.M - row0 < 32 ? (int)(a.M - row0) : 32;
+#pragma unroll 1
+    for (int r0 = 0; r0 < rows; r0 += 8) {
+        uint16_t v[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) v[r] = col && r0 + r < rows ? src[(r0 + r) * a.N] : (uint16_t)0;
+#pragma unroll
+        for (int r = 0; r < 8; ++r) *reinterpret_cast<uint16_t *>(buf + sw64(r0 + r, lane >> 3) + (lane & 7) * 2) = v[r];
+    }
 }
-__device__ __forceinline__ void block_out(const uint8_t *buf, uint16_t *dst, long long row0, long long col0,
-                                          const TcArgs &a, int lane) {
-    for (int r = 0; r < 32; ++r)
-        if (row0 + r < a.M && col0 + lane < a.N)
-            dst[(row0 + r) * a.N + col0 + lane] =
-                *reinterpret_cast<const uint16_t *>(buf + sw64(r, lane >> 3) + (lane & 7) * 2);
+__device__ __forceinline__ void block_out(const uint8_t *buf, uint16_t *dst, long long row0, long long col0, const TcArgs &a,
+                                          int lane) {
+    const bool col = col0 + lane < a.N;
+    dst += row0 * a.N + col0 + lane;
+    const int rows = a.M - row0 < 32 ? (int)(a.M - row0) : 32;
+#pragma unroll 1
+    for (int r0 = 0; r0 < rows; r0 += 8) {
+        uint16_t v[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) v[r] = *reinterpret_cast<const uint16_t *>(buf + sw64(r0 + r, lane >> 3) + (lane & 7) * 2);
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+            if (col && r0 + r < rows) dst[(r0 + r) * a.N] = v[r];
+    }
 }
 
 // One piece of work: a whole tile, or one of the pieces along k of a tail tile.
@@ -387,9 +403,9 @@ gemm_tc(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtens
 #pragma unroll
                     for (int j = 0; j < 4; ++j) add8(x + 8 * j, bb[j]);
                 } else if (a.bias) {
+                    const float one = col + lane < a.N ? __bfloat162float(a.bias[col + lane]) : 0.f;
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (col + j < a.N) x[j] += __bfloat162float(a.bias[col + j]);
+                    for (int j = 0; j < 32; ++j) x[j] += __shfl_sync(0xffffffffu, one, j);
                 }
                 if (a.pre) put_pre(pb, x, a.act, lane);
                 act_chunk(x, a.act);
@@ -398,7 +414,7 @@ gemm_tc(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtens
                         ok = mbar_poll(&rb[par], (rphase >> par) & 1u, abort_word, &g_linear_flag, 5);
                         rphase ^= 1u << par;
                     } else {
-                        block_in(yb, a.res, row0, col, a, lane);
+                        block_in(yb, (const uint16_t *)a.res, row0, col, a, lane);
                     }
                     __syncwarp();
 #pragma unroll
