@@ -93,19 +93,32 @@ __device__ __forceinline__ void block_in(uint8_t *buf, const uint16_t *src, long
         for (int r = 0; r < 8; ++r) *reinterpret_cast<uint16_t *>(buf + sw64(r0 + r, lane >> 3) + (lane & 7) * 2) = v[r];
     }
 }
+// (Out: two rows at a time, in words between the rows' odd ends, which follow in two stores for all rows.)
 __device__ __forceinline__ void block_out(const uint8_t *buf, uint16_t *dst, long long row0, long long col0, const TcArgs &a,
                                           int lane) {
-    const bool col = col0 + lane < a.N;
-    dst += row0 * a.N + col0 + lane;
-    const int rows = a.M - row0 < 32 ? (int)(a.M - row0) : 32;
+    const int cols = a.N - col0 < 32 ? (int)(a.N - col0) : 32, rows = a.M - row0 < 32 ? (int)(a.M - row0) : 32;
+    const int l = lane & 15, h = lane >> 4, odd = (int)(a.N & 1), par0 = (int)((row0 * a.N + col0) & 1);
+    auto word = [&](int r, int w) { return *reinterpret_cast<const uint32_t *>(buf + sw64(r, w >> 2) + (w & 3) * 4); };
+    dst += row0 * a.N + col0;
 #pragma unroll 1
     for (int r0 = 0; r0 < rows; r0 += 8) {
-        uint16_t v[8];
+        uint32_t v[4];
 #pragma unroll
-        for (int r = 0; r < 8; ++r) v[r] = *reinterpret_cast<const uint16_t *>(buf + sw64(r0 + r, lane >> 3) + (lane & 7) * 2);
+        for (int i = 0; i < 4; ++i) {
+            const int r = r0 + 2 * i + h, par = (par0 + r * odd) & 1;
+            v[i] = __funnelshift_r(word(r, l), word(r, l < 15 ? l + 1 : 15), 16 * par);
+        }
 #pragma unroll
-        for (int r = 0; r < 8; ++r)
-            if (col && r0 + r < rows) dst[(r0 + r) * a.N] = v[r];
+        for (int i = 0; i < 4; ++i) {
+            const int r = r0 + 2 * i + h, c = 2 * l + ((par0 + r * odd) & 1);
+            if (r < rows && c + 1 < cols) *reinterpret_cast<uint32_t *>(dst + (long long)r * a.N + c) = v[i];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int r = 16 * i + (lane >> 1), par = (par0 + r * odd) & 1, c = lane & 1 ? cols - 1 : 0;
+        if (r < rows && (lane & 1 ? (cols - par) & 1 : par))
+            dst[(long long)r * a.N + c] = *reinterpret_cast<const uint16_t *>(buf + sw64(r, c >> 3) + (c & 7) * 2);
     }
 }
 
@@ -137,6 +150,17 @@ __device__ __forceinline__ void add8(float *v, uint4 x) {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[2 * i] += bf_lo(w[i]), v[2 * i + 1] += bf_hi(w[i]);
+}
+// Eight elements of the bias from column c on, zeros behind the last.
+__device__ __forceinline__ uint4 bias_end(const TcArgs &a, long long c) {
+    uint32_t w[4] = {};
+    const uint16_t *b = reinterpret_cast<const uint16_t *>(a.bias);
+    if (c < a.N) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (c + e < a.N) w[e / 2] |= (uint32_t)b[c + e] << (16 * (e & 1));
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 __device__ __forceinline__ void put_chunk(uint8_t *buf, const float (&v)[32], int lane) {
 #pragma unroll
@@ -367,11 +391,11 @@ gemm_tc(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtens
                 const int par = two ? (int)(cc++ & 1) : 0;
                 uint8_t *yb = bufs + par * kBuf, *pb = bufs + kBuf;
                 uint4 bb[4];
-                const bool vec_bias = a.bias && !a.direct && k_.piece < 0;
-                if (vec_bias) {
+                const bool add_bias = a.bias && k_.piece < 0;
+                if (add_bias) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        bb[j] = col + 8 * j < a.N ? __ldg(reinterpret_cast<const uint4 *>(a.bias + col) + j) : make_uint4(0, 0, 0, 0);
+                        bb[j] = col + 8 * j + 8 <= a.N ? __ldg(reinterpret_cast<const uint4 *>(a.bias + col) + j) : bias_end(a, col + 8 * j);
                 }
                 if (tma && lane == 0) {
                     if (!two) {
@@ -399,13 +423,9 @@ gemm_tc(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtens
                         reinterpret_cast<float4 *>(o)[j] = make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
                     continue;
                 }
-                if (vec_bias) {
+                if (add_bias) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) add8(x + 8 * j, bb[j]);
-                } else if (a.bias) {
-                    const float one = col + lane < a.N ? __bfloat162float(a.bias[col + lane]) : 0.f;
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) x[j] += __shfl_sync(0xffffffffu, one, j);
                 }
                 if (a.pre) put_pre(pb, x, a.act, lane);
                 act_chunk(x, a.act);
